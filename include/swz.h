@@ -473,6 +473,99 @@ int swz_tc_rate_ex(int dtype, int n, int cta_pair, int mmas_per_stage, const voi
                    const void* B, int n_mma, int num_ctas, uint64_t* d_times, float* d_D,
                    void* stream);
 
+/* ---- linear layers in 8 bits ----------------------------------------------
+ * No source page has a counterpart: products of 8-bit floating-point operands
+ * with one fp32 scale for each block of 128, what quantises those operands,
+ * and the orthogonalised update, so that the forward product, the gradients
+ * and the update of a linear layer run on this library's kernels.
+ */
+enum { SWZ_F32 = 3 }; /* element type of inputs and outputs below, besides
+                         SWZ_F16 and SWZ_BF16                                 */
+enum swz_f8 { SWZ_E4M3 = 0, SWZ_E5M2 = 1 };
+enum swz_block {
+  SWZ_BLOCK_ROW = 0,   /* 1 x 128: one scale for 128 values of a row.  Stored
+                          by block: the scale of row m, block kb at
+                          scales[kb * ld_scales + m] (ld_scales >= rows)      */
+  SWZ_BLOCK_SQUARE = 1 /* 128 x 128: the scale of row block mb, block kb at
+                          scales[mb * ld_scales + kb] (ld_scales >= blocks
+                          along K)                                            */
+};
+
+/* An 8-bit matrix, K contiguous: element (m, k) is data[m * ld + k] times its
+ * block's scale.  data 16-byte aligned, ld a multiple of 16 (what lies beyond
+ * the last column of a row is not looked at); the last block of a row, and the
+ * last row of square blocks, may be cut by the edge. */
+typedef struct swz_fp8_matrix {
+  const void* data;
+  int64_t ld;
+  const float* scales;
+  int64_t ld_scales;
+  int fmt;   /* SWZ_E4M3 or SWZ_E5M2 */
+  int block; /* SWZ_BLOCK_ROW or SWZ_BLOCK_SQUARE */
+} swz_fp8_matrix;
+
+/*
+ * swz_quantize_fp8 -- x (M x K, rows ldx elements apart; SWZ_F16, SWZ_BF16 or
+ * SWZ_F32) to 8 bits with block scales, and / or its transpose:
+ *   q  (M x K, rows ldq apart) and scales  -- x in blocks of its rows or squares
+ *   qt (K x M, rows ldqt apart) and scales_t -- x^T in blocks of its own rows
+ *      (128 values along M) or in the same squares
+ * either pair may be NULL, not both; ldq, ldqt as in swz_fp8_matrix.  For a
+ * block with largest magnitude amax:
+ *   ac = max(amax, 2^-96), r = F / ac, scale = ac / F (both rounded to fp32;
+ *   F = 448 for e4m3, 57344 for e5m2), q = x * r rounded to nearest even.
+ * A block of zeros gives zeros; one that holds an infinity or NaN gives a
+ * scale that is not finite and reads back as not finite.  The bytes up to the
+ * next multiple of 16 of a row of qt (8 of q) are written as zeros.
+ * M = 0 or K = 0: no-op.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_quantize_fp8(const void* x, int dtype, int64_t ldx, int M, int K, int block, int fmt,
+                     void* q, int64_t ldq, float* scales, int64_t ld_scales, void* qt,
+                     int64_t ldqt, float* scales_t, int64_t ld_scales_t, void* stream);
+
+/* Options of swz_gemm_fp8; NULL = serpentine order with strips of 8, the
+ * rest zero. */
+typedef struct swz_gemm_fp8_opts {
+  int order, group;     /* tile order as in swz_gemm                          */
+  int tile;             /* 0 automatic; 128: one CTA, 128 x 128 of C; 256: CTA
+                           pair, 256 x 256                                    */
+  int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share a
+                           128 x 128 tile's K and add their sums in order     */
+  int num_programs;     /* tile 128 or 256 without a split: CTAs to launch (a
+                           multiple of 2 for 256); 0 = one per SM             */
+  uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                       */
+  uint32_t timeout_ms;  /* bound of every device wait; 0 = 2000 ms            */
+} swz_gemm_fp8_opts;
+
+/*
+ * swz_gemm_fp8 -- C = A * B^T:
+ *   C[m, n] = sum over blocks kb of 128 along K of  sa[m, kb] * sb[n, kb]
+ *             * sum over k in kb of  A[m, k] * B[n, k]
+ * A: M x K in row blocks; B: N x K in row or square blocks; formats free on
+ * each side.  C: M x N, rows ldc elements apart, SWZ_F32, SWZ_BF16 or SWZ_F16
+ * (written, never read); sums in fp32, rounded once.  Any M, N, K >= 0 (K = 0
+ * writes zeros); rows of C that start on 16 or 32 bytes are stored wider.
+ * The result is deterministic; the automatic choice of tile and split depends
+ * on the sizes and the SM count only.  Errors: SWZ_EINVAL, SWZ_ENOTBIJECTIVE,
+ * SWZ_EUNSUPPORTED (A in square blocks, unknown tile or split, a split of more
+ * parts than blocks of K), SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t ldc,
+                 int c_dtype, int M, int N, int K, const swz_gemm_fp8_opts* opts, void* stream);
+
+/*
+ * swz_linear_fp8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is
+ * quantised in row blocks (e4m3) and multiplied by W (N x K) as in
+ * swz_gemm_fp8.  Up to 16 rows one kernel reads W once and quantises x on the
+ * way; more rows go through d_workspace (16-byte aligned, at least
+ * swz_linear_fp8_workspace_size bytes; contents free before and after; NULL
+ * when the size is 0).  Errors: as swz_gemm_fp8.
+ */
+int swz_linear_fp8(const void* x, int dtype, int64_t ldx, const swz_fp8_matrix* W, void* y,
+                   int64_t ldy, int y_dtype, int M, int N, int K, void* d_workspace,
+                   uint64_t workspace_bytes, void* stream);
+int swz_linear_fp8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
+
 /* Synchronises `stream`, then returns and clears the current device's
  * status word: SWZ_OK, or SWZ_ETIMEOUT if a kernel's bounded wait expired
  * since the last check. */

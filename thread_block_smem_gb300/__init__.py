@@ -8,7 +8,9 @@ Two layers:
   * ``swz_*`` -- one-to-one mirrors of the C entry points (raw device
     pointers as ints, stream as an int cudaStream_t).
   * ``tile_map``, ``gemm``, ``transpose``, ``gemm_plan`` -- the same calls on
-    torch tensors (pointers and the current stream are taken from them).
+    torch tensors (pointers and the current stream are taken from them); the
+    linear-layer operators (``quantize_fp8``, ``gemm_fp8``, ``linear_fp8`` and
+    its gradient) are in ``linear.py``.
 """
 from __future__ import annotations
 
@@ -37,7 +39,8 @@ EXPORTS = ["swz_tile_map", "swz_is_bijective", "swz_gemm", "swz_gemm_ex", "swz_g
            "swz_device_info", "swz_l2_model", "swz_gemm_workspace_size",
            "swz_gemm_streamk_noalloc", "swz_gemm_host", "swz_gemm_mma_sync", "swz_tc_rate",
            "swz_tc_rate_ex",
-           "swz_l2_model_bytes", "swz_calibrate", "swz_gemm_die_plan"]
+           "swz_l2_model_bytes", "swz_calibrate", "swz_gemm_die_plan", "swz_quantize_fp8",
+           "swz_gemm_fp8", "swz_linear_fp8", "swz_linear_fp8_workspace_size"]
 
 
 class SwzError(RuntimeError):
@@ -97,6 +100,7 @@ def lib() -> ctypes.CDLL:
         L.swz_calibrate.argtypes = [ip, i, ip]
         L.swz_gemm_die_plan.argtypes = [i, i, i, ctypes.POINTER(swz_gemm_opts),
                                         ctypes.POINTER(ctypes.c_int32), i, ip, ip, ip]
+        linear.declare(L)
         for name in EXPORTS:
             if name != "swz_strerror":
                 getattr(L, name).restype = ctypes.c_int
@@ -470,3 +474,12 @@ def transpose(x, layout="xor", out=None, stream=None):
 def check_status(stream=None):
     """Raises SwzError(SWZ_ETIMEOUT) if a bounded device wait expired."""
     _check(swz_check_status(_stream(stream)), "swz_check_status")
+
+
+# linear layers in 8 bits (linear.py)
+from . import linear  # noqa: E402
+from .linear import (SWZ_BLOCK_ROW, SWZ_BLOCK_SQUARE, SWZ_E4M3, SWZ_E5M2, SWZ_F32,  # noqa: E402,F401
+                     fp8_empty, fp8_linear, gemm_fp8, linear_fp8, linear_fp8_backward,
+                     linear_fp8_forward, quantize_fp8, swz_fp8_matrix, swz_gemm_fp8,
+                     swz_gemm_fp8_opts, swz_linear_fp8, swz_linear_fp8_workspace_size,
+                     swz_quantize_fp8)

@@ -47,6 +47,7 @@
 #include <vector>
 
 #include "common.h"
+#include "ops.h"
 #include "ptx.cuh"
 #include "tile_order.cuh"
 
@@ -1656,7 +1657,9 @@ extern "C" int swz_check_status(void* stream) {
   if (v != 0) {
     const unsigned int zero = 0;
     SWZ_CUDA_TRY(cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero)));
-    return SWZ_ETIMEOUT;
   }
-  return SWZ_OK;
+  bool expired = false;  // the linear-layer operators keep a word of their own
+  const int rc = take_op_status(&expired);
+  if (rc != SWZ_OK) return rc;
+  return v != 0 || expired ? SWZ_ETIMEOUT : SWZ_OK;
 }

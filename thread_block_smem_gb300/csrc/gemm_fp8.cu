@@ -1,0 +1,609 @@
+// gemm_fp8.cu -- C = A * B^T of 8-bit operands with one fp32 scale for each
+// block of 128 along K:
+//     C[m, n] = sum over blocks kb of  sa[m, kb] sb[n, kb]
+//               * sum over k in kb of  A[m, k] B[n, k]
+// A (M x K) has row blocks (1 x 128); B (N x K) square (128 x 128) or row
+// blocks.  Both K-major, e4m3 or e5m2 each; C fp32, bf16 or fp16.
+//
+// Mathematics and split: the tensor core sums the 128 products of a block
+// exactly scaled operands in fp32; the sum of a block is scaled and added to
+// fp32 accumulators in registers.  So every block of K is an MMA accumulation
+// of its own, and its tile is read back from TMEM, multiplied and added.
+//   * 320 threads, one CTA per SM.  Warps 0-7: the sums (warp w: TMEM lanes
+//     32 (w mod 4) .., columns half w / 4 of the tile), warp 8: TMA producer,
+//     warp 9: TMEM allocation and (one lane) MMA issue.
+//   * TMEM holds 512 / BN tiles in turn, so the tensor core runs ahead of the
+//     readers; a stage of shared memory is one block of K (128 bytes a row).
+//   * CTA pair (256 x 256): each CTA loads its 128 rows of A and half of B
+//     and sums 128 x 256 of C; one CTA: 128 x 128.
+//   * split: a cluster of 2, 4 or 8 CTAs shares one 128 x 128 tile by ranges
+//     of K and adds the partial tiles through distributed shared memory in
+//     rank order (deterministic, no workspace): for few tiles.
+//   * tiles are dealt out by the framework's tile orders, w = cluster + i P.
+#include <mutex>
+
+#include "common.h"
+#include "f8.cuh"
+#include "ops.h"
+#include "pipe.cuh"
+#include "tile_order.cuh"
+
+namespace swz {
+namespace gemm8 {
+
+constexpr int BM = 128, BK = 128;
+constexpr int kMathWarps = 8;
+constexpr int kThreads = (kMathWarps + 2) * 32;
+
+template <int BN, bool PAIR>
+struct Cfg {
+  static constexpr int CG = PAIR ? 2 : 1;
+  static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // rows of B this CTA loads
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN_LOCAL * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 6;
+  static constexpr int NBUF = 512 / BN;
+  static constexpr int COLS = BN / 2;  // columns a warp sums
+  static constexpr int SB_BYTES = kMathWarps * 2 * COLS * 4;  // scales of B by column
+  static constexpr int BARS = 2 * STAGES + 2 * NBUF + 1;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SB_BYTES + BARS * 8 + 16;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(STAGES * STAGE_BYTES >= BM * BN * 4 || PAIR, "a partial tile fits the ring");
+};
+
+struct Params {
+  void* C;
+  int64_t ldc;
+  const float* sa;
+  int64_t ldsa;
+  const float* sb;
+  int64_t ldsb;
+  int M, N;
+  int c_dtype;
+  int order;
+  uint32_t group, sched_m, sched_n, num_kb, idesc, split;
+  uint32_t c_align;  // bytes that every row start and base of C are a multiple of (32, 16 or less)
+  uint32_t debug_flags;
+  unsigned int* status;
+  uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ uint32_t pack_out(float a, float b, int dtype) {
+  if (dtype == SWZ_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// one element, for the ragged edge and unaligned rows
+__device__ __forceinline__ void store1(void* C, int64_t at, float v, int dtype) {
+  if (dtype == SWZ_F32) static_cast<float*>(C)[at] = v;
+  else if (dtype == SWZ_BF16) static_cast<__nv_bfloat16*>(C)[at] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(C)[at] = __float2half_rn(v);
+}
+
+// 16 consecutive elements of a row starting at column n (a multiple of 16)
+__device__ __forceinline__ void store16(const Params& p, int64_t row, int n, const float (&f)[16]) {
+  const int64_t at = row * p.ldc + n;
+  if (n + 16 <= p.N && p.c_align >= 16) {
+    if (p.c_dtype == SWZ_F32) {
+      float* c = static_cast<float*>(p.C) + at;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(f[8 * h + j]);
+        if (p.c_align >= 32) {
+          pipe::st_global_32b(c + 8 * h, v);
+        } else {
+          *reinterpret_cast<uint4*>(c + 8 * h) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(c + 8 * h + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+      }
+    } else {
+      uint16_t* c = static_cast<uint16_t*>(p.C) + at;
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = pack_out(f[2 * j], f[2 * j + 1], p.c_dtype);
+      if (p.c_align >= 32) {
+        pipe::st_global_32b(c, v);
+      } else {
+        *reinterpret_cast<uint4*>(c) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4*>(c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (n + j < p.N) store1(p.C, at + j, f[j], p.c_dtype);
+  }
+}
+
+template <int BN, bool PAIR, bool BROW>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA,
+                    const __grid_constant__ CUtensorMap tmB, const Params p) {
+  using K_ = Cfg<BN, PAIR>;
+  constexpr int CG = K_::CG, STAGES = K_::STAGES, NBUF = K_::NBUF, COLS = K_::COLS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sA = ptx::smem_u32(smem);
+  const uint32_t sB = sA + STAGES * K_::A_BYTES;
+  float* sb_cols = reinterpret_cast<float*>(smem + STAGES * K_::STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * K_::STAGE_BYTES + K_::SB_BYTES);
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + NBUF + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + K_::BARS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // rank: of a pair, which 128 rows of the tile; of a split, which range of K
+  const uint32_t crank = (PAIR || p.split > 1) ? ptx::cluster_ctarank() : 0u;
+  const uint32_t rank = PAIR ? crank : 0u;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tmA);
+    ptx::prefetch_tensormap(&tmB);
+    for (uint32_t s = 0; s < uint32_t(STAGES); ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (uint32_t a = 0; a < uint32_t(NBUF); ++a) {
+      ptx::mbar_init(tfull_bar(a), 1);
+      ptx::mbar_init(tempty_bar(a), kMathWarps * CG);
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMathWarps + 1) {
+    ptx::tmem_alloc<CG>(ptx::smem_u32(tmem_slot), 512);
+    ptx::tmem_relinquish<CG>();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  pipe::Ctl ctl;
+  ctl.status = p.status;
+  ctl.abort_flag = abort_flag;
+  ctl.peer_abort = 0;
+  if constexpr (PAIR) ctl.peer_abort = ptx::map_to_rank(ptx::smem_u32(abort_flag), rank ^ 1u);
+  ctl.timeout_ns = p.timeout_ns;
+
+  const uint32_t units = p.sched_m * p.sched_n;
+  const uint32_t cl = PAIR ? 2u : p.split;
+  const uint32_t w0 = blockIdx.x / cl, P = gridDim.x / cl;
+  uint32_t kb0 = 0, kb1 = p.num_kb;
+  if (!PAIR && p.split > 1) {
+    kb0 = uint32_t(uint64_t(p.num_kb) * crank / p.split);
+    kb1 = uint32_t(uint64_t(p.num_kb) * (crank + 1) / p.split);
+  }
+  // nothing above touches global memory
+  ptx::grid_dep_wait();
+  if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
+  bool aborted = false;
+
+  if (warp == kMathWarps) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
+      const uint64_t pol = ptx::l2_policy_evict_last();
+      for (uint32_t w = w0; w < units && !aborted; w += P) {
+        const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
+        const int32_t m0 = int32_t((t.m * CG + rank) * BM);
+        const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
+        for (uint32_t kb = kb0; kb < kb1; ++kb) {
+          if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) { aborted = true; break; }
+          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
+          const int32_t k0 = int32_t(kb * BK);
+          const uint32_t a_dst = sA + stage * K_::A_BYTES, b_dst = sB + stage * K_::B_BYTES;
+          if (skip) {
+            skip = false;
+          } else if constexpr (PAIR) {
+            const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
+            ptx::tma_load_2d_pair(a_dst, &tmA, fb, k0, m0, pol);
+            ptx::tma_load_2d_pair(b_dst, &tmB, fb, k0, n0, pol);
+          } else {
+            ptx::tma_load_2d(a_dst, &tmA, full_bar(stage), k0, m0, pol);
+            ptx::tma_load_2d(b_dst, &tmB, full_bar(stage), k0, n0, pol);
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      // every stage released: no commit is in flight towards this CTA
+      for (int i = 0; i < STAGES && !aborted; ++i) {
+        if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) aborted = true;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (aborted) pipe::spin_ns(50000);  // copies already issued land
+    }
+    __syncwarp();
+  } else if (warp == kMathWarps + 1) {
+    // ---------------- MMA issuer (leader CTA) ----------------
+    if (lane == 0 && leader) {
+      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+      bool issued = false;
+      const uint64_t adesc0 = pipe::sdesc128(sA, 16, 1024);
+      const uint64_t bdesc0 = pipe::sdesc128(sB, 16, 1024);
+      for (uint32_t w = w0; w < units && !aborted; w += P) {
+        for (uint32_t kb = kb0; kb < kb1; ++kb) {
+          if (!pipe::wait(tempty_bar(buf), buf_phase ^ 1u, ctl) ||
+              !pipe::wait(full_bar(stage), phase, ctl)) {
+            aborted = true;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::A_BYTES >> 4));
+          const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::B_BYTES >> 4));
+          const uint32_t d = tmem_base + buf * BN;
+#pragma unroll
+          for (uint32_t kk = 0; kk < BK / 32; ++kk)
+            pipe::mma_f8<CG>(d, a + kk * 2, b + kk * 2, p.idesc, kk != 0);
+          issued = true;
+          if constexpr (PAIR) {
+            ptx::mma_commit_pair(empty_bar(stage), 0x3);
+            ptx::mma_commit_pair(tfull_bar(buf), 0x3);
+          } else {
+            ptx::mma_commit(empty_bar(stage));
+            ptx::mma_commit(tfull_bar(buf));
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+        }
+      }
+      if (aborted && issued) {
+        if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
+        else ptx::mma_commit(drain_bar);
+        const uint64_t t0 = ptx::global_timer_ns();
+        while (!ptx::mbar_try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp < kMathWarps) {
+    // ---------------- sums ----------------
+    const uint32_t q = warp & 3u, half = warp >> 2;
+    uint32_t buf = 0, buf_phase = 0;
+    float* const my_sb = sb_cols + warp * 2 * COLS;
+    uint64_t acc[COLS / 2];
+    for (uint32_t w = w0; w < units && !aborted; w += P) {
+      const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
+      const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
+      const int64_t col0 = int64_t(t.n) * BN + half * COLS;
+      const bool row_in = row < p.M;
+      const float* sa = p.sa + row;
+      const float* sb = BROW ? p.sb : p.sb + (col0 / 128 < (p.N + 127) / 128 ? col0 / 128 : 0) * p.ldsb;
+      // scales of a block for this thread's row and (square blocks) for its
+      // columns, loaded two blocks ahead
+      auto load_s = [&](uint32_t kb) -> float2 {
+        if (kb >= kb1) return make_float2(0.f, 0.f);
+        float2 v;
+        v.x = row_in ? __ldg(sa + int64_t(kb) * p.ldsa) : 0.f;
+        v.y = BROW ? 1.f : __ldg(sb + kb);
+        return v;
+      };
+      float sbn[COLS / 32];
+      auto load_sb = [&](uint32_t kb) {
+#pragma unroll
+        for (int j = 0; j < COLS / 32; ++j) {
+          const int64_t n = col0 + j * 32 + lane;
+          sbn[j] = kb < kb1 && n < p.N ? __ldg(sb + int64_t(kb) * p.ldsb + n) : 0.f;
+        }
+      };
+      float2 s_cur = load_s(kb0), s_n1 = load_s(kb0 + 1);
+      if constexpr (BROW) load_sb(kb0);
+#pragma unroll
+      for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+#pragma unroll 1
+      for (uint32_t kb = kb0; kb < kb1; ++kb) {
+        const float2 s_n2 = load_s(kb + 2);
+        float* const sbuf = my_sb + (kb & 1u) * COLS;
+        if constexpr (BROW) {
+#pragma unroll
+          for (int j = 0; j < COLS / 32; ++j) sbuf[j * 32 + lane] = sbn[j];
+          __syncwarp();
+          load_sb(kb + 1);
+        }
+        const bool ok = pipe::wait(tfull_bar(buf), buf_phase, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+        ptx::tc_fence_after();
+        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + buf * BN + half * COLS;
+        const float s = s_cur.x * s_cur.y;
+        const uint64_t s2 = pipe::pack2(s, s);
+        uint32_t r[2][16];
+        pipe::tmem_ld16(taddr, r[0]);
+        pipe::tmem_ld_wait16(r[0]);
+#pragma unroll
+        for (int c = 0; c < COLS / 16; ++c) {
+          if (c + 1 < COLS / 16) pipe::tmem_ld16(taddr + (c + 1) * 16, r[(c + 1) & 1]);
+          if constexpr (BROW) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 b = *reinterpret_cast<const float4*>(sbuf + c * 16 + 4 * j);
+              acc[c * 8 + 2 * j] =
+                  pipe::fma2(pipe::pack2(r[c & 1][4 * j], r[c & 1][4 * j + 1]),
+                             pipe::mul2(pipe::pack2(b.x, b.y), s2), acc[c * 8 + 2 * j]);
+              acc[c * 8 + 2 * j + 1] =
+                  pipe::fma2(pipe::pack2(r[c & 1][4 * j + 2], r[c & 1][4 * j + 3]),
+                             pipe::mul2(pipe::pack2(b.z, b.w), s2), acc[c * 8 + 2 * j + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[c * 8 + j] = pipe::fma2(pipe::pack2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2,
+                                          acc[c * 8 + j]);
+          }
+          if (c + 1 < COLS / 16) pipe::tmem_ld_wait16(r[(c + 1) & 1]);
+          if (c + 2 == COLS / 16) {  // the last columns have been read
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(buf), 0));
+              else ptx::mbar_arrive(tempty_bar(buf));
+            }
+          }
+        }
+        s_cur = s_n1;
+        s_n1 = s_n2;
+        if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+      }
+      if (aborted) break;
+      if (PAIR || p.split == 1) {
+        if (row_in) {
+#pragma unroll
+          for (int c = 0; c < COLS / 16; ++c) {
+            const int64_t n = col0 + c * 16;
+            if (n >= p.N) break;
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) pipe::unpack2(acc[c * 8 + j], f[2 * j], f[2 * j + 1]);
+            store16(p, row, int(n), f);
+          }
+        }
+      } else {
+        // partial tile to shared memory, over the ring (every load has been
+        // consumed): row r, 16-byte chunk c at r * BN * 4 + (c ^ (r mod 32)) * 16
+        const uint32_t r = q * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < COLS / 4; ++c) {
+          float a, b, d, e;
+          pipe::unpack2(acc[2 * c], a, b);
+          pipe::unpack2(acc[2 * c + 1], d, e);
+          const uint32_t chunk = (half * (COLS / 4) + c) ^ (r & 31u);
+          *reinterpret_cast<float4*>(smem + r * (BN * 4) + chunk * 16) = make_float4(a, b, d, e);
+        }
+      }
+    }
+  }
+
+  if (!PAIR && p.split > 1) {
+    // add the partial tiles: rank r of S takes rows r * 128 / S .. of the tile
+    __syncwarp();
+    ptx::cluster_sync();
+    if (warp < kMathWarps && !aborted) {
+      const TileCoord t = tile_of(p.order, w0, p.sched_m, p.sched_n, p.group);
+      const uint32_t rows = BM / p.split;
+      for (uint32_t i = warp; i < rows; i += kMathWarps) {
+        const uint32_t r = crank * rows + i;
+        const int64_t row = int64_t(t.m) * BM + r;
+        if (row >= p.M) break;
+        const uint32_t at = sA + r * (BN * 4) + ((lane ^ (r & 31u)) << 4);
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t j = 0; j < p.split; ++j) {
+          float a, b, c, d;
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+                       : "r"(ptx::map_to_rank(at, j))
+                       : "memory");
+          f[0] += a;
+          f[1] += b;
+          f[2] += c;
+          f[3] += d;
+        }
+        const int64_t n = int64_t(t.n) * BN + lane * 4;
+        const int64_t o = row * p.ldc + n;
+        if (n + 4 <= p.N && p.c_align >= 16) {
+          if (p.c_dtype == SWZ_F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.C) + o) =
+                make_float4(f[0], f[1], f[2], f[3]);
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + o) =
+                make_uint2(pack_out(f[0], f[1], p.c_dtype), pack_out(f[2], f[3], p.c_dtype));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) store1(p.C, o + j, f[j], p.c_dtype);
+        }
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // no CTA leaves while its partial tile is read
+  }
+
+  // ---------------- teardown ----------------
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == kMathWarps + 1) ptx::tmem_dealloc<CG>(tmem_base, 512);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int BN, bool PAIR, bool BROW>
+static int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& prm,
+                  uint32_t programs, cudaStream_t stream) {
+  using K_ = Cfg<BN, PAIR>;
+  auto kern = gemm_fp8_kernel<BN, PAIR, BROW>;
+  static std::mutex mu;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  SWZ_CUDA_TRY(cudaGetDevice(&dev));
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      SWZ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        K_::SMEM_BYTES));
+      attr_set[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(programs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = K_::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = PAIR ? 2 : prm.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, ta, tb, prm));
+  return SWZ_OK;
+}
+
+struct Choice {
+  int tile;        // 128: one CTA, 256: CTA pair
+  uint32_t split;  // CTAs that share a tile's K (tile 128)
+};
+
+static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// The variant with the least estimated time, in SM cycles: waves of tiles
+// times (blocks of K times the cycles of one, plus a tile's fixed part).
+static Choice choose(uint64_t M, uint64_t N, uint64_t kb, uint32_t sms) {
+  const uint64_t pairs = sms / 2;
+  uint64_t best = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), pairs) * (kb * 540 + 3000);
+  Choice c{256, 1};
+  const uint64_t tiles = ceil_div(M, 128) * ceil_div(N, 128);
+  for (uint32_t s = 1; s <= 8; s *= 2) {
+    if (s > 1 && kb < 2 * s) break;
+    const uint64_t t = ceil_div(tiles * s, sms) * (ceil_div(kb, s) * 380 + 2500 + (s > 1 ? 2000 : 0));
+    if (t < best) {
+      best = t;
+      c = Choice{128, s};
+    }
+  }
+  return c;
+}
+
+}  // namespace gemm8
+}  // namespace swz
+
+using namespace swz;
+using namespace swz::gemm8;
+
+static bool matrix_ok(const swz_fp8_matrix* m, int rows, int K) {
+  const int64_t kb = (int64_t(K) + 127) / 128;
+  return m->data && aligned16(m->data) && m->ld >= K && m->ld % 16 == 0 && m->scales &&
+         aligned4(m->scales) && m->ld_scales >= (m->block == SWZ_BLOCK_SQUARE ? kb : int64_t(rows));
+}
+
+extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t ldc,
+                            int c_dtype, int M, int N, int K, const swz_gemm_fp8_opts* opts,
+                            void* stream) {
+  swz_gemm_fp8_opts o = {};
+  o.order = SWZ_SERPENTINE;
+  o.group = 8;
+  if (opts) o = *opts;
+  if (M < 0 || N < 0 || K < 0 || !A || !B) return SWZ_EINVAL;
+  if (!order_is_valid(o.order) || (order_uses_group(o.order) && o.group < 1)) return SWZ_EINVAL;
+  if (c_dtype != SWZ_F16 && c_dtype != SWZ_BF16 && c_dtype != SWZ_F32) return SWZ_EINVAL;
+  for (const swz_fp8_matrix* m : {A, B}) {
+    if (m->fmt != SWZ_E4M3 && m->fmt != SWZ_E5M2) return SWZ_EINVAL;
+    if (m->block != SWZ_BLOCK_ROW && m->block != SWZ_BLOCK_SQUARE) return SWZ_EINVAL;
+  }
+  if (A->block != SWZ_BLOCK_ROW) return SWZ_EUNSUPPORTED;
+  if (o.tile != 0 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
+  if (o.split_k != 0 && o.split_k != 1 && o.split_k != 2 && o.split_k != 4 && o.split_k != 8)
+    return SWZ_EUNSUPPORTED;
+  if (o.tile == 256 && o.split_k > 1) return SWZ_EUNSUPPORTED;
+  if (o.num_programs < 0 || (o.num_programs && o.tile == 0)) return SWZ_EINVAL;
+  if (M == 0 || N == 0) return SWZ_OK;
+  const int64_t es = c_dtype == SWZ_F32 ? 4 : 2;
+  const uintptr_t ca = reinterpret_cast<uintptr_t>(C);
+  if (!C || ca % uintptr_t(es) != 0 || (M > 1 && ldc < N)) return SWZ_EINVAL;
+  if (K > 0 && (!matrix_ok(A, M, K) || !matrix_ok(B, N, K))) return SWZ_EINVAL;
+  DeviceInfo dev{};
+  int rc = current_device(&dev);
+  if (rc != SWZ_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t ld = M > 1 ? ldc : N;
+  if (K == 0) {
+    SWZ_CUDA_TRY(cudaMemset2DAsync(C, size_t(ld * es), 0, size_t(N) * es, size_t(M), s));
+    return SWZ_OK;
+  }
+  const uint32_t kb = uint32_t((int64_t(K) + 127) / 128);
+  Choice ch = choose(uint64_t(M), uint64_t(N), kb, uint32_t(dev.num_sms));
+  if (o.tile == 256) ch = Choice{256, 1};
+  if (o.tile == 128) ch = Choice{128, o.split_k ? uint32_t(o.split_k) : (ch.tile == 128 ? ch.split : 1u)};
+  if (o.tile == 0 && o.split_k) ch = Choice{o.split_k == 1 ? ch.tile : 128, uint32_t(o.split_k)};
+  if (ch.split > kb) return SWZ_EUNSUPPORTED;  // an empty range of K
+  const bool pair = ch.tile == 256;
+  const uint64_t sm = ceil_div(uint64_t(M), pair ? 256 : 128);
+  const uint64_t sn = ceil_div(uint64_t(N), pair ? 256 : 128);
+  const uint64_t cl = pair ? 2 : ch.split;
+  if (sm * sn * cl > uint64_t(INT32_MAX)) return SWZ_EINVAL;
+  if ((o.order == SWZ_MORTON || o.order == SWZ_XOR) &&
+      !order_is_bijective(o.order, uint32_t(sm), uint32_t(sn), 1))
+    return SWZ_ENOTBIJECTIVE;
+  if (o.num_programs % int(cl) != 0) return SWZ_EINVAL;
+
+  CUtensorMap ta, tb;
+  rc = encode_bytes(&ta, A->data, uint64_t(M), uint64_t(K), uint64_t(A->ld), 128);
+  if (rc != SWZ_OK) return rc;
+  rc = encode_bytes(&tb, B->data, uint64_t(N), uint64_t(K), uint64_t(B->ld), 128);
+  if (rc != SWZ_OK) return rc;
+
+  Params prm{};
+  prm.C = C;
+  prm.ldc = ld;
+  prm.sa = A->scales;
+  prm.ldsa = A->ld_scales;
+  prm.sb = B->scales;
+  prm.ldsb = B->ld_scales;
+  prm.M = M;
+  prm.N = N;
+  prm.c_dtype = c_dtype;
+  prm.order = o.order;
+  prm.group = order_uses_group(o.order) ? uint32_t(o.group) : 1u;
+  prm.sched_m = uint32_t(sm);
+  prm.sched_n = uint32_t(sn);
+  prm.num_kb = kb;
+  prm.idesc = pipe::idesc(A->fmt, B->fmt, false, false, pair ? 256 : 128, pair ? 256 : 128);
+  prm.split = ch.split;
+  const uintptr_t bits = ca | (M > 1 ? uintptr_t(ld * es) : 0);
+  prm.c_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
+  prm.debug_flags = o.debug_flags;
+  prm.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  rc = op_status_word(&prm.status);
+  if (rc != SWZ_OK) return rc;
+  uint64_t programs = sm * sn * cl;
+  if (ch.split == 1) {
+    const uint64_t cap = o.num_programs ? uint64_t(o.num_programs)
+                                        : uint64_t(dev.num_sms) / cl * cl;
+    if (programs > cap) programs = cap;
+  }
+  const bool brow = B->block == SWZ_BLOCK_ROW;
+  if (pair)
+    return brow ? launch<256, true, true>(ta, tb, prm, uint32_t(programs), s)
+                : launch<256, true, false>(ta, tb, prm, uint32_t(programs), s);
+  return brow ? launch<128, false, true>(ta, tb, prm, uint32_t(programs), s)
+              : launch<128, false, false>(ta, tb, prm, uint32_t(programs), s);
+}

@@ -1,0 +1,309 @@
+"""Linear layers in 8 bits on torch tensors: block quantisation, the product of
+8-bit operands, the layer's forward and gradient, over the C entry points of
+include/swz.h (argument marshalling only; every computation runs in the
+library's kernels).
+
+8-bit matrices are ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` tensors of
+shape (rows, K) whose rows start on multiples of 16 bytes (``quantize_fp8``
+makes them so; ``fp8_empty`` allocates one).  Scales are fp32: of ``"row"``
+blocks (1 x 128) a tensor (ceil(K / 128), rows), of ``"square"`` ones (128 x
+128) a tensor (ceil(rows / 128), ceil(K / 128)).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import thread_block_smem_gb300 as _swz
+
+SWZ_F32 = 3
+SWZ_E4M3, SWZ_E5M2 = 0, 1
+SWZ_BLOCK_ROW, SWZ_BLOCK_SQUARE = 0, 1
+BLOCK = 128
+BLOCKS = {"row": SWZ_BLOCK_ROW, "square": SWZ_BLOCK_SQUARE}
+FORMATS = {"e4m3": SWZ_E4M3, "e5m2": SWZ_E5M2}
+
+
+class swz_fp8_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("ld_scales", ctypes.c_int64), ("fmt", ctypes.c_int), ("block", ctypes.c_int)]
+
+
+class swz_gemm_fp8_opts(ctypes.Structure):
+    _fields_ = [("order", ctypes.c_int), ("group", ctypes.c_int), ("tile", ctypes.c_int),
+                ("split_k", ctypes.c_int), ("num_programs", ctypes.c_int),
+                ("debug_flags", ctypes.c_uint32), ("timeout_ms", ctypes.c_uint32)]
+
+
+def declare(L):
+    """Argument types of this module's entry points on the loaded library."""
+    i, i64, u64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
+    mat = ctypes.POINTER(swz_fp8_matrix)
+    L.swz_quantize_fp8.argtypes = [vp, i, i64, i, i, i, i, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.swz_gemm_fp8.argtypes = [mat, mat, vp, i64, i, i, i, i, ctypes.POINTER(swz_gemm_fp8_opts), vp]
+    L.swz_linear_fp8.argtypes = [vp, i, i64, mat, vp, i64, i, i, i, i, vp, u64, vp]
+    L.swz_linear_fp8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
+
+
+# ---- raw mirrors ----------------------------------------------------------------
+def swz_quantize_fp8(x, dtype, ldx, M, K, block, fmt, q, ldq, scales, ld_scales, qt, ldqt,
+                     scales_t, ld_scales_t, stream=0):
+    return _swz.lib().swz_quantize_fp8(x, dtype, ldx, M, K, block, fmt, q, ldq, scales, ld_scales,
+                                       qt, ldqt, scales_t, ld_scales_t, stream)
+
+
+def swz_gemm_fp8(A, B, C, ldc, c_dtype, M, N, K, opts=None, stream=0):
+    return _swz.lib().swz_gemm_fp8(ctypes.byref(A), ctypes.byref(B), C, ldc, c_dtype, M, N, K,
+                                   ctypes.byref(opts) if opts is not None else None, stream)
+
+
+def swz_linear_fp8(x, dtype, ldx, W, y, ldy, y_dtype, M, N, K, workspace, workspace_bytes,
+                   stream=0):
+    return _swz.lib().swz_linear_fp8(x, dtype, ldx, ctypes.byref(W), y, ldy, y_dtype, M, N, K,
+                                     workspace, workspace_bytes, stream)
+
+
+def swz_linear_fp8_workspace_size(M, N, K):
+    b = ctypes.c_uint64(0)
+    rc = _swz.lib().swz_linear_fp8_workspace_size(M, N, K, ctypes.byref(b))
+    return rc, b.value
+
+
+# ---- helpers ----------------------------------------------------------------------
+_types = None
+
+
+def _dtypes():
+    """{torch dtype: code} of the 16- and 32-bit types, and of the 8-bit ones."""
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.float16: _swz.SWZ_F16, torch.bfloat16: _swz.SWZ_BF16,
+                   torch.float32: SWZ_F32},
+                  {torch.float8_e4m3fn: SWZ_E4M3, torch.float8_e5m2: SWZ_E5M2})
+    return _types
+
+
+def _code(t, what):
+    codes = _dtypes()[0]
+    if t not in codes:
+        raise TypeError(f"{what} must be fp16, bf16 or fp32")
+    return codes[t]
+
+
+def _rows(x, what):
+    """(rows, columns, elements from row to row) of a 2-D tensor with contiguous rows."""
+    if x.dim() != 2:
+        raise ValueError(f"{what}: 2-D tensor expected")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: CUDA tensor expected")
+    m, k = x.shape
+    ld, one = x.stride()
+    if k > 1 and one != 1:
+        raise ValueError(f"{what}: contiguous rows expected")
+    if m > 1 and ld < k:
+        raise ValueError(f"{what}: rows must not overlap")
+    return m, k, ld if m > 1 else max(k, 1)
+
+
+def _on(stream):
+    """Context in which what is allocated belongs to the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _block(block):
+    if block not in BLOCKS:
+        raise ValueError("block must be 'row' or 'square'")
+    return BLOCKS[block]
+
+
+def _blocks(n):
+    return (n + BLOCK - 1) // BLOCK
+
+
+def fp8_empty(rows, cols, dtype, device="cuda"):
+    """Uninitialised 8-bit (rows, cols) tensor whose rows start on multiples of 16 bytes."""
+    import torch
+    ld = (cols + 15) // 16 * 16
+    q = torch.empty((rows, ld), dtype=dtype, device=device)
+    return q if ld == cols else q[:, :cols]
+
+
+def _matrix(q, scales, block, what):
+    """swz_fp8_matrix of an 8-bit tensor and its scales, checked."""
+    fmt = _dtypes()[1].get(q.dtype)
+    if fmt is None:
+        raise TypeError(f"{what}: float8_e4m3fn or float8_e5m2 expected")
+    m, k, ld = _rows(q, what)
+    if m <= 1 or k == 0:  # no second row whose place matters
+        ld = (k + 15) // 16 * 16
+    if ld % 16 or q.data_ptr() % 16:
+        raise ValueError(f"{what}: rows must start on multiples of 16 bytes")
+    if scales.dtype.itemsize != 4 or not scales.dtype.is_floating_point or not scales.is_cuda:
+        raise TypeError(f"{what}: fp32 CUDA scales expected")
+    want = (_blocks(k), m) if block == SWZ_BLOCK_ROW else (_blocks(m), _blocks(k))
+    if tuple(scales.shape) != want:
+        raise ValueError(f"{what}: scales of shape {want} expected, got {tuple(scales.shape)}")
+    _, _, lds = _rows(scales, f"{what} scales")
+    if scales.shape[0] <= 1:
+        lds = max(want[1], 1)
+    return swz_fp8_matrix(q.data_ptr(), ld, scales.data_ptr(), lds, fmt, block), m, k
+
+
+# ---- operators --------------------------------------------------------------------
+def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
+    """(q, scales) of x (M x K; fp16, bf16 or fp32, contiguous rows), with
+    ``transposed`` (q, scales, qt, scales_t): also x^T (K x M) in 8 bits, by
+    blocks of its own rows or by the same squares, in the same read of x.
+
+    For a block with largest magnitude amax: ac = max(amax, 2^-96), r = F / ac,
+    scale = ac / F (F = 448 for e4m3, 57344 for e5m2), q = x r rounded to
+    nearest even."""
+    import torch
+    M, K, ldx = _rows(x, "x")
+    code, b = _code(x.dtype, "x"), _block(block)
+    if fmt not in FORMATS:
+        raise ValueError("fmt must be 'e4m3' or 'e5m2'")
+    f8 = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
+    dev = x.device
+    kb, mb = _blocks(K), _blocks(M)
+    with _on(stream):
+        q = fp8_empty(M, K, f8, dev)
+        s = torch.empty((mb, kb) if b else (kb, M), dtype=torch.float32, device=dev)
+        qt = st = None
+        if transposed:
+            qt = fp8_empty(K, M, f8, dev)
+            st = torch.empty((kb, mb) if b else (mb, K), dtype=torch.float32, device=dev)
+    pad = lambda n: (n + 15) // 16 * 16  # noqa: E731
+    _swz._check(swz_quantize_fp8(
+        x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), pad(K), s.data_ptr(),
+        kb if b else M, qt.data_ptr() if transposed else None, pad(M),
+        st.data_ptr() if transposed else None, mb if b else K, _swz._stream(stream)),
+        "swz_quantize_fp8")
+    return (q, s, qt, st) if transposed else (q, s)
+
+
+def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order="serpentine",
+             group=8, tile=0, split_k=0, num_programs=0, debug_flags=0, timeout_ms=0,
+             stream=None):
+    """C = A B^T (M x N) of 8-bit operands: a (M x K) with scales sa of its row
+    blocks, b (N x K) with scales sb of its ``b_block`` blocks.  ``out`` (M x
+    N, contiguous rows) or ``out_dtype`` (fp32, bf16 or fp16; default bf16).
+    ``order``, ``group``: the order of the output tiles, as in ``gemm``;
+    ``tile``, ``split_k``, ``num_programs``: see swz_gemm_fp8_opts (0 =
+    automatic)."""
+    import torch
+    A, M, K = _matrix(a, sa, SWZ_BLOCK_ROW, "a")
+    B, N, K2 = _matrix(b, sb, _block(b_block), "b")
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a.device, stream)
+    opts = swz_gemm_fp8_opts(_swz._order(order), group, tile, split_k, num_programs, debug_flags,
+                             timeout_ms)
+    _swz._check(swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _swz._stream(stream)),
+                "swz_gemm_fp8")
+    return C
+
+
+def _output(out, dtype, M, N, device, stream):
+    """(tensor, elements from row to row, type code) of an M x N result."""
+    import torch
+    if out is None:
+        code = _code(dtype, "out_dtype")
+        with _on(stream):
+            return torch.empty((M, N), dtype=dtype, device=device), N, code
+    code = _code(out.dtype, "out")
+    m, n, ld = _rows(out, "out")
+    if (m, n) != (M, N):
+        raise ValueError(f"out: shape {(M, N)} expected")
+    return out, ld, code
+
+
+def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=None):
+    """y = x W^T (M x N): x (M x K; fp16, bf16 or fp32) is quantised in row
+    blocks (e4m3) and multiplied by W (N x K) kept as (qw, sw).  ``out`` or
+    ``out_dtype`` (default: x's type)."""
+    import torch
+    M, K, ldx = _rows(x, "x")
+    code = _code(x.dtype, "x")
+    W, N, K2 = _matrix(qw, sw, _block(w_block), "qw")
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x.device, stream)
+    rc, need = swz_linear_fp8_workspace_size(M, N, K)
+    _swz._check(rc, "swz_linear_fp8_workspace_size")
+    ws = None
+    if need:
+        with _on(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _swz._check(swz_linear_fp8(x.data_ptr(), code, ldx, W, y.data_ptr(), ldy, ycode, M, N, K,
+                               ws.data_ptr() if need else None, need, _swz._stream(stream)),
+                "swz_linear_fp8")
+    return y
+
+
+def linear_fp8_forward(x, w, *, out_dtype=None, stream=None):
+    """(y, saved) of a layer in training: y = x W^T with x (M x K) quantised in
+    row blocks and w (N x K) in square ones; ``saved`` holds x^T and W^T in 8
+    bits for linear_fp8_backward."""
+    qx, sx, qxt, sxt = quantize_fp8(x, "row", transposed=True, stream=stream)
+    qw, sw, qwt, swt = quantize_fp8(w, "square", transposed=True, stream=stream)
+    y = gemm_fp8(qx, sx, qw, sw, out_dtype=out_dtype or x.dtype, stream=stream)
+    return y, (qxt, sxt, qwt, swt)
+
+
+def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None, dw_dtype=None,
+                        stream=None):
+    """(dx, dw) of linear_fp8_forward: dx = dy W (M x K; default dy's type)
+    and dw = dy^T x (N x K; default fp32), dy quantised in row blocks along N
+    and along the rows; None in place of one that is not needed."""
+    import torch
+    qxt, sxt, qwt, swt = saved
+    M, N, ldd = _rows(dy, "dy")
+    if M != qxt.shape[1] or N != qwt.shape[1]:
+        raise ValueError("dy does not have the shape of the layer's output")
+    dx = dw = None
+    if need_dx or need_dw:
+        out = quantize_fp8(dy, "row", transposed=need_dw, stream=stream)
+        if need_dx:
+            dx = gemm_fp8(out[0], out[1], qwt, swt, out_dtype=dx_dtype or dy.dtype, stream=stream)
+        if need_dw:
+            dw = gemm_fp8(out[2], out[3], qxt, sxt, b_block="row",
+                          out_dtype=dw_dtype or torch.float32, stream=stream)
+    return dx, dw
+
+
+_function = None
+
+
+def fp8_linear(x, w):
+    """y = x W^T with its gradient, for torch.autograd: x (..., K), w (N, K);
+    forward and backward as linear_fp8_forward / linear_fp8_backward, the
+    gradient of w in fp32 rounded to w's type."""
+    global _function
+    if _function is None:
+        import torch
+
+        class Fp8Linear(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, w):
+                y, saved = linear_fp8_forward(x, w)
+                ctx.save_for_backward(*saved)
+                ctx.w_dtype = w.dtype
+                return y
+
+            @staticmethod
+            def backward(ctx, dy):
+                dy = dy if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1] else dy.contiguous()
+                return linear_fp8_backward(
+                    dy, ctx.saved_tensors, need_dx=ctx.needs_input_grad[0],
+                    need_dw=ctx.needs_input_grad[1], dw_dtype=ctx.w_dtype)
+
+        _function = Fp8Linear
+    flat = x.reshape(-1, x.shape[-1])
+    return _function.apply(flat, w).reshape(*x.shape[:-1], w.shape[0])
