@@ -566,6 +566,37 @@ int swz_linear_fp8(const void* x, int dtype, int64_t ldx, const swz_fp8_matrix* 
                    uint64_t workspace_bytes, void* stream);
 int swz_linear_fp8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
 
+/* Options of swz_newton_schulz; NULL = all zero. */
+typedef struct swz_newton_schulz_opts {
+  int tile;             /* 0 automatic for each product; 128 or 256 (CTA pair) */
+  uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                        */
+  uint32_t timeout_ms;  /* bound of every device wait; 0 = 2000 ms             */
+} swz_newton_schulz_opts;
+
+/*
+ * swz_newton_schulz -- the orthogonalised update of `batch` matrices G (m x n,
+ * rows ldg and matrices batch_stride_g elements apart; SWZ_F16, SWZ_BF16 or
+ * SWZ_F32): X = G / (|G|_F + eps), then `steps` (1 to 64) times
+ *   A = X X^T, B = b A + c A^2, X = a X + B X    (m <= n; for m > n with
+ *   A = X^T X on the right, which is the same X)
+ * and Y = X (rows ldy, matrices batch_stride_y apart; y_dtype).  Products
+ * with fp16 operands scaled by powers of two and fp32 sums; the a X term in
+ * fp32 in all steps but the last two (in the first of any number of steps).
+ * A matrix of zeros gives zeros; one with an infinity or NaN a result that is
+ * not finite.  d_workspace: 256-byte aligned device scratch of at least
+ * swz_newton_schulz_workspace_size bytes, contents free before and after;
+ * calls that share it must not overlap.  G and Y may be the same buffer.
+ * Limits: m * n <= 2^31, batch <= 65535; SWZ_EUNSUPPORTED for coefficients
+ * under which singular values can pass 10^15.  Errors: SWZ_EINVAL,
+ * SWZ_EUNSUPPORTED, SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t batch_stride_g, void* Y,
+                      int y_dtype, int64_t ldy, int64_t batch_stride_y, int batch, int m, int n,
+                      int steps, double a, double b, double c, double eps,
+                      const swz_newton_schulz_opts* opts, void* d_workspace,
+                      uint64_t workspace_bytes, void* stream);
+int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes);
+
 /* Synchronises `stream`, then returns and clears the current device's
  * status word: SWZ_OK, or SWZ_ETIMEOUT if a kernel's bounded wait expired
  * since the last check. */

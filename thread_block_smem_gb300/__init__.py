@@ -10,7 +10,7 @@ Two layers:
   * ``tile_map``, ``gemm``, ``transpose``, ``gemm_plan`` -- the same calls on
     torch tensors (pointers and the current stream are taken from them); the
     linear-layer operators (``quantize_fp8``, ``gemm_fp8``, ``linear_fp8`` and
-    its gradient) are in ``linear.py``.
+    its gradient, ``newton_schulz``) are in ``linear.py``.
 """
 from __future__ import annotations
 
@@ -40,7 +40,8 @@ EXPORTS = ["swz_tile_map", "swz_is_bijective", "swz_gemm", "swz_gemm_ex", "swz_g
            "swz_gemm_streamk_noalloc", "swz_gemm_host", "swz_gemm_mma_sync", "swz_tc_rate",
            "swz_tc_rate_ex",
            "swz_l2_model_bytes", "swz_calibrate", "swz_gemm_die_plan", "swz_quantize_fp8",
-           "swz_gemm_fp8", "swz_linear_fp8", "swz_linear_fp8_workspace_size"]
+           "swz_gemm_fp8", "swz_linear_fp8", "swz_linear_fp8_workspace_size",
+           "swz_newton_schulz", "swz_newton_schulz_workspace_size"]
 
 
 class SwzError(RuntimeError):
@@ -480,6 +481,7 @@ def check_status(stream=None):
 from . import linear  # noqa: E402
 from .linear import (SWZ_BLOCK_ROW, SWZ_BLOCK_SQUARE, SWZ_E4M3, SWZ_E5M2, SWZ_F32,  # noqa: E402,F401
                      fp8_empty, fp8_linear, gemm_fp8, linear_fp8, linear_fp8_backward,
-                     linear_fp8_forward, quantize_fp8, swz_fp8_matrix, swz_gemm_fp8,
-                     swz_gemm_fp8_opts, swz_linear_fp8, swz_linear_fp8_workspace_size,
-                     swz_quantize_fp8)
+                     linear_fp8_forward, newton_schulz, quantize_fp8, swz_fp8_matrix,
+                     swz_gemm_fp8, swz_gemm_fp8_opts, swz_linear_fp8,
+                     swz_linear_fp8_workspace_size, swz_newton_schulz, swz_newton_schulz_opts,
+                     swz_newton_schulz_workspace_size, swz_quantize_fp8)

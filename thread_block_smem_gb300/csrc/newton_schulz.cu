@@ -1,0 +1,882 @@
+// newton_schulz.cu -- the orthogonalised update: X = G / (|G|_F + eps), then
+// `steps` times
+//     A = X X^T,  B = b A + c A^2,  X = a X + B X          (m <= n)
+//     A = X^T X,  B = b A + c A^2,  X = a X + X B          (m >  n)
+// for a batch of m x n matrices, so the square products are on the short side.
+//
+// Mathematics and precision: the products run on the tensor cores with fp16
+// operands and fp32 sums.  What is rounded to fp16 is scaled by a power of two
+// first: singular values stay below a bound that the host steps through the
+// polynomial, which bounds every entry of X, A and B; the first X is G itself
+// times a power of two, the exact 1 / (|G| + eps) goes into the epilogues.
+// bf16 operands (8 times coarser) left the result 1 % off on normal matrices,
+// fp16 ones 0.1 %.  Directions with small singular values come out of the a X
+// term alone, growing by a at each step, and a rounding of X to fp16 would grow
+// with them: so the a X term takes X in fp32 (G itself in the first step) in
+// all steps but the last two, whose roundings no longer grow by more than a^2
+// (a matrix of rank 16 plus 1 % noise: 0.03 % off instead of 4 %).  In the last
+// two steps it takes the fp16 X that the products take: an error that both
+// terms share is contracted by the polynomial near 1, one of them alone is not.
+//
+// Bound: the tensor cores (three products a step).  A and A^2 are symmetric:
+// only tiles on and above the diagonal are computed, the epilogue writes both
+// halves, which saves a third of the work of a square matrix.
+//
+// Kernel: as the library's GEMM -- one CTA (128 x 128) or a CTA pair (256 x
+// 256) per tile, persistent; warp 8 TMA producer, warp 9 MMA issuer, warps 0-7
+// epilogue (TMEM lanes 32 (w mod 4) .., columns half w / 4), two tiles of TMEM
+// in turn so that an epilogue overlaps the next tile's products.  X as a
+// K x N operand is read N-major from shared memory, X^T X takes both operands
+// so, and nothing is ever transposed in memory.
+#include <math.h>
+
+#include <mutex>
+
+#include "common.h"
+#include "f8.cuh"
+#include "ops.h"
+#include "pipe.cuh"
+#include "tile_order.cuh"
+
+namespace swz {
+namespace ns {
+
+constexpr int BM = 128;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+
+template <int BN, bool PAIR>
+struct Cfg {
+  static constexpr int CG = PAIR ? 2 : 1;
+  static constexpr int KA = BN == 128 ? 2 : 1;         // 64-element atoms of K in a stage
+  static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // = 128 in both shapes
+  static constexpr int OP_BYTES = 128 * 128 * KA;      // an operand's share of a stage
+  static constexpr int STAGE_BYTES = 2 * OP_BYTES;
+  static constexpr int STAGES = 192 * 1024 / STAGE_BYTES;
+  static constexpr int BARS = 2 * STAGES + 5;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BARS * 8 + 16;
+};
+
+// What an epilogue makes of a tile's sums.
+enum Mode : int {
+  kGram = 0,    // A = f * acc, both halves
+  kPoly = 1,    // B = u * A + f * acc, both halves
+  kUpdate = 2,  // X' = a * X + f * acc
+};
+
+// X as the a X term reads it
+enum Source : int { kFromG = 0, kFromF32 = 1, kFromF16 = 2 };
+
+// per matrix of the batch: X = G * p1 * p2 * f, and the first fp16 X is G * p1
+// * p2; a later fp16 X is X times the step's power of two times `up`, a power
+// of two above 1 when |G| is so far below eps that X is tiny (down = 1 / up)
+struct Scale {
+  float p1, p2, f, up, down;
+};
+
+struct Params {
+  int mode;
+  uint32_t a_mn, b_mn;          // operands given K x rows
+  uint32_t tiles_m, tiles_n;    // scheduler grid of one matrix
+  uint32_t per_matrix, units;   // tiles of one matrix (upper triangle when symmetric), of all
+  uint32_t num_kb;              // stages of K
+  uint32_t idesc;
+  int M, N;                     // of the result
+  // results and what they are made of, fp16 with rows ld elements apart (a
+  // multiple of 16) unless said otherwise
+  __half* out;
+  int64_t ld_out, batch_out;
+  const __half* in;             // kPoly: A; kUpdate from fp16: X
+  int64_t ld_in, batch_in;
+  float f, u;                   // factors (see Mode)
+  const Scale* scale;           // of the batch
+  int first;                    // the first step's X
+  int source;                   // kUpdate
+  float a, out_scale;           // kUpdate: X' times out_scale goes to `out`
+  const float* master_in;
+  float* master_out;            // NULL: not kept
+  int64_t ld_master, batch_master;
+  const uint8_t* g;             // the caller's G
+  int64_t ld_g, batch_g;
+  int g_dtype;
+  uint8_t* y;                   // the caller's result in the last step, else NULL
+  int64_t ld_y, batch_y;
+  int y_dtype;
+  unsigned int* status;
+  uint64_t timeout_ns;
+  uint32_t debug_flags;
+};
+
+__device__ __forceinline__ float load_any(const uint8_t* p, int64_t at, int dtype) {
+  if (dtype == SWZ_F32) return __ldg(reinterpret_cast<const float*>(p) + at);
+  if (dtype == SWZ_BF16)
+    return __bfloat162float(__ushort_as_bfloat16(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
+  return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
+}
+__device__ __forceinline__ void store_any(uint8_t* p, int64_t at, float v, int dtype) {
+  if (dtype == SWZ_F32) reinterpret_cast<float*>(p)[at] = v;
+  else if (dtype == SWZ_BF16) reinterpret_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+  else reinterpret_cast<__half*>(p)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// tile t of the upper triangle of a T x T grid, rows first
+__device__ __forceinline__ TileCoord upper_tile(uint32_t t, uint32_t T) {
+  uint32_t i = 0, left = t;
+  while (left >= T - i) {
+    left -= T - i;
+    ++i;
+  }
+  TileCoord c;
+  c.m = i;
+  c.n = i + left;
+  return c;
+}
+
+template <int BN, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                   const __grid_constant__ CUtensorMap tmB, const Params p) {
+  using K_ = Cfg<BN, PAIR>;
+  constexpr int CG = K_::CG, STAGES = K_::STAGES, KA = K_::KA, COLS = BN / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sA = ptx::smem_u32(smem);
+  const uint32_t sB = sA + STAGES * K_::OP_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * K_::STAGE_BYTES);
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + K_::BARS);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&tmA);
+    ptx::prefetch_tensormap(&tmB);
+    for (uint32_t s = 0; s < uint32_t(STAGES); ++s) {
+      ptx::mbar_init(full_bar(s), 1);
+      ptx::mbar_init(empty_bar(s), 1);
+    }
+    for (uint32_t a = 0; a < 2; ++a) {
+      ptx::mbar_init(tfull_bar(a), 1);
+      ptx::mbar_init(tempty_bar(a), kEpiWarps * CG);
+    }
+    ptx::mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kEpiWarps + 1) {
+    ptx::tmem_alloc<CG>(ptx::smem_u32(tmem_slot), 2 * BN);
+    ptx::tmem_relinquish<CG>();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pipe::Ctl ctl;
+  ctl.status = p.status;
+  ctl.abort_flag = abort_flag;
+  ctl.peer_abort = 0;
+  if constexpr (PAIR) ctl.peer_abort = ptx::map_to_rank(ptx::smem_u32(abort_flag), rank ^ 1u);
+  ctl.timeout_ns = p.timeout_ns;
+  const uint32_t w0 = blockIdx.x / CG, P = gridDim.x / CG;
+  const bool sym = p.mode != kUpdate;
+  auto tile_at = [&](uint32_t w, uint32_t& b) -> TileCoord {
+    b = w / p.per_matrix;
+    const uint32_t t = w - b * p.per_matrix;
+    return sym ? upper_tile(t, p.tiles_m) : tile_of(kSerpentine, t, p.tiles_m, p.tiles_n, 8u);
+  };
+  // nothing above touches global memory
+  ptx::grid_dep_wait();
+  if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
+  bool aborted = false;
+
+  if (warp == kEpiWarps) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
+      const uint64_t pol = ptx::l2_policy_evict_last();
+      // 128 rows (or columns, MN-major) of an operand from r0, K elements k0 ..
+      auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t r0, int32_t k0,
+                      int32_t b, bool mn) {
+        if (mn) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if constexpr (PAIR)
+              ptx::tma_load_3d_pair(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
+            else
+              ptx::tma_load_3d(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < KA; ++j) {
+            if constexpr (PAIR)
+              ptx::tma_load_3d_pair(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
+            else
+              ptx::tma_load_3d(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
+          }
+        }
+      };
+      for (uint32_t w = w0; w < p.units && !aborted; w += P) {
+        uint32_t b;
+        const TileCoord t = tile_at(w, b);
+        const int32_t m0 = int32_t((t.m * CG + rank) * BM);
+        const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
+        for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
+          if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) { aborted = true; break; }
+          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
+          if (skip) {
+            skip = false;
+          } else {
+            const uint32_t fb = PAIR ? ptx::map_to_rank(full_bar(stage), 0) : full_bar(stage);
+            const int32_t k0 = int32_t(kb * (64 * KA));
+            load(sA + stage * K_::OP_BYTES, &tmA, fb, m0, k0, int32_t(b), p.a_mn != 0);
+            load(sB + stage * K_::OP_BYTES, &tmB, fb, n0, k0, int32_t(b), p.b_mn != 0);
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      for (int i = 0; i < STAGES && !aborted; ++i) {
+        if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) aborted = true;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+      if (aborted) pipe::spin_ns(50000);
+    }
+    __syncwarp();
+  } else if (warp == kEpiWarps + 1) {
+    // ---------------- MMA issuer (leader CTA) ----------------
+    if (lane == 0 && leader) {
+      uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+      bool issued = false;
+      const uint64_t adesc0 = p.a_mn ? pipe::sdesc128(sA, 64 * KA * 128, 1024)
+                                     : pipe::sdesc128(sA, 16, 1024);
+      const uint64_t bdesc0 = p.b_mn ? pipe::sdesc128(sB, 64 * KA * 128, 1024)
+                                     : pipe::sdesc128(sB, 16, 1024);
+      const bool amn = p.a_mn != 0, bmn = p.b_mn != 0;
+      for (uint32_t w = w0; w < p.units && !aborted; w += P) {
+        if (!pipe::wait(tempty_bar(acc), acc_phase ^ 1u, ctl)) { aborted = true; break; }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem_base + acc * BN;
+#pragma unroll 4
+        for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
+          if (!pipe::wait(full_bar(stage), phase, ctl)) { aborted = true; break; }
+          ptx::tc_fence_after();
+          const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
+          const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
+          // slice kk: 16 elements of K; K-major 32 bytes into atom kk / 4,
+          // MN-major 16 rows of 128 bytes down
+#pragma unroll
+          for (uint32_t kk = 0; kk < uint32_t(4 * KA); ++kk) {
+            const uint32_t km = ((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
+            const uint32_t mn = 128u * kk;
+            ptx::mma<CG, 0>(d, a + (amn ? mn : km), b + (bmn ? mn : km), p.idesc,
+                            kb != 0 || kk != 0);
+          }
+          issued = true;
+          if constexpr (PAIR) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+          else ptx::mma_commit(empty_bar(stage));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (aborted) break;
+        if constexpr (PAIR) ptx::mma_commit_pair(tfull_bar(acc), 0x3);
+        else ptx::mma_commit(tfull_bar(acc));
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (aborted && issued) {
+        if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
+        else ptx::mma_commit(drain_bar);
+        const uint64_t t0 = ptx::global_timer_ns();
+        while (!ptx::mbar_try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue ----------------
+    const uint32_t q = warp & 3u, half = warp >> 2;
+    uint32_t acc = 0, acc_phase = 0;
+    for (uint32_t w = w0; w < p.units; w += P) {
+      uint32_t b;
+      const TileCoord t = tile_at(w, b);
+      const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
+      const int64_t col0 = int64_t(t.n) * BN + half * COLS;
+      const bool row_in = row < p.M;
+      const Scale sc = p.scale[b];
+      const float fx = p.first ? sc.f : sc.down;  // X over the fp16 X's power of two
+      const float f = p.mode == kPoly ? p.f : p.mode == kGram ? p.f * fx * fx : p.f * fx;
+      const float out_scale = p.mode == kUpdate ? p.out_scale * sc.up : 1.f;
+      const bool ok = pipe::wait(tfull_bar(acc), acc_phase, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+      ptx::tc_fence_after();
+      const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc * BN + half * COLS;
+#pragma unroll 1
+      for (int c = 0; c < COLS / 16; ++c) {
+        const int64_t col = col0 + c * 16;
+        if (col >= p.N) break;
+        __syncwarp();
+        uint32_t r[16];
+        pipe::tmem_ld16(taddr + c * 16, r);
+        float v[16];
+        // what the sums are added to, while they load
+        if (p.mode == kGram) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        } else if (!row_in) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        } else if (p.mode == kPoly || p.source == kFromF16) {
+          const float u = p.mode == kPoly ? p.u : p.a * p.u * fx;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.in + b * p.batch_in + row * p.ld_in + col);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = src[h];
+            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&e[j]));
+              v[8 * h + 2 * j] = u * z.x;
+              v[8 * h + 2 * j + 1] = u * z.y;
+            }
+          }
+        } else if (p.source == kFromF32) {
+          const float4* src = reinterpret_cast<const float4*>(p.master_in + b * p.batch_master +
+                                                              row * p.ld_master + col);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const float4 x = src[h];
+            v[4 * h] = p.a * x.x;
+            v[4 * h + 1] = p.a * x.y;
+            v[4 * h + 2] = p.a * x.z;
+            v[4 * h + 3] = p.a * x.w;
+          }
+        } else {
+          const int64_t at = b * p.batch_g + row * p.ld_g + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            v[j] = col + j < p.N
+                       ? p.a * (load_any(p.g, at + j, p.g_dtype) * sc.p1 * sc.p2 * sc.f)
+                       : 0.f;
+        }
+        pipe::tmem_ld_wait16(r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = fmaf(f, __uint_as_float(r[j]), v[j]);
+        if (!row_in) continue;
+        if (p.y) {
+          const int64_t at = b * p.batch_y + row * p.ld_y + col;
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (col + j < p.N) store_any(p.y, at + j, v[j], p.y_dtype);
+          continue;
+        }
+        if (p.master_out) {
+          float4* dst = reinterpret_cast<float4*>(p.master_out + b * p.batch_master +
+                                                  row * p.ld_master + col);
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            dst[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+        }
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = half2_bits(v[2 * j] * out_scale, v[2 * j + 1] * out_scale);
+        __half* out = p.out + b * p.batch_out;
+        pipe::st_global_32b(out + row * p.ld_out + col, o);
+        if (sym && t.m != t.n) {
+          // the other half: lanes are neighbours along its rows
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (col + j < p.N)
+              reinterpret_cast<uint16_t*>(out)[(col + j) * p.ld_out + row] =
+                  uint16_t(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(acc), 0));
+        else ptx::mbar_arrive(tempty_bar(acc));
+      }
+      acc ^= 1u;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (warp == kEpiWarps + 1) ptx::tmem_dealloc<CG>(tmem_base, 2 * BN);
+}
+
+// ---- the norm and the first X ---------------------------------------------------
+// Sum of squares of each matrix in three scales -- as they are, and of the
+// values times 2^-80 and 2^80 -- so that no finite G overflows and none that
+// matters underflows; per CTA in fp32 by thread, then in double, in a fixed
+// order.
+constexpr int kNormThreads = 256;
+
+struct NormArgs {
+  const uint8_t* g;
+  int64_t ld_g, batch_g;
+  int g_dtype, m, n;
+  int wide;              // rows of G start on 16 bytes
+  uint32_t parts;        // CTAs of a matrix
+  double* partial;       // [batch][parts][3]
+  double eps;
+  double headroom;       // |G| / (|G| + eps) below this leaves room to scale X up
+  Scale* scale;
+  __half* x;             // first fp16 X
+  int64_t ld_x, batch_x;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NormArgs p) {
+  __shared__ double red[3][kNormThreads / 32];
+  ptx::grid_dep_wait();
+  if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
+  const uint32_t b = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  const uint32_t chunks = (uint32_t(p.n) + 7u) / 8u;  // of 8 values of a row
+  const uint64_t total = uint64_t(chunks) * uint32_t(p.m);
+  const uint64_t beg = total * part / p.parts, end = total * (part + 1) / p.parts;
+  const uint8_t* g = p.g + b * p.batch_g * T::kBytes;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+  for (uint64_t i = beg + threadIdx.x; i < end; i += kNormThreads) {
+    const uint32_t r = uint32_t(i / chunks), c = uint32_t(i - uint64_t(r) * chunks);
+    uint32_t w[T::kWords];
+    f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes, p.n - int(c * 8), p.wide != 0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = T::value(w, j), lo = v * 0x1p-80f, hi = v * 0x1p80f;
+      s0 = fmaf(v, v, s0);
+      s1 = fmaf(lo, lo, s1);
+      s2 = fmaf(hi, hi, s2);
+    }
+  }
+  double d[3] = {s0, s1, s2};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) d[k] += __shfl_xor_sync(0xFFFFFFFFu, d[k], o);
+    if (threadIdx.x % 32 == 0) red[k][threadIdx.x / 32] = d[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    double v = 0.0;
+    for (int j = 0; j < kNormThreads / 32; ++j) v += red[threadIdx.x][j];
+    p.partial[(uint64_t(b) * p.parts + part) * 3 + threadIdx.x] = v;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) ns_start_kernel(const NormArgs p) {
+  __shared__ Scale sc;
+  ptx::grid_dep_wait();
+  if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
+  const uint32_t b = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  if (threadIdx.x < 32) {
+    double d[3] = {0.0, 0.0, 0.0};
+    for (uint32_t j = threadIdx.x; j < p.parts; j += 32)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) d[k] += p.partial[(uint64_t(b) * p.parts + j) * 3 + k];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) d[k] += __shfl_xor_sync(0xFFFFFFFFu, d[k], o);
+    if (threadIdx.x == 0) {
+      // the scale whose squares neither overflowed nor underflowed
+      double norm;
+      if (!(d[0] < 1e36)) norm = sqrt(d[1]) * 0x1p80;
+      else if (d[0] > 1e-30) norm = sqrt(d[0]);
+      else norm = sqrt(d[2]) * 0x1p-80;
+      const double root = sqrt(double(p.m) * double(p.n));
+      int e = 0;
+      if (norm > 0.0 && norm < 1e300) e = int(floor(log2(root / norm)));
+      const double div = norm + p.eps;
+      sc.p1 = float(exp2(double(e / 2)));
+      sc.p2 = float(exp2(double(e - e / 2)));
+      sc.f = div > 0.0 ? float(exp2(-double(e)) / div) : (div == 0.0 ? 0.f : float(div));
+      // X grows from |G| / (|G| + eps) by known factors, its bound by others
+      const double share = norm / div;
+      int z = 0;
+      if (share > 0.0 && share < p.headroom) z = int(floor(log2(p.headroom / share)));
+      if (z > 126) z = 126;
+      sc.up = float(exp2(double(z)));
+      sc.down = float(exp2(-double(z)));
+      if (part == 0) p.scale[b] = sc;
+    }
+  }
+  __syncthreads();
+  const float p1 = sc.p1, p2 = sc.p2;
+  const uint32_t chunks = (uint32_t(p.n) + 7u) / 8u;
+  const uint64_t total = uint64_t(chunks) * uint32_t(p.m);
+  const uint64_t beg = total * part / p.parts, end = total * (part + 1) / p.parts;
+  const uint8_t* g = p.g + b * p.batch_g * T::kBytes;
+  __half* x = p.x + b * p.batch_x;
+  for (uint64_t i = beg + threadIdx.x; i < end; i += kNormThreads) {
+    const uint32_t r = uint32_t(i / chunks), c = uint32_t(i - uint64_t(r) * chunks);
+    uint32_t w[T::kWords];
+    f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes, p.n - int(c * 8), p.wide != 0, w);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = half2_bits(T::value(w, 2 * j) * p1 * p2, T::value(w, 2 * j + 1) * p1 * p2);
+    *reinterpret_cast<uint4*>(x + int64_t(r) * p.ld_x + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+static uint64_t round_up(uint64_t a, uint64_t b) { return (a + b - 1) / b * b; }
+
+constexpr uint32_t kMaxParts = 128;  // CTAs that share a matrix's norm
+
+struct Layout {
+  int64_t ldx, ldd;                        // elements
+  uint64_t x0, x1, master, a, b, partial, scale, total;  // byte offsets
+};
+
+static Layout layout(uint64_t batch, uint64_t m, uint64_t n) {
+  const uint64_t d = m < n ? m : n;
+  Layout L;
+  L.ldx = int64_t(round_up(n, 16));
+  L.ldd = int64_t(round_up(d, 16));
+  uint64_t at = 0;
+  auto take = [&](uint64_t bytes) {
+    const uint64_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  L.x0 = take(batch * m * L.ldx * 2);
+  L.x1 = take(batch * m * L.ldx * 2);
+  L.master = take(batch * m * L.ldx * 4);
+  L.a = take(batch * d * L.ldd * 2);
+  L.b = take(batch * d * L.ldd * 2);
+  L.partial = take(batch * kMaxParts * 3 * 8);
+  L.scale = take(batch * sizeof(Scale));
+  L.total = at;
+  return L;
+}
+
+// largest |a s + b s^3 + c s^5| on [0, hi]
+static double poly_max(double a, double b, double c, double hi) {
+  auto at = [&](double s) { return fabs(s * (a + s * s * (b + c * s * s))); };
+  double best = at(hi);
+  // where the derivative a + 3 b t + 5 c t^2 vanishes, t = s^2
+  const double disc = 9 * b * b - 20 * a * c;
+  double t[3] = {-1, -1, -1};
+  if (c != 0 && disc >= 0) {
+    t[0] = (-3 * b + sqrt(disc)) / (10 * c);
+    t[1] = (-3 * b - sqrt(disc)) / (10 * c);
+  } else if (c == 0 && b != 0) {
+    t[2] = -a / (3 * b);
+  }
+  for (double x : t)
+    if (x > 0 && x < hi * hi) best = fmax(best, at(sqrt(x)));
+  return best;
+}
+
+// exponent of the largest power of two that keeps values up to `bound` below
+// 2^15 in fp16, between -100 and `most`
+static int room(double bound, int most) {
+  if (!(bound > 0)) return most;
+  const int e = 14 - int(ceil(log2(bound)));
+  return e < -100 ? -100 : e > most ? most : e;
+}
+
+template <int BN, bool PAIR>
+static int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& prm, int num_sms,
+                  cudaStream_t stream) {
+  using K_ = Cfg<BN, PAIR>;
+  auto kern = ns_gemm_kernel<BN, PAIR>;
+  static std::mutex mu;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  SWZ_CUDA_TRY(cudaGetDevice(&dev));
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      SWZ_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        K_::SMEM_BYTES));
+      attr_set[dev] = true;
+    }
+  }
+  const uint32_t cap = uint32_t(num_sms) / K_::CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((prm.units < cap ? prm.units : cap) * K_::CG);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = K_::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = K_::CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, ta, tb, prm));
+  return SWZ_OK;
+}
+
+template <typename T>
+static int launch_norm(const NormArgs& a, uint32_t grid, bool start, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (start) SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, ns_start_kernel<T>, a));
+  else SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, ns_norm_kernel<T>, a));
+  return SWZ_OK;
+}
+
+struct Operand {
+  const __half* p;
+  uint64_t rows, cols;
+  int64_t ld;
+  bool mn;  // given K x rows
+};
+
+// One product: the tile shape by the estimated number of waves, the maps, the launch.
+static int product(const Operand& A, const Operand& B, uint64_t batch, uint64_t K, Params prm,
+                   const DeviceInfo& dev, int tile, cudaStream_t s) {
+  const uint64_t M = uint64_t(prm.M), N = uint64_t(prm.N);
+  const bool sym = prm.mode != kUpdate;
+  auto tiles = [&](uint64_t t) {
+    const uint64_t tm = (M + t - 1) / t, tn = (N + t - 1) / t;
+    return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
+  };
+  // in units of the time of a 128-wide tile on one SM: a pair's tile takes
+  // twice that
+  const uint64_t t128 = (tiles(128) + dev.num_sms - 1) / dev.num_sms;
+  const uint64_t t256 = (tiles(256) + dev.num_sms / 2 - 1) / (dev.num_sms / 2) * 2;
+  const bool pair = tile ? tile == 256 : t256 <= t128;
+  const uint64_t bn = pair ? 256 : 128;
+  const int ka = pair ? 1 : 2;
+  CUtensorMap map[2];
+  const Operand* ops[2] = {&A, &B};
+  for (int i = 0; i < 2; ++i) {
+    const Operand& o = *ops[i];
+    const int rc = encode_half(&map[i], o.p, batch, o.rows, o.cols, uint64_t(o.ld),
+                               o.rows * uint64_t(o.ld), 64, o.mn ? 64u * ka : 128u, true);
+    if (rc != SWZ_OK) return rc;
+  }
+  const uint64_t units = tiles(bn);
+  if (units > uint64_t(INT32_MAX)) return SWZ_EINVAL;
+  prm.tiles_m = uint32_t((M + bn - 1) / bn);
+  prm.tiles_n = uint32_t((N + bn - 1) / bn);
+  prm.units = uint32_t(units);
+  prm.per_matrix = uint32_t(units / batch);
+  prm.num_kb = uint32_t((K + 64 * ka - 1) / (64 * ka));
+  prm.a_mn = A.mn;
+  prm.b_mn = B.mn;
+  prm.idesc = pipe::idesc(0, 0, A.mn, B.mn, int(bn), int(bn));
+  return pair ? launch<256, true>(map[0], map[1], prm, dev.num_sms, s)
+              : launch<128, false>(map[0], map[1], prm, dev.num_sms, s);
+}
+
+}  // namespace ns
+}  // namespace swz
+
+using namespace swz;
+using namespace swz::ns;
+
+static bool sizes_ok(int batch, int m, int n) {
+  return batch >= 0 && m >= 0 && n >= 0 && int64_t(m) * n <= (int64_t(1) << 31) && batch <= 65535;
+}
+
+extern "C" int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes) {
+  if (!h_bytes || !sizes_ok(batch, m, n)) return SWZ_EINVAL;
+  *h_bytes = batch && m && n ? layout(uint64_t(batch), uint64_t(m), uint64_t(n)).total : 0;
+  return SWZ_OK;
+}
+
+extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t batch_stride_g,
+                                 void* Y, int y_dtype, int64_t ldy, int64_t batch_stride_y,
+                                 int batch, int m, int n, int steps, double a, double b, double c,
+                                 double eps, const swz_newton_schulz_opts* opts, void* d_workspace,
+                                 uint64_t workspace_bytes, void* stream) {
+  swz_newton_schulz_opts o = {};
+  if (opts) o = *opts;
+  if (!sizes_ok(batch, m, n) || steps < 1 || steps > 64) return SWZ_EINVAL;
+  for (int d : {dtype, y_dtype})
+    if (d != SWZ_F16 && d != SWZ_BF16 && d != SWZ_F32) return SWZ_EINVAL;
+  if (!(eps >= 0.0) || !isfinite(eps) || !isfinite(a) || !isfinite(b) || !isfinite(c))
+    return SWZ_EINVAL;
+  if (o.tile != 0 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
+  if (batch == 0 || m == 0 || n == 0) return SWZ_OK;
+  const int64_t gs = dtype == SWZ_F32 ? 4 : 2, ys = y_dtype == SWZ_F32 ? 4 : 2;
+  const uintptr_t ga = reinterpret_cast<uintptr_t>(G);
+  if (!G || ga % uintptr_t(gs) != 0 || (m > 1 && ldg < n) ||
+      (batch > 1 && batch_stride_g < (m - 1) * ldg + n))
+    return SWZ_EINVAL;
+  if (!Y || reinterpret_cast<uintptr_t>(Y) % uintptr_t(ys) != 0 || (m > 1 && ldy < n) ||
+      (batch > 1 && batch_stride_y < (m - 1) * ldy + n))
+    return SWZ_EINVAL;
+  // the range of singular values, step by step, gives the powers of two
+  // and how far below them X can stay: hi over the largest growth, in all steps
+  double hi[65], grown = 1.0, headroom = 1.0;
+  hi[0] = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    hi[i + 1] = 1.01 * poly_max(a, b, c, hi[i]);
+    if (!(hi[i + 1] < 1e15)) return SWZ_EUNSUPPORTED;
+    const double h2 = hi[i] * hi[i], mid = c != 0 ? -b / (2 * c) : -1.0;
+    double g = fmax(fabs(a), fabs(a + h2 * (b + c * h2)));
+    if (mid > 0 && mid < h2) g = fmax(g, fabs(a + mid * (b + c * mid)));
+    grown *= 1.01 * g;
+    if (grown > 0) headroom = fmin(headroom, hi[i + 1] / grown);
+  }
+  const Layout L = layout(uint64_t(batch), uint64_t(m), uint64_t(n));
+  const uintptr_t wsa = reinterpret_cast<uintptr_t>(d_workspace);
+  if (!wsa || (wsa & 255u) || workspace_bytes < L.total) return SWZ_EINVAL;
+  DeviceInfo dev{};
+  int rc = current_device(&dev);
+  if (rc != SWZ_OK) return rc;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  const bool wide = m <= n;
+  const uint64_t d = uint64_t(wide ? m : n);
+
+  NormArgs na{};
+  na.g = static_cast<const uint8_t*>(G);
+  na.ld_g = m > 1 ? ldg : n;
+  na.batch_g = batch > 1 ? batch_stride_g : 0;
+  na.g_dtype = dtype;
+  na.m = m;
+  na.n = n;
+  na.wide = ga % 16 == 0 && (m == 1 || (na.ld_g * gs) % 16 == 0) &&
+            (batch == 1 || (na.batch_g * gs) % 16 == 0);
+  // at least 1024 chunks of 8 values a CTA, and no more CTAs than fill the GPU
+  const uint64_t chunks = (uint64_t(n) + 7) / 8 * uint64_t(m);
+  uint64_t parts = (chunks + 1023) / 1024;
+  const uint64_t fill = (uint64_t(dev.num_sms) * 4 + batch - 1) / batch;
+  if (parts > fill) parts = fill;
+  if (parts > kMaxParts) parts = kMaxParts;
+  na.parts = uint32_t(parts);
+  na.partial = reinterpret_cast<double*>(ws + L.partial);
+  na.eps = eps;
+  na.headroom = headroom;
+  na.scale = reinterpret_cast<Scale*>(ws + L.scale);
+  na.x = reinterpret_cast<__half*>(ws + L.x0);
+  na.ld_x = L.ldx;
+  na.batch_x = int64_t(m) * L.ldx;
+  const uint32_t grid = uint32_t(parts) * uint32_t(batch);
+  for (int start = 0; start < 2; ++start) {
+    if (dtype == SWZ_BF16) rc = launch_norm<f8::Bf16>(na, grid, start != 0, s);
+    else if (dtype == SWZ_F16) rc = launch_norm<f8::F16>(na, grid, start != 0, s);
+    else rc = launch_norm<f8::F32>(na, grid, start != 0, s);
+    if (rc != SWZ_OK) return rc;
+  }
+
+  Params base{};
+  base.g = na.g;
+  base.ld_g = na.ld_g;
+  base.batch_g = na.batch_g;
+  base.g_dtype = dtype;
+  base.ld_master = L.ldx;
+  base.batch_master = int64_t(m) * L.ldx;
+  base.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  base.debug_flags = o.debug_flags;
+  base.scale = na.scale;
+  rc = op_status_word(&base.status);
+  if (rc != SWZ_OK) return rc;
+  __half* const xs[2] = {reinterpret_cast<__half*>(ws + L.x0),
+                         reinterpret_cast<__half*>(ws + L.x1)};
+  __half* const Am = reinterpret_cast<__half*>(ws + L.a);
+  __half* const Bm = reinterpret_cast<__half*>(ws + L.b);
+  float* const master = reinterpret_cast<float*>(ws + L.master);
+  // steps that take the a X term in fp32 (the first takes G itself in any case)
+  const int masters = steps - 2;
+  int ex = 0;                     // the fp16 X is X * 2^ex (after the first step)
+  for (int i = 0; i < steps; ++i) {
+    __half* const x = xs[i & 1];
+    const Operand xk{x, uint64_t(m), uint64_t(n), L.ldx, false};   // rows of X along K
+    const Operand xm{x, uint64_t(m), uint64_t(n), L.ldx, true};
+    const Operand ak{Am, d, d, L.ldd, false}, bk{Bm, d, d, L.ldd, false};
+    const double h2 = hi[i] * hi[i] * 1.01;
+    const int ea = room(h2, 14);
+    // largest |b t + c t^2| on [0, h2]
+    double bmax = fabs(h2 * (b + c * h2));
+    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < h2) bmax = fmax(bmax, b * b / (4 * fabs(c)));
+    const int eb = room(1.01 * bmax, 14);
+
+    Params p = base;
+    p.mode = kGram;
+    p.M = p.N = int(d);
+    p.out = Am;
+    p.ld_out = L.ldd;
+    p.batch_out = int64_t(d) * L.ldd;
+    p.first = i == 0;
+    p.f = float(exp2(double(ea - (i == 0 ? 0 : 2 * ex))));
+    rc = wide ? product(xk, xk, uint64_t(batch), uint64_t(n), p, dev, o.tile, s)
+              : product(xm, xm, uint64_t(batch), uint64_t(m), p, dev, o.tile, s);
+    if (rc != SWZ_OK) return rc;
+
+    p = base;
+    p.debug_flags = 0;
+    p.mode = kPoly;
+    p.M = p.N = int(d);
+    p.in = Am;
+    p.ld_in = L.ldd;
+    p.batch_in = int64_t(d) * L.ldd;
+    p.out = Bm;
+    p.ld_out = L.ldd;
+    p.batch_out = int64_t(d) * L.ldd;
+    p.u = float(b * exp2(double(eb - ea)));
+    p.f = float(c * exp2(double(eb - 2 * ea)));
+    rc = product(ak, ak, uint64_t(batch), d, p, dev, o.tile, s);
+    if (rc != SWZ_OK) return rc;
+
+    p = base;
+    p.debug_flags = 0;
+    p.mode = kUpdate;
+    p.M = m;
+    p.N = n;
+    p.first = i == 0;
+    p.a = float(a);
+    p.u = float(exp2(-double(ex)));
+    p.f = float(exp2(-double(eb) - (i == 0 ? 0.0 : double(ex))));
+    p.source = i == 0 ? kFromG : i < masters ? kFromF32 : kFromF16;
+    p.in = x;
+    p.ld_in = L.ldx;
+    p.batch_in = int64_t(m) * L.ldx;
+    p.master_in = master;
+    if (i == steps - 1) {
+      p.y = static_cast<uint8_t*>(Y);
+      p.ld_y = m > 1 ? ldy : n;
+      p.batch_y = batch > 1 ? batch_stride_y : 0;
+      p.y_dtype = y_dtype;
+    } else {
+      ex = room(hi[i + 1] * 1.01, 12);
+      p.out = xs[(i + 1) & 1];
+      p.ld_out = L.ldx;
+      p.batch_out = int64_t(m) * L.ldx;
+      p.out_scale = float(exp2(double(ex)));
+      p.master_out = i + 1 < masters ? master : nullptr;
+    }
+    rc = wide ? product(bk, xm, uint64_t(batch), d, p, dev, o.tile, s)
+              : product(xk, bk, uint64_t(batch), d, p, dev, o.tile, s);
+    if (rc != SWZ_OK) return rc;
+  }
+  return SWZ_OK;
+}

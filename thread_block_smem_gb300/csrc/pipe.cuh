@@ -21,14 +21,14 @@ struct Ctl {
   uint64_t timeout_ns;
 };
 
-__device__ __noinline__ void raise_abort(const Ctl& c) {
+static __device__ __noinline__ void raise_abort(const Ctl& c) {
   atomicCAS(c.status, 0u, 1u);
   *c.abort_flag = 1;
   if (c.peer_abort)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
 }
 
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
   const uint64_t t0 = ptx::global_timer_ns();
   for (uint32_t n = 1;; ++n) {
     if (ptx::mbar_try_wait(bar, parity)) return true;

@@ -35,6 +35,11 @@ class swz_gemm_fp8_opts(ctypes.Structure):
                 ("debug_flags", ctypes.c_uint32), ("timeout_ms", ctypes.c_uint32)]
 
 
+class swz_newton_schulz_opts(ctypes.Structure):
+    _fields_ = [("tile", ctypes.c_int), ("debug_flags", ctypes.c_uint32),
+                ("timeout_ms", ctypes.c_uint32)]
+
+
 def declare(L):
     """Argument types of this module's entry points on the loaded library."""
     i, i64, u64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_void_p
@@ -43,6 +48,10 @@ def declare(L):
     L.swz_gemm_fp8.argtypes = [mat, mat, vp, i64, i, i, i, i, ctypes.POINTER(swz_gemm_fp8_opts), vp]
     L.swz_linear_fp8.argtypes = [vp, i, i64, mat, vp, i64, i, i, i, i, vp, u64, vp]
     L.swz_linear_fp8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
+    f = ctypes.c_double
+    L.swz_newton_schulz.argtypes = [vp, i, i64, i64, vp, i, i64, i64, i, i, i, i, f, f, f, f,
+                                    ctypes.POINTER(swz_newton_schulz_opts), vp, u64, vp]
+    L.swz_newton_schulz_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
 
 
 # ---- raw mirrors ----------------------------------------------------------------
@@ -66,6 +75,20 @@ def swz_linear_fp8(x, dtype, ldx, W, y, ldy, y_dtype, M, N, K, workspace, worksp
 def swz_linear_fp8_workspace_size(M, N, K):
     b = ctypes.c_uint64(0)
     rc = _swz.lib().swz_linear_fp8_workspace_size(M, N, K, ctypes.byref(b))
+    return rc, b.value
+
+
+def swz_newton_schulz(G, dtype, ldg, batch_stride_g, Y, y_dtype, ldy, batch_stride_y, batch, m, n,
+                      steps, a, b, c, eps, opts, workspace, workspace_bytes, stream=0):
+    return _swz.lib().swz_newton_schulz(
+        G, dtype, ldg, batch_stride_g, Y, y_dtype, ldy, batch_stride_y, batch, m, n, steps, a, b,
+        c, eps, ctypes.byref(opts) if opts is not None else None, workspace, workspace_bytes,
+        stream)
+
+
+def swz_newton_schulz_workspace_size(batch, m, n):
+    b = ctypes.c_uint64(0)
+    rc = _swz.lib().swz_newton_schulz_workspace_size(batch, m, n, ctypes.byref(b))
     return rc, b.value
 
 
@@ -307,3 +330,44 @@ def fp8_linear(x, w):
         _function = Fp8Linear
     flat = x.reshape(-1, x.shape[-1])
     return _function.apply(flat, w).reshape(*x.shape[:-1], w.shape[0])
+
+
+def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, *, out=None,
+                  out_dtype=None, tile=0, debug_flags=0, timeout_ms=0, stream=None):
+    """The orthogonalised update of G (m x n, or a stack batch x m x n; fp16,
+    bf16 or fp32, contiguous rows): X = G / (|G|_F + eps), then ``steps`` times
+    X = a X + (b A + c A^2) X with A = X X^T (on the right with X^T X when m >
+    n), ``coefficients`` = (a, b, c).  ``out`` (G's shape; may be G) or
+    ``out_dtype`` (default bf16)."""
+    import torch
+    if G.dim() not in (2, 3):
+        raise ValueError("G: 2-D or 3-D tensor expected")
+    code = _code(G.dtype, "G")
+    if out is None:
+        ycode = _code(out_dtype or torch.bfloat16, "out_dtype")
+        with _on(stream):
+            out = torch.empty(G.shape, dtype=out_dtype or torch.bfloat16, device=G.device)
+    else:
+        ycode = _code(out.dtype, "out")
+        if out.shape != G.shape:
+            raise ValueError(f"out: shape {tuple(G.shape)} expected")
+    g, y = (t if t.dim() == 3 else t.unsqueeze(0) for t in (G, out))
+    batch, m, n = g.shape
+    ld = []
+    for t, what in ((g, "G"), (y, "out")):
+        if not t.is_cuda:
+            raise ValueError(f"{what}: CUDA tensor expected")
+        sb, sm, sn = t.stride()
+        if (n > 1 and sn != 1) or (m > 1 and sm < n) or (batch > 1 and sb < (m - 1) * sm + n):
+            raise ValueError(f"{what}: contiguous rows that do not overlap expected")
+        ld.append((sm if m > 1 else max(n, 1), sb if batch > 1 else 0))
+    a, b, c = coefficients
+    rc, need = swz_newton_schulz_workspace_size(batch, m, n)
+    _swz._check(rc, "swz_newton_schulz_workspace_size")
+    with _on(stream):
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=G.device)
+    opts = swz_newton_schulz_opts(tile, debug_flags, timeout_ms)
+    _swz._check(swz_newton_schulz(g.data_ptr(), code, *ld[0], y.data_ptr(), ycode, *ld[1], batch, m,
+                                  n, steps, a, b, c, eps, opts, ws.data_ptr(), need,
+                                  _swz._stream(stream)), "swz_newton_schulz")
+    return out
