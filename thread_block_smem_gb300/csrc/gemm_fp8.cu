@@ -9,9 +9,15 @@
 // exactly scaled operands in fp32; the sum of a block is scaled and added to
 // fp32 accumulators in registers.  So every block of K is an MMA accumulation
 // of its own, and its tile is read back from TMEM, multiplied and added.
-//   * 320 threads, one CTA per SM.  Warps 0-7: the sums (warp w: TMEM lanes
-//     32 (w mod 4) .., columns half w / 4 of the tile), warp 8: TMA producer,
-//     warp 9: TMEM allocation and (one lane) MMA issue.
+//   * One CTA per SM.  BN / 16 summing warps (warp w: TMEM lanes 32 (w mod 4)
+//     .., columns 64 (w / 4) .. of the tile), then a TMA producer, a warp for
+//     TMEM allocation and (one lane) MMA issue, and one for the scales.  Half
+//     the summing warps with 128 columns each could not hide TMEM's latency:
+//     @@
+//   * The scales go through a ring of shared memory of their own, 12 blocks
+//     deep: loaded by the summing warps themselves, two blocks ahead,
+//     each block cost an L2 round trip (876 SM cycles for a 128 x 128 tile
+//     whose MMAs take 256).  4-byte copies: rows of scales start anywhere.
 //   * TMEM holds 512 / BN tiles in turn, so the tensor core runs ahead of the
 //     readers; a stage of shared memory is one block of K (128 bytes a row).
 //   * CTA pair (256 x 256): each CTA loads its 128 rows of A and half of B
@@ -32,8 +38,15 @@ namespace swz {
 namespace gemm8 {
 
 constexpr int BM = 128, BK = 128;
-constexpr int kMathWarps = 8;
-constexpr int kThreads = (kMathWarps + 2) * 32;
+constexpr int kMath = 8;       // summing warps
+constexpr int kIssuers = 2;    // warps that issue MMAs, a block of K each in turn
+constexpr int kThreads = (kMath + 2 + kIssuers) * 32;
+// Registers of the pair's kernel: 384 threads are launched with 168 each,
+// 64512 in all; the four warps that only issue copies and MMAs give some up
+// for the summing warps (128 sums and 64 columns in flight): 256 * 208 + 128 *
+// 88 = 64512.
+constexpr int kMathRegs = 208, kIssueRegs = 88;
+constexpr int kScaleKb = 4;    // blocks of K whose scales share a slot of the ring
 
 template <int BN, bool PAIR>
 struct Cfg {
@@ -41,12 +54,14 @@ struct Cfg {
   static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // rows of B this CTA loads
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN_LOCAL * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = PAIR && BN == 128 ? 8 : 6;
   static constexpr int NBUF = 512 / BN;
-  static constexpr int COLS = BN / 2;  // columns a warp sums
-  static constexpr int SB_BYTES = kMathWarps * 2 * COLS * 4;  // scales of B by column
-  static constexpr int BARS = 2 * STAGES + 2 * NBUF + 1;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + SB_BYTES + BARS * 8 + 16;
+  static constexpr int COLS = 4 * BN / kMath;     // columns a summing warp holds
+  static constexpr int SLOTS = 3;         // ring of scales: 128 of A's rows, then B's,
+  static constexpr int SLOT = BM + BN;    // floats, of kScaleKb blocks
+  static constexpr int BARS = 2 * STAGES + 2 * NBUF + 2 * SLOTS + kIssuers;
+  static constexpr int SMEM_BYTES =
+      1024 + STAGES * STAGE_BYTES + SLOTS * kScaleKb * SLOT * 4 + BARS * 8 + 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
   static_assert(STAGES * STAGE_BYTES >= BM * BN * 4 || PAIR, "a partial tile fits the ring");
 };
@@ -127,23 +142,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmB, const Params p) {
   using K_ = Cfg<BN, PAIR>;
   constexpr int CG = K_::CG, STAGES = K_::STAGES, NBUF = K_::NBUF, COLS = K_::COLS;
+  constexpr uint32_t SLOTS = K_::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sA = ptx::smem_u32(smem);
   const uint32_t sB = sA + STAGES * K_::A_BYTES;
-  float* sb_cols = reinterpret_cast<float*>(smem + STAGES * K_::STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * K_::STAGE_BYTES + K_::SB_BYTES);
+  float* const ring = reinterpret_cast<float*>(smem + STAGES * K_::STAGE_BYTES);
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(smem + STAGES * K_::STAGE_BYTES +
+                                  SLOTS * kScaleKb * K_::SLOT * 4);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + a); };
   auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * STAGES + NBUF + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
+  auto sfull_bar = [&](uint32_t i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + i); };
+  auto sempty_bar = [&](uint32_t i) { return bar0 + 8u * (2 * STAGES + 2 * NBUF + SLOTS + i); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF + 2 * SLOTS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + K_::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0);  // known uniform
+  const uint32_t lane = threadIdx.x % 32;
   // rank: of a pair, which 128 rows of the tile; of a split, which range of K
   const uint32_t crank = (PAIR || p.split > 1) ? ptx::cluster_ctarank() : 0u;
   const uint32_t rank = PAIR ? crank : 0u;
@@ -158,13 +179,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (uint32_t a = 0; a < uint32_t(NBUF); ++a) {
       ptx::mbar_init(tfull_bar(a), 1);
-      ptx::mbar_init(tempty_bar(a), kMathWarps * CG);
+      ptx::mbar_init(tempty_bar(a), kMath * CG);
     }
-    ptx::mbar_init(drain_bar, 1);
+    for (uint32_t i = 0; i < SLOTS; ++i) {
+      ptx::mbar_init(sfull_bar(i), 32);
+      ptx::mbar_init(sempty_bar(i), kMath);
+    }
+    for (int i = 0; i < kIssuers; ++i) ptx::mbar_init(drain_bar + 8u * i, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == kMathWarps + 1) {
+  if (warp == kMath + 1) {
     ptx::tmem_alloc<CG>(ptx::smem_u32(tmem_slot), 512);
     ptx::tmem_relinquish<CG>();
   }
@@ -194,171 +219,252 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
   bool aborted = false;
 
-  if (warp == kMathWarps) {
+  if (warp >= kMath) {
+   if constexpr (PAIR && BN == 256) pipe::regs_dec<kIssueRegs>();
+   if (warp == kMath) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
-      const uint64_t pol = ptx::l2_policy_evict_last();
-      for (uint32_t w = w0; w < units && !aborted; w += P) {
-        const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
-        const int32_t m0 = int32_t((t.m * CG + rank) * BM);
-        const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
-        for (uint32_t kb = kb0; kb < kb1; ++kb) {
-          if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) { aborted = true; break; }
+    uint32_t stage = 0, phase = 0;
+    bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
+    const uint64_t pol = ptx::l2_policy_evict_last();
+    const uint32_t full0 = PAIR ? ptx::map_to_rank(full_bar(0), 0) : full_bar(0);
+    for (uint32_t w = w0; w < units && !aborted; w += P) {
+      const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
+      const int32_t m0 = int32_t((t.m * CG + rank) * BM);
+      const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
+      for (uint32_t kb = kb0; kb < kb1; ++kb) {
+        const bool ok = pipe::wait(empty_bar(stage), phase ^ 1u, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+        if (pipe::elect_one()) {
           if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
-          const int32_t k0 = int32_t(kb * BK);
-          const uint32_t a_dst = sA + stage * K_::A_BYTES, b_dst = sB + stage * K_::B_BYTES;
-          if (skip) {
-            skip = false;
-          } else if constexpr (PAIR) {
-            const uint32_t fb = ptx::map_to_rank(full_bar(stage), 0);
-            ptx::tma_load_2d_pair(a_dst, &tmA, fb, k0, m0, pol);
-            ptx::tma_load_2d_pair(b_dst, &tmB, fb, k0, n0, pol);
-          } else {
-            ptx::tma_load_2d(a_dst, &tmA, full_bar(stage), k0, m0, pol);
-            ptx::tma_load_2d(b_dst, &tmB, full_bar(stage), k0, n0, pol);
+          if (!skip) {
+            const int32_t k0 = int32_t(kb * BK);
+            const uint32_t a_dst = sA + stage * K_::A_BYTES, b_dst = sB + stage * K_::B_BYTES;
+            if constexpr (PAIR) {
+              ptx::tma_load_2d_pair(a_dst, &tmA, full0 + 8u * stage, k0, m0, pol);
+              ptx::tma_load_2d_pair(b_dst, &tmB, full0 + 8u * stage, k0, n0, pol);
+            } else {
+              ptx::tma_load_2d(a_dst, &tmA, full0 + 8u * stage, k0, m0, pol);
+              ptx::tma_load_2d(b_dst, &tmB, full0 + 8u * stage, k0, n0, pol);
+            }
           }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-      }
-      // every stage released: no commit is in flight towards this CTA
-      for (int i = 0; i < STAGES && !aborted; ++i) {
-        if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) aborted = true;
+        __syncwarp();
+        skip = false;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (aborted) pipe::spin_ns(50000);  // copies already issued land
     }
+    // every stage released: no commit is in flight towards this CTA
+    for (int i = 0; i < STAGES && !aborted; ++i) {
+      const bool ok = pipe::wait(empty_bar(stage), phase ^ 1u, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) aborted = true;
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (aborted) pipe::spin_ns(50000);  // copies already issued land
     __syncwarp();
-  } else if (warp == kMathWarps + 1) {
-    // ---------------- MMA issuer (leader CTA) ----------------
-    if (lane == 0 && leader) {
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
+   } else if (warp <= kMath + kIssuers) {
+    // ---------------- MMA issuers (leader CTA) ----------------
+    // The whole warp runs the loop and one elected lane issues: descriptors
+    // then live in uniform registers.  With the loop inside one lane's branch
+    // every operand of an MMA was moved there first, and the four MMAs of a
+    // block took twice as long to issue as to run.
+    if (leader) {
+      // issuer i takes every kIssuers-th block: each is an accumulation of its
+      // own, so their order does not matter, and the barrier tests and commits
+      // of one pass while the other's MMAs run
+      const uint32_t me = warp - (kMath + 1);
+      uint32_t stage = me, phase = 0, buf = me, buf_phase = 0, turn = me;
       bool issued = false;
       const uint64_t adesc0 = pipe::sdesc128(sA, 16, 1024);
       const uint64_t bdesc0 = pipe::sdesc128(sB, 16, 1024);
       for (uint32_t w = w0; w < units && !aborted; w += P) {
-        for (uint32_t kb = kb0; kb < kb1; ++kb) {
-          if (!pipe::wait(tempty_bar(buf), buf_phase ^ 1u, ctl) ||
-              !pipe::wait(full_bar(stage), phase, ctl)) {
-            aborted = true;
-            break;
-          }
+        uint32_t kb = kb0 + turn;  // the first of this tile's blocks that is mine
+        for (; kb < kb1; kb += kIssuers) {
+          const bool ok = pipe::wait(full_bar(stage), phase, ctl) &&
+                          pipe::wait(tempty_bar(buf), buf_phase ^ 1u, ctl);
+          if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
           ptx::tc_fence_after();
           const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::A_BYTES >> 4));
           const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::B_BYTES >> 4));
           const uint32_t d = tmem_base + buf * BN;
+          if (pipe::elect_one()) {
 #pragma unroll
-          for (uint32_t kk = 0; kk < BK / 32; ++kk)
-            pipe::mma_f8<CG>(d, a + kk * 2, b + kk * 2, p.idesc, kk != 0);
-          issued = true;
-          if constexpr (PAIR) {
-            ptx::mma_commit_pair(empty_bar(stage), 0x3);
-            ptx::mma_commit_pair(tfull_bar(buf), 0x3);
-          } else {
-            ptx::mma_commit(empty_bar(stage));
-            ptx::mma_commit(tfull_bar(buf));
+            for (uint32_t kk = 0; kk < BK / 32; ++kk)
+              pipe::mma_f8<CG>(d, a + kk * 2, b + kk * 2, p.idesc, kk != 0);
+            if constexpr (PAIR) {
+              ptx::mma_commit_pair(tfull_bar(buf), 0x3);
+              ptx::mma_commit_pair(empty_bar(stage), 0x3);
+            } else {
+              ptx::mma_commit(tfull_bar(buf));
+              ptx::mma_commit(empty_bar(stage));
+            }
           }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-          if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+          __syncwarp();
+          issued = true;
+          stage += kIssuers;
+          if (stage >= uint32_t(STAGES)) { stage -= STAGES; phase ^= 1u; }
+          buf += kIssuers;
+          if (buf >= uint32_t(NBUF)) { buf -= NBUF; buf_phase ^= 1u; }
         }
+        turn = kb - kb1;  // blocks of the next tile before mine
       }
       if (aborted && issued) {
-        if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
-        else ptx::mma_commit(drain_bar);
+        // drain: wait (bounded) until every MMA issued so far has completed
+        const uint32_t drain = drain_bar + 8u * me;
+        if (pipe::elect_one()) {
+          if constexpr (PAIR) ptx::mma_commit_pair(drain, 0x1);
+          else ptx::mma_commit(drain);
+        }
         const uint64_t t0 = ptx::global_timer_ns();
-        while (!ptx::mbar_try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
+        while (!pipe::try_wait(drain, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
         }
       }
     }
     __syncwarp();
-  } else if (warp < kMathWarps) {
+   } else {
+    // ---------------- scales ----------------
+    uint32_t slot = 0, phase = 0;
+    const uint32_t ring0 = ptx::smem_u32(ring);
+    for (uint32_t w = w0; w < units && !aborted; w += P) {
+      const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
+      const int64_t m0 = int64_t(t.m * CG + rank) * BM + lane;
+      const int64_t n0 = int64_t(t.n) * BN;
+      for (uint32_t kb = kb0; kb < kb1; kb += kScaleKb) {
+        const bool ok = pipe::wait(sempty_bar(slot), phase ^ 1u, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+#pragma unroll 1
+        for (uint32_t i = 0; i < uint32_t(kScaleKb) && kb + i < kb1; ++i) {
+          const uint32_t dst = ring0 + (slot * kScaleKb + i) * (K_::SLOT * 4) + lane * 4;
+          const float* sa = p.sa + int64_t(kb + i) * p.ldsa;
+#pragma unroll
+          for (int j = 0; j < BM / 32; ++j)
+            pipe::copy4(dst + j * 128, sa + m0 + j * 32, m0 + j * 32 < p.M, p.sa);
+          if constexpr (BROW) {
+            const float* sb = p.sb + int64_t(kb + i) * p.ldsb;
+            const int64_t n = n0 + lane;
+#pragma unroll
+            for (int j = 0; j < BN / 32; ++j)
+              pipe::copy4(dst + (BM + j * 32) * 4, sb + n + j * 32, n + j * 32 < p.N, p.sb);
+          } else if (lane < uint32_t(BN / 128)) {  // the tile's square blocks
+            const int64_t n = n0 + lane * 128;
+            pipe::copy4(dst + BM * 4, p.sb + n / 128 * p.ldsb + kb + i, n < p.N, p.sb);
+          }
+        }
+        pipe::copies_arrive(sfull_bar(slot));
+        if (++slot == SLOTS) { slot = 0; phase ^= 1u; }
+      }
+    }
+    pipe::copies_wait();
+    __syncwarp();
+   }
+  } else {
     // ---------------- sums ----------------
-    const uint32_t q = warp & 3u, half = warp >> 2;
-    uint32_t buf = 0, buf_phase = 0;
-    float* const my_sb = sb_cols + warp * 2 * COLS;
+    if constexpr (PAIR && BN == 256) pipe::regs_inc<kMathRegs>();
+    const uint32_t q = warp & 3u, part = warp >> 2;  // rows 32 q .., columns COLS part ..
+    uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0;
+    const uint32_t tfull0 = tfull_bar(0), sfull0 = sfull_bar(0), sempty0 = sempty_bar(0);
+    const uint32_t tempty0 = PAIR ? ptx::map_to_rank(tempty_bar(0), 0) : tempty_bar(0);
+    const uint32_t taddr0 = tmem_base + ((q * 32u) << 16) + part * COLS;
+    // this thread's row scale, and its warp's scales of B, in the ring's first block
+    const uint32_t sa0 = ptx::smem_u32(ring) + (q * 32 + lane) * 4;
+    const uint32_t sb_off = BROW ? (BM + part * COLS - (q * 32 + lane)) * 4
+                                 : (BM + part * COLS / 128 - (q * 32 + lane)) * 4;
     uint64_t acc[COLS / 2];
+    uint32_t r[2][32];  // the block's columns, as two halves
+    auto add = [&](uint32_t(&d)[32], int c, float s, uint32_t sa) {
+      const uint64_t s2 = pipe::pack2(s, s);
+      if constexpr (BROW) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float b[4];
+          pipe::ld_shared4(sa + sb_off + (c * 32 + 4 * j) * 4, b);
+          uint64_t* a = acc + c * 16 + 2 * j;
+          a[0] = pipe::fma2(pipe::pack2(d[4 * j], d[4 * j + 1]),
+                            pipe::mul2(pipe::pack2(b[0], b[1]), s2), a[0]);
+          a[1] = pipe::fma2(pipe::pack2(d[4 * j + 2], d[4 * j + 3]),
+                            pipe::mul2(pipe::pack2(b[2], b[3]), s2), a[1]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          acc[c * 16 + j] = pipe::fma2(pipe::pack2(d[2 * j], d[2 * j + 1]), s2, acc[c * 16 + j]);
+      }
+    };
+    // scales of the block at `sa`
+    auto scale = [&](uint32_t sa) {
+      float s = pipe::ld_shared(sa);
+      if constexpr (!BROW) s *= pipe::ld_shared(sa + sb_off);
+      return s;
+    };
+    // The scales' slot of the next block, at the start of one.  One vote for
+    // its four blocks: after a wait that ran out the next ones return at once
+    // (the abort flag), and what is summed is not used.
+    auto take_slot = [&]() {
+      const bool ok = pipe::wait(sfull0 + 8u * slot, slot_phase, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok && *ctl.abort_flag == 0)) aborted = true;
+      const uint32_t sa = sa0 + slot * (kScaleKb * K_::SLOT * 4);
+      if (++slot == SLOTS) { slot = 0; slot_phase ^= 1u; }
+      return sa;
+    };
+    auto free_slot = [&]() {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(sempty0 + 8u * (slot == 0 ? SLOTS - 1 : slot - 1));
+    };
+    // both halves are in registers: the tensor core may have the buffer
+    auto landed = [&]() {
+      pipe::tmem_ld_wait32(r[0]);
+      pipe::tmem_ld_wait32(r[1]);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) pipe::arrive_at(tempty0 + 8u * buf);
+        else ptx::mbar_arrive(tempty0 + 8u * buf);
+      }
+      if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+    };
     for (uint32_t w = w0; w < units && !aborted; w += P) {
       const TileCoord t = tile_of(p.order, w, p.sched_m, p.sched_n, p.group);
       const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
-      const int64_t col0 = int64_t(t.n) * BN + half * COLS;
+      const int64_t col0 = int64_t(t.n) * BN + part * COLS;
       const bool row_in = row < p.M;
-      const float* sa = p.sa + row;
-      const float* sb = BROW ? p.sb : p.sb + (col0 / 128 < (p.N + 127) / 128 ? col0 / 128 : 0) * p.ldsb;
-      // scales of a block for this thread's row and (square blocks) for its
-      // columns, loaded two blocks ahead
-      auto load_s = [&](uint32_t kb) -> float2 {
-        if (kb >= kb1) return make_float2(0.f, 0.f);
-        float2 v;
-        v.x = row_in ? __ldg(sa + int64_t(kb) * p.ldsa) : 0.f;
-        v.y = BROW ? 1.f : __ldg(sb + kb);
-        return v;
-      };
-      float sbn[COLS / 32];
-      auto load_sb = [&](uint32_t kb) {
-#pragma unroll
-        for (int j = 0; j < COLS / 32; ++j) {
-          const int64_t n = col0 + j * 32 + lane;
-          sbn[j] = kb < kb1 && n < p.N ? __ldg(sb + int64_t(kb) * p.ldsb + n) : 0.f;
-        }
-      };
-      float2 s_cur = load_s(kb0), s_n1 = load_s(kb0 + 1);
-      if constexpr (BROW) load_sb(kb0);
 #pragma unroll
       for (int j = 0; j < COLS / 2; ++j) acc[j] = 0ull;
+      uint32_t sa = take_slot();
+      pipe::wait(tfull0 + 8u * buf, buf_phase, ctl);
+      __syncwarp();
+      ptx::tc_fence_after();
+      ptx::tmem_ld_32x32b_x32(taddr0 + buf * BN, r[0]);
+      ptx::tmem_ld_32x32b_x32(taddr0 + buf * BN + 32, r[1]);
+      float s = scale(sa);
+      landed();
+      // The next block's barrier is tested and its first half loaded between
+      // the two halves of this one: with a block's wait, loads, release and
+      // 64 FMAs one after the other a warp took 500 cycles for a block, and
+      // twice the warps took as long.
 #pragma unroll 1
-      for (uint32_t kb = kb0; kb < kb1; ++kb) {
-        const float2 s_n2 = load_s(kb + 2);
-        float* const sbuf = my_sb + (kb & 1u) * COLS;
-        if constexpr (BROW) {
-#pragma unroll
-          for (int j = 0; j < COLS / 32; ++j) sbuf[j * 32 + lane] = sbn[j];
-          __syncwarp();
-          load_sb(kb + 1);
-        }
-        const bool ok = pipe::wait(tfull_bar(buf), buf_phase, ctl);
-        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+      for (uint32_t kb = kb0 + 1; kb < kb1 && !aborted; ++kb) {
+        const bool ready = pipe::test_wait(tfull0 + 8u * buf, buf_phase);
+        add(r[0], 0, s, sa);
+        const bool turn = (kb - kb0) % kScaleKb == 0;
+        const uint32_t sa_cur = sa;
+        const float s_cur = s;
+        if (!ready) pipe::wait(tfull0 + 8u * buf, buf_phase, ctl);
+        __syncwarp();
         ptx::tc_fence_after();
-        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + buf * BN + half * COLS;
-        const float s = s_cur.x * s_cur.y;
-        const uint64_t s2 = pipe::pack2(s, s);
-        uint32_t r[2][16];
-        pipe::tmem_ld16(taddr, r[0]);
-        pipe::tmem_ld_wait16(r[0]);
-#pragma unroll
-        for (int c = 0; c < COLS / 16; ++c) {
-          if (c + 1 < COLS / 16) pipe::tmem_ld16(taddr + (c + 1) * 16, r[(c + 1) & 1]);
-          if constexpr (BROW) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 b = *reinterpret_cast<const float4*>(sbuf + c * 16 + 4 * j);
-              acc[c * 8 + 2 * j] =
-                  pipe::fma2(pipe::pack2(r[c & 1][4 * j], r[c & 1][4 * j + 1]),
-                             pipe::mul2(pipe::pack2(b.x, b.y), s2), acc[c * 8 + 2 * j]);
-              acc[c * 8 + 2 * j + 1] =
-                  pipe::fma2(pipe::pack2(r[c & 1][4 * j + 2], r[c & 1][4 * j + 3]),
-                             pipe::mul2(pipe::pack2(b.z, b.w), s2), acc[c * 8 + 2 * j + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[c * 8 + j] = pipe::fma2(pipe::pack2(r[c & 1][2 * j], r[c & 1][2 * j + 1]), s2,
-                                          acc[c * 8 + j]);
-          }
-          if (c + 1 < COLS / 16) pipe::tmem_ld_wait16(r[(c + 1) & 1]);
-          if (c + 2 == COLS / 16) {  // the last columns have been read
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(buf), 0));
-              else ptx::mbar_arrive(tempty_bar(buf));
-            }
-          }
+        ptx::tmem_ld_32x32b_x32(taddr0 + buf * BN, r[0]);
+        add(r[1], 1, s_cur, sa_cur);
+        if (turn) {
+          free_slot();
+          sa = take_slot();
+        } else {
+          sa += K_::SLOT * 4;
         }
-        s_cur = s_n1;
-        s_n1 = s_n2;
-        if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+        ptx::tmem_ld_32x32b_x32(taddr0 + buf * BN + 32, r[1]);
+        s = scale(sa);
+        landed();
       }
+      add(r[0], 0, s, sa);
+      add(r[1], 1, s, sa);
+      free_slot();
       if (aborted) break;
       if (PAIR || p.split == 1) {
         if (row_in) {
@@ -381,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a, b, d, e;
           pipe::unpack2(acc[2 * c], a, b);
           pipe::unpack2(acc[2 * c + 1], d, e);
-          const uint32_t chunk = (half * (COLS / 4) + c) ^ (r & 31u);
+          const uint32_t chunk = (part * (COLS / 4) + c) ^ (r & 31u);
           *reinterpret_cast<float4*>(smem + r * (BN * 4) + chunk * 16) = make_float4(a, b, d, e);
         }
       }
@@ -392,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // add the partial tiles: rank r of S takes rows r * 128 / S .. of the tile
     __syncwarp();
     ptx::cluster_sync();
-    if (warp < kMathWarps && !aborted) {
+    if (warp < kMath && !aborted) {
       const TileCoord t = tile_of(p.order, w0, p.sched_m, p.sched_n, p.group);
       const uint32_t rows = BM / p.split;
-      for (uint32_t i = warp; i < rows; i += kMathWarps) {
+      for (uint32_t i = warp; i < rows; i += kMath) {
         const uint32_t r = crank * rows + i;
         const int64_t row = int64_t(t.m) * BM + r;
         if (row >= p.M) break;
@@ -437,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if constexpr (PAIR) ptx::cluster_sync();
   ptx::tc_fence_after();
-  if (warp == kMathWarps + 1) ptx::tmem_dealloc<CG>(tmem_base, 512);
+  if (warp == kMath + 1) ptx::tmem_dealloc<CG>(tmem_base, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -557,7 +663,7 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
   if (ch.split > kb) return SWZ_EUNSUPPORTED;  // an empty range of K
   const bool pair = ch.tile == 256;
   const uint64_t sm = ceil_div(uint64_t(M), pair ? 256 : 128);
-  const uint64_t sn = ceil_div(uint64_t(N), pair ? 256 : 128);
+  const uint64_t sn = ceil_div(uint64_t(N), 128);
   const uint64_t cl = pair ? 2 : ch.split;
   if (sm * sn * cl > uint64_t(INT32_MAX)) return SWZ_EINVAL;
   if ((o.order == SWZ_MORTON || o.order == SWZ_XOR) &&
@@ -568,7 +674,7 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
   CUtensorMap ta, tb;
   rc = encode_bytes(&ta, A->data, uint64_t(M), uint64_t(K), uint64_t(A->ld), 128);
   if (rc != SWZ_OK) return rc;
-  rc = encode_bytes(&tb, B->data, uint64_t(N), uint64_t(K), uint64_t(B->ld), 128);
+  rc = encode_bytes(&tb, B->data, uint64_t(N), uint64_t(K), uint64_t(B->ld), pair ? 64 : 128);
   if (rc != SWZ_OK) return rc;
 
   Params prm{};
@@ -586,7 +692,7 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
   prm.sched_m = uint32_t(sm);
   prm.sched_n = uint32_t(sn);
   prm.num_kb = kb;
-  prm.idesc = pipe::idesc(A->fmt, B->fmt, false, false, pair ? 256 : 128, pair ? 256 : 128);
+  prm.idesc = pipe::idesc(A->fmt, B->fmt, false, false, pair ? 256 : 128, 128);
   prm.split = ch.split;
   const uintptr_t bits = ca | (M > 1 ? uintptr_t(ld * es) : 0);
   prm.c_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
@@ -602,8 +708,8 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
   }
   const bool brow = B->block == SWZ_BLOCK_ROW;
   if (pair)
-    return brow ? launch<256, true, true>(ta, tb, prm, uint32_t(programs), s)
-                : launch<256, true, false>(ta, tb, prm, uint32_t(programs), s);
+    return brow ? launch<128, true, true>(ta, tb, prm, uint32_t(programs), s)
+                : launch<128, true, false>(ta, tb, prm, uint32_t(programs), s);
   return brow ? launch<128, false, true>(ta, tb, prm, uint32_t(programs), s)
               : launch<128, false, false>(ta, tb, prm, uint32_t(programs), s);
 }

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
         else ptx::mma_commit(drain_bar);
         const uint64_t t0 = ptx::global_timer_ns();
-        while (!ptx::mbar_try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
+        while (!pipe::try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
         }
       }
     }
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty_bar(acc), 0));
+        if constexpr (PAIR) pipe::arrive_at(ptx::map_to_rank(tempty_bar(acc), 0));
         else ptx::mbar_arrive(tempty_bar(acc));
       }
       acc ^= 1u;

@@ -14,6 +14,46 @@
 namespace swz {
 namespace pipe {
 
+// Barrier waits and arrivals at CTA scope.  What they order is TMEM and the
+// copies' shared memory, which tcgen05's fences and the barriers' own
+// transaction counts cover; at cluster scope every arrival is a memory fence
+// and every wait drops the L1, which cost a CTA pair that exchanges one tile
+// of TMEM per block of K half of its time (8192^3 in 8 bits: 1018 to 494 us).
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+// True in one lane of the (converged) warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 struct Ctl {
   unsigned int* status;      // device status word
   volatile int* abort_flag;  // this CTA's, in shared memory
@@ -21,32 +61,32 @@ struct Ctl {
   uint64_t timeout_ns;
 };
 
-static __device__ __noinline__ void raise_abort(const Ctl& c) {
+__device__ __forceinline__ void raise_abort(const Ctl& c) {
   atomicCAS(c.status, 0u, 1u);
   *c.abort_flag = 1;
   if (c.peer_abort)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
 }
 
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, const Ctl& c) {
-  const uint64_t t0 = ptx::global_timer_ns();
+// Waits for the phase of `bar` with parity `parity`; false if the kernel is
+// aborting or the bound expired (then the abort is raised).  The timer is not
+// read until the hardware's own suspended tries have failed 64 times.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
+  if (test_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+#pragma unroll 1
   for (uint32_t n = 1;; ++n) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((n & 31u) == 0) {
+    if (try_wait(bar, parity)) return true;
+    if ((n & 63u) == 0) {
       if (*c.abort_flag) return false;
-      if (ptx::global_timer_ns() - t0 > c.timeout_ns) {
+      const uint64_t t = ptx::global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > c.timeout_ns) {
         raise_abort(c);
         return false;
       }
     }
   }
-}
-
-// Waits for the phase of `bar` with parity `parity`; false if the kernel is
-// aborting or the bound expired (then the abort is raised).
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Ctl& c) {
-  if (ptx::mbar_test_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, c);
 }
 
 __device__ __forceinline__ void spin_ns(uint64_t ns) {
@@ -111,6 +151,16 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
 // Two fp32 values in a 64-bit register, multiplied and added in one
 // instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -135,6 +185,43 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// This warpgroup's registers per thread, out of what the block was launched
+// with (all four warps execute the same one, each in its role's branch: where
+// the branches meet again the compiler keeps to the smaller number).
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Asynchronous copy of one float to shared memory, zero when !in (`any`: a
+// valid address, not read then); copies_arrive arrives on `bar` (one of 32
+// lanes) when this thread's copies so far have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool in, const float* any) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(in ? src : any),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ld_shared4(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // 32 bytes to a 32-byte aligned global address in one instruction.
