@@ -528,9 +528,11 @@ int swz_quantize_fp8(const void* x, int dtype, int64_t ldx, int M, int K, int bl
 typedef struct swz_gemm_fp8_opts {
   int order, group;     /* tile order as in swz_gemm                          */
   int tile;             /* 0 automatic; 128: one CTA, 128 x 128 of C; 256: CTA
-                           pair, 256 x 256                                    */
-  int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share a
-                           128 x 128 tile's K and add their sums in order     */
+                           pair, 256 x 128.  Automatic with up to 32 rows: 128
+                           columns of C and all its rows                      */
+  int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share the
+                           K of a tile that is not a pair's and add their sums
+                           in order                                           */
   int num_programs;     /* tile 128 or 256 without a split: CTAs to launch (a
                            multiple of 2 for 256); 0 = one per SM             */
   uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                       */
@@ -556,10 +558,9 @@ int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int6
 /*
  * swz_linear_fp8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is
  * quantised in row blocks (e4m3) and multiplied by W (N x K) as in
- * swz_gemm_fp8.  Up to 16 rows one kernel reads W once and quantises x on the
- * way; more rows go through d_workspace (16-byte aligned, at least
- * swz_linear_fp8_workspace_size bytes; contents free before and after; NULL
- * when the size is 0).  Errors: as swz_gemm_fp8.
+ * swz_gemm_fp8.  d_workspace: 16-byte aligned device scratch of at least
+ * swz_linear_fp8_workspace_size bytes, contents free before and after; NULL
+ * when the size is 0.  Errors: as swz_gemm_fp8.
  */
 int swz_linear_fp8(const void* x, int dtype, int64_t ldx, const swz_fp8_matrix* W, void* y,
                    int64_t ldy, int y_dtype, int M, int N, int K, void* d_workspace,

@@ -131,6 +131,8 @@ def test_quantize_zeros_tiny_and_not_finite(swz, dtype):
     (77, 200, 2048, dict(tile=128, split_k=8)), (200, 140, 1100, dict(tile=128, split_k=4)),
     (129, 300, 333, dict(tile=128, split_k=2)), (513, 1111, 600, {}),
     (700, 900, 384, dict(tile=256, num_programs=4)), (700, 900, 384, dict(tile=128, num_programs=5)),
+    (1, 300, 200, {}), (16, 129, 2000, {}), (17, 1000, 1100, {}), (33, 500, 5000, {}), (64, 257, 640, {}),
+    (5, 200, 1100, dict(split_k=8)), (40, 4100, 300, dict(split_k=1)), (64, 64, 3000, dict(split_k=4)),
 ])
 def test_gemm_fp8(swz, M, N, K, cfg, b_block):
     a, b = rand((M, K), torch.float32, M + K).cuda(), rand((N, K), torch.float32, N + 7).cuda()
@@ -208,7 +210,7 @@ def test_gemm_fp8_padding_is_not_read(swz):
 @pytest.mark.parametrize("w_block,fmt", [("square", "e4m3"), ("row", "e4m3"), ("square", "e5m2")])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 64, 128), (1, 4096, 4096), (3, 100, 77),
                                    (8, 1000, 1999), (9, 130, 5000), (16, 515, 640), (17, 515, 640),
-                                   (100, 300, 1000)])
+                                   (100, 300, 1000), (2, 700, 9000), (16, 40, 14000), (5, 5000, 300)])
 def test_linear_fp8(swz, M, N, K, w_block, fmt):
     for dtype, out in ((torch.bfloat16, None), (torch.float16, torch.float32),
                        (torch.float32, torch.bfloat16)):
@@ -305,6 +307,15 @@ def test_timeout_is_reported(swz):
     (qa, sa) = swz.quantize_fp8(rand((300, 512), torch.bfloat16, 1).cuda())
     (qb, sb) = swz.quantize_fp8(rand((300, 512), torch.bfloat16, 2).cuda(), "square")
     want = swz.gemm_fp8(qa, sa, qb, sb)
+    few = swz.quantize_fp8(rand((9, 512), torch.bfloat16, 3).cuda())
+    for split in (1, 2):
+        want_few = swz.gemm_fp8(*few, qb, sb, split_k=split)
+        swz.gemm_fp8(*few, qb, sb, split_k=split, debug_flags=swz.SWZ_DEBUG_SKIP_FIRST_LOAD,
+                     timeout_ms=50)
+        with pytest.raises(swz.SwzError) as e:
+            swz.check_status()
+        assert e.value.code == swz.SWZ_ETIMEOUT
+        assert torch.equal(swz.gemm_fp8(*few, qb, sb, split_k=split), want_few)
     for cfg in (dict(tile=128), dict(tile=256), dict(tile=128, split_k=2)):
         swz.gemm_fp8(qa, sa, qb, sb, debug_flags=swz.SWZ_DEBUG_SKIP_FIRST_LOAD, timeout_ms=50, **cfg)
         with pytest.raises(swz.SwzError) as e:

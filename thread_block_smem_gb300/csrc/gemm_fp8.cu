@@ -27,6 +27,7 @@
 //     rank order (deterministic, no workspace): for few tiles.
 //   * tiles are dealt out by the framework's tile orders, w = cluster + i P.
 #include <mutex>
+#include <type_traits>
 
 #include "common.h"
 #include "f8.cuh"
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       free_slot();
       if (aborted) break;
       if (PAIR || p.split == 1) {
-        if (row_in) {
+        if (p.c_align >= 16) {
 #pragma unroll
           for (int c = 0; c < COLS / 16; ++c) {
             const int64_t n = col0 + c * 16;
@@ -475,7 +476,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             float f[16];
 #pragma unroll
             for (int j = 0; j < 8; ++j) pipe::unpack2(acc[c * 8 + j], f[2 * j], f[2 * j + 1]);
-            store16(p, row, int(n), f);
+            if (row_in) store16(p, row, int(n), f);
+          }
+        } else {
+          // rows of C that start anywhere: a lane a column instead of a row, so
+          // that a store is one piece of a row (element by element from the
+          // rows' lanes it took 5 times as long)
+#pragma unroll
+          for (int c = 0; c < COLS / 32; ++c) {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              pipe::unpack2(acc[c * 16 + j], f[2 * j], f[2 * j + 1]);
+            pipe::transpose32(f, lane);
+            const int64_t n = col0 + c * 32 + lane, r0 = row - lane;
+            if (n < p.N)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (r0 + i < p.M) store1(p.C, (r0 + i) * p.ldc + n, f[i], p.c_dtype);
+            __syncwarp();
           }
         }
       } else {
@@ -500,39 +519,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();
     if (warp < kMath && !aborted) {
       const TileCoord t = tile_of(p.order, w0, p.sched_m, p.sched_n, p.group);
-      const uint32_t rows = BM / p.split;
-      for (uint32_t i = warp; i < rows; i += kMath) {
-        const uint32_t r = crank * rows + i;
-        const int64_t row = int64_t(t.m) * BM + r;
-        if (row >= p.M) break;
-        const uint32_t at = sA + r * (BN * 4) + ((lane ^ (r & 31u)) << 4);
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        for (uint32_t j = 0; j < p.split; ++j) {
-          float a, b, c, d;
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(a), "=f"(b), "=f"(c), "=f"(d)
-                       : "r"(ptx::map_to_rank(at, j))
-                       : "memory");
-          f[0] += a;
-          f[1] += b;
-          f[2] += c;
-          f[3] += d;
-        }
-        const int64_t n = int64_t(t.n) * BN + lane * 4;
-        const int64_t o = row * p.ldc + n;
-        if (n + 4 <= p.N && p.c_align >= 16) {
-          if (p.c_dtype == SWZ_F32)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.C) + o) =
-                make_float4(f[0], f[1], f[2], f[3]);
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + o) =
-                make_uint2(pack_out(f[0], f[1], p.c_dtype), pack_out(f[2], f[3], p.c_dtype));
-        } else {
+      const int64_t n = int64_t(t.n) * BN + lane * 4;
+      // A remote read takes about 1 us: a warp has eight of them in flight,
+      // from all S ranks for 8 / S rows.
+      auto reduce = [&](auto ranks) {
+        constexpr uint32_t S = decltype(ranks)::value, RW = 8 / S, rows = BM / S;
+#pragma unroll 1
+        for (uint32_t i = warp * RW; i < rows; i += kMath * RW) {
+          float f[RW][S][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (n + j < p.N) store1(p.C, o + j, f[j], p.c_dtype);
+          for (uint32_t k = 0; k < RW; ++k) {
+            const uint32_t r = crank * rows + i + k;
+            const uint32_t at = sA + r * (BN * 4) + ((lane ^ (r & 31u)) << 4);
+#pragma unroll
+            for (uint32_t j = 0; j < S; ++j)
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(f[k][j][0]), "=f"(f[k][j][1]), "=f"(f[k][j][2]),
+                             "=f"(f[k][j][3])
+                           : "r"(ptx::map_to_rank(at, j)));
+          }
+#pragma unroll
+          for (uint32_t k = 0; k < RW; ++k) {
+            const int64_t row = int64_t(t.m) * BM + crank * rows + i + k;
+            if (row >= p.M) continue;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = f[k][0][e];
+#pragma unroll
+              for (uint32_t j = 1; j < S; ++j) v[e] += f[k][j][e];
+            }
+            const int64_t o = row * p.ldc + n;
+            if (n + 4 <= p.N && p.c_align >= 16) {
+              if (p.c_dtype == SWZ_F32)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.C) + o) =
+                    make_float4(v[0], v[1], v[2], v[3]);
+              else
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + o) = make_uint2(
+                    pack_out(v[0], v[1], p.c_dtype), pack_out(v[2], v[3], p.c_dtype));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) store1(p.C, o + e, v[e], p.c_dtype);
+            }
+          }
         }
-      }
+      };
+      if (p.split == 2) reduce(std::integral_constant<uint32_t, 2>{});
+      else if (p.split == 4) reduce(std::integral_constant<uint32_t, 4>{});
+      else reduce(std::integral_constant<uint32_t, 8>{});
     }
     __syncwarp();
     ptx::cluster_sync();  // no CTA leaves while its partial tile is read
@@ -592,15 +627,17 @@ struct Choice {
 static uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // The variant with the least estimated time, in SM cycles: waves of tiles
-// times (blocks of K times the cycles of one, plus a tile's fixed part).
+// times (blocks of K times the cycles of one, plus a tile's fixed part), fitted
+// to one to four waves of 4096 x 4096 and to splits of 27 to 256 tiles.
 static Choice choose(uint64_t M, uint64_t N, uint64_t kb, uint32_t sms) {
-  const uint64_t pairs = sms / 2;
-  uint64_t best = ceil_div(ceil_div(M, 256) * ceil_div(N, 256), pairs) * (kb * 540 + 3000);
+  const uint64_t pairs = sms / 2, tn = ceil_div(N, 128);
+  uint64_t best = ceil_div(ceil_div(M, 256) * tn, pairs) * (kb * 370 + 5800);
   Choice c{256, 1};
-  const uint64_t tiles = ceil_div(M, 128) * ceil_div(N, 128);
+  const uint64_t tiles = ceil_div(M, 128) * tn;
   for (uint32_t s = 1; s <= 8; s *= 2) {
     if (s > 1 && kb < 2 * s) break;
-    const uint64_t t = ceil_div(tiles * s, sms) * (ceil_div(kb, s) * 380 + 2500 + (s > 1 ? 2000 : 0));
+    const uint64_t t =
+        ceil_div(tiles * s, sms) * (ceil_div(kb, s) * 390 + 6200 + (s > 1 ? 3200 : 0));
     if (t < best) {
       best = t;
       c = Choice{128, s};
@@ -624,6 +661,12 @@ static bool matrix_ok(const swz_fp8_matrix* m, int rows, int K) {
 extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t ldc,
                             int c_dtype, int M, int N, int K, const swz_gemm_fp8_opts* opts,
                             void* stream) {
+  return swz::gemm_fp8(A, B, C, ldc, c_dtype, M, N, K, opts, stream, false);
+}
+
+int swz::gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t ldc,
+                  int c_dtype, int M, int N, int K, const swz_gemm_fp8_opts* opts, void* stream,
+                  bool early_b) {
   swz_gemm_fp8_opts o = {};
   o.order = SWZ_SERPENTINE;
   o.group = 8;
@@ -656,6 +699,12 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
     return SWZ_OK;
   }
   const uint32_t kb = uint32_t((int64_t(K) + 127) / 128);
+  const uint64_t timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  if (o.tile == 0 && M <= kFewRows) {
+    if (o.split_k > 0 && uint32_t(o.split_k) > kb) return SWZ_EUNSUPPORTED;
+    return gemm_fp8_rows(*A, *B, C, ld, c_dtype, M, N, K, o.split_k, o.debug_flags, timeout_ns,
+                         early_b, dev.num_sms, s);
+  }
   Choice ch = choose(uint64_t(M), uint64_t(N), kb, uint32_t(dev.num_sms));
   if (o.tile == 256) ch = Choice{256, 1};
   if (o.tile == 128) ch = Choice{128, o.split_k ? uint32_t(o.split_k) : (ch.tile == 128 ? ch.split : 1u)};
@@ -697,7 +746,7 @@ extern "C" int swz_gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, vo
   const uintptr_t bits = ca | (M > 1 ? uintptr_t(ld * es) : 0);
   prm.c_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
   prm.debug_flags = o.debug_flags;
-  prm.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  prm.timeout_ns = timeout_ns;
   rc = op_status_word(&prm.status);
   if (rc != SWZ_OK) return rc;
   uint64_t programs = sm * sn * cl;

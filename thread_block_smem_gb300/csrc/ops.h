@@ -2,7 +2,10 @@
 // and tensor maps.
 #pragma once
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include "swz.h"
 
 namespace swz {
 
@@ -25,5 +28,17 @@ int encode_bytes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
 int encode_half(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t cols,
                 uint64_t ld, uint64_t batch_stride, uint32_t box_cols, uint32_t box_rows,
                 bool swizzle);
+
+// swz_gemm_fp8; `early_b`: the kernel before in the stream is the quantiser of
+// A, launched by the same caller, and B may be read while it runs.
+int gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t ldc, int c_dtype,
+             int M, int N, int K, const swz_gemm_fp8_opts* opts, void* stream, bool early_b);
+
+// Its kernel for up to kFewRows rows of A (arguments checked by the caller;
+// split 0: automatic).
+constexpr int kFewRows = 32;
+int gemm_fp8_rows(const swz_fp8_matrix& A, const swz_fp8_matrix& B, void* C, int64_t ldc,
+                  int c_dtype, int M, int N, int K, int split, uint32_t debug_flags,
+                  uint64_t timeout_ns, bool early_b, int num_sms, cudaStream_t stream);
 
 }  // namespace swz

@@ -224,6 +224,21 @@ __device__ __forceinline__ void ld_shared4(uint32_t addr, float (&v)[4]) {
                : "memory");
 }
 
+// 32 x 32 values of a warp, lane i with row i, to lane i with column i.
+__device__ __forceinline__ void transpose32(float (&v)[32], uint32_t lane) {
+#pragma unroll
+  for (uint32_t s = 16; s > 0; s /= 2) {
+    const bool high = (lane & s) != 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) {
+      if (i & s) continue;
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, high ? v[i] : v[i | s], s);
+      if (high) v[i] = got;
+      else v[i | s] = got;
+    }
+  }
+}
+
 // 32 bytes to a 32-byte aligned global address in one instruction.
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),

@@ -93,25 +93,27 @@ def swz_newton_schulz_workspace_size(batch, m, n):
 
 
 # ---- helpers ----------------------------------------------------------------------
-_types = None
+# A call on small tensors costs the host more than the GPU, so what every call
+# needs is looked up once: torch, the type codes, the library.
+torch = None
+_codes = _f8_codes = _f8_types = _L = None
 
 
-def _dtypes():
-    """{torch dtype: code} of the 16- and 32-bit types, and of the 8-bit ones."""
-    global _types
-    if _types is None:
-        import torch
-        _types = ({torch.float16: _swz.SWZ_F16, torch.bfloat16: _swz.SWZ_BF16,
-                   torch.float32: SWZ_F32},
-                  {torch.float8_e4m3fn: SWZ_E4M3, torch.float8_e5m2: SWZ_E5M2})
-    return _types
+def _init():
+    global torch, _codes, _f8_codes, _f8_types, _L
+    import torch as t
+    _codes = {t.float16: _swz.SWZ_F16, t.bfloat16: _swz.SWZ_BF16, t.float32: SWZ_F32}
+    _f8_codes = {t.float8_e4m3fn: SWZ_E4M3, t.float8_e5m2: SWZ_E5M2}
+    _f8_types = {"e4m3": t.float8_e4m3fn, "e5m2": t.float8_e5m2}
+    _L = _swz.lib()
+    torch = t
 
 
 def _code(t, what):
-    codes = _dtypes()[0]
-    if t not in codes:
+    code = _codes.get(t)
+    if code is None:
         raise TypeError(f"{what} must be fp16, bf16 or fp32")
-    return codes[t]
+    return code
 
 
 def _rows(x, what):
@@ -122,27 +124,43 @@ def _rows(x, what):
         raise ValueError(f"{what}: CUDA tensor expected")
     m, k = x.shape
     ld, one = x.stride()
-    if k > 1 and one != 1:
+    if one != 1 and k > 1:
         raise ValueError(f"{what}: contiguous rows expected")
-    if m > 1 and ld < k:
+    if m <= 1:
+        return m, k, k or 1
+    if ld < k:
         raise ValueError(f"{what}: rows must not overlap")
-    return m, k, ld if m > 1 else max(k, 1)
+    return m, k, ld
 
 
 def _on(stream):
     """Context in which what is allocated belongs to the stream that the call runs on."""
     if stream is None:
         return contextlib.nullcontext()
-    import torch
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
 
 
+def _handle(stream, x):
+    """The cudaStream_t that a call runs on (None: the current stream of x's device)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(x.device.index)
+    return _swz._stream(stream)
+
+
+def _empty(shape, dtype, x, stream):
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with _on(stream):
+        return x.new_empty(shape, dtype=dtype)
+
+
 def _block(block):
-    if block not in BLOCKS:
+    code = BLOCKS.get(block)
+    if code is None:
         raise ValueError("block must be 'row' or 'square'")
-    return BLOCKS[block]
+    return code
 
 
 def _blocks(n):
@@ -151,31 +169,43 @@ def _blocks(n):
 
 def fp8_empty(rows, cols, dtype, device="cuda"):
     """Uninitialised 8-bit (rows, cols) tensor whose rows start on multiples of 16 bytes."""
-    import torch
+    if torch is None:
+        _init()
     ld = (cols + 15) // 16 * 16
     q = torch.empty((rows, ld), dtype=dtype, device=device)
-    return q if ld == cols else q[:, :cols]
+    return q if ld == cols else q.narrow(1, 0, cols)
 
 
 def _matrix(q, scales, block, what):
     """swz_fp8_matrix of an 8-bit tensor and its scales, checked."""
-    fmt = _dtypes()[1].get(q.dtype)
+    fmt = _f8_codes.get(q.dtype)
     if fmt is None:
         raise TypeError(f"{what}: float8_e4m3fn or float8_e5m2 expected")
     m, k, ld = _rows(q, what)
     if m <= 1 or k == 0:  # no second row whose place matters
         ld = (k + 15) // 16 * 16
-    if ld % 16 or q.data_ptr() % 16:
+    at = q.data_ptr()
+    if ld % 16 or at % 16:
         raise ValueError(f"{what}: rows must start on multiples of 16 bytes")
-    if scales.dtype.itemsize != 4 or not scales.dtype.is_floating_point or not scales.is_cuda:
+    if scales.dtype != torch.float32 or not scales.is_cuda:
         raise TypeError(f"{what}: fp32 CUDA scales expected")
     want = (_blocks(k), m) if block == SWZ_BLOCK_ROW else (_blocks(m), _blocks(k))
-    if tuple(scales.shape) != want:
+    if scales.shape != want:
         raise ValueError(f"{what}: scales of shape {want} expected, got {tuple(scales.shape)}")
     _, _, lds = _rows(scales, f"{what} scales")
-    if scales.shape[0] <= 1:
-        lds = max(want[1], 1)
-    return swz_fp8_matrix(q.data_ptr(), ld, scales.data_ptr(), lds, fmt, block), m, k
+    return swz_fp8_matrix(at, ld, scales.data_ptr(), lds, fmt, block), m, k
+
+
+def _output(out, dtype, M, N, x, stream):
+    """(tensor, elements from row to row, type code) of an M x N result."""
+    if out is None:
+        code = _code(dtype, "out_dtype")
+        return _empty((M, N), dtype, x, stream), N, code
+    code = _code(out.dtype, "out")
+    m, n, ld = _rows(out, "out")
+    if m != M or n != N:
+        raise ValueError(f"out: shape {(M, N)} expected")
+    return out, ld, code
 
 
 # ---- operators --------------------------------------------------------------------
@@ -187,28 +217,29 @@ def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
     For a block with largest magnitude amax: ac = max(amax, 2^-96), r = F / ac,
     scale = ac / F (F = 448 for e4m3, 57344 for e5m2), q = x r rounded to
     nearest even."""
-    import torch
+    if torch is None:
+        _init()
     M, K, ldx = _rows(x, "x")
     code, b = _code(x.dtype, "x"), _block(block)
-    if fmt not in FORMATS:
+    f8 = _f8_types.get(fmt)
+    if f8 is None:
         raise ValueError("fmt must be 'e4m3' or 'e5m2'")
-    f8 = torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2
-    dev = x.device
-    kb, mb = _blocks(K), _blocks(M)
-    with _on(stream):
-        q = fp8_empty(M, K, f8, dev)
-        s = torch.empty((mb, kb) if b else (kb, M), dtype=torch.float32, device=dev)
-        qt = st = None
-        if transposed:
-            qt = fp8_empty(K, M, f8, dev)
-            st = torch.empty((kb, mb) if b else (mb, K), dtype=torch.float32, device=dev)
-    pad = lambda n: (n + 15) // 16 * 16  # noqa: E731
-    _swz._check(swz_quantize_fp8(
-        x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), pad(K), s.data_ptr(),
-        kb if b else M, qt.data_ptr() if transposed else None, pad(M),
-        st.data_ptr() if transposed else None, mb if b else K, _swz._stream(stream)),
+    kb, mb = (K + 127) // 128, (M + 127) // 128
+    ldq, ldt = (K + 15) // 16 * 16, (M + 15) // 16 * 16
+    q = _empty((M, ldq), f8, x, stream)
+    s = _empty((mb, kb) if b else (kb, M), torch.float32, x, stream)
+    if not transposed:
+        _swz._check(_L.swz_quantize_fp8(
+            x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), ldq, s.data_ptr(),
+            kb if b else M, None, 0, None, 0, _handle(stream, x)), "swz_quantize_fp8")
+        return (q if ldq == K else q.narrow(1, 0, K)), s
+    qt = _empty((K, ldt), f8, x, stream)
+    st = _empty((kb, mb) if b else (mb, K), torch.float32, x, stream)
+    _swz._check(_L.swz_quantize_fp8(
+        x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), ldq, s.data_ptr(),
+        kb if b else M, qt.data_ptr(), ldt, st.data_ptr(), mb if b else K, _handle(stream, x)),
         "swz_quantize_fp8")
-    return (q, s, qt, st) if transposed else (q, s)
+    return (q if ldq == K else q.narrow(1, 0, K)), s, (qt if ldt == M else qt.narrow(1, 0, M)), st
 
 
 def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order="serpentine",
@@ -220,52 +251,37 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
     ``order``, ``group``: the order of the output tiles, as in ``gemm``;
     ``tile``, ``split_k``, ``num_programs``: see swz_gemm_fp8_opts (0 =
     automatic)."""
-    import torch
+    if torch is None:
+        _init()
     A, M, K = _matrix(a, sa, SWZ_BLOCK_ROW, "a")
     B, N, K2 = _matrix(b, sb, _block(b_block), "b")
     if K != K2:
         raise ValueError("inner dimensions differ")
-    C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a.device, stream)
+    C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a, stream)
     opts = swz_gemm_fp8_opts(_swz._order(order), group, tile, split_k, num_programs, debug_flags,
                              timeout_ms)
-    _swz._check(swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _swz._stream(stream)),
+    _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
                 "swz_gemm_fp8")
     return C
-
-
-def _output(out, dtype, M, N, device, stream):
-    """(tensor, elements from row to row, type code) of an M x N result."""
-    import torch
-    if out is None:
-        code = _code(dtype, "out_dtype")
-        with _on(stream):
-            return torch.empty((M, N), dtype=dtype, device=device), N, code
-    code = _code(out.dtype, "out")
-    m, n, ld = _rows(out, "out")
-    if (m, n) != (M, N):
-        raise ValueError(f"out: shape {(M, N)} expected")
-    return out, ld, code
 
 
 def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=None):
     """y = x W^T (M x N): x (M x K; fp16, bf16 or fp32) is quantised in row
     blocks (e4m3) and multiplied by W (N x K) kept as (qw, sw).  ``out`` or
     ``out_dtype`` (default: x's type)."""
-    import torch
+    if torch is None:
+        _init()
     M, K, ldx = _rows(x, "x")
     code = _code(x.dtype, "x")
     W, N, K2 = _matrix(qw, sw, _block(w_block), "qw")
     if K != K2:
         raise ValueError("inner dimensions differ")
-    y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x.device, stream)
+    y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x, stream)
     rc, need = swz_linear_fp8_workspace_size(M, N, K)
     _swz._check(rc, "swz_linear_fp8_workspace_size")
-    ws = None
-    if need:
-        with _on(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _swz._check(swz_linear_fp8(x.data_ptr(), code, ldx, W, y.data_ptr(), ldy, ycode, M, N, K,
-                               ws.data_ptr() if need else None, need, _swz._stream(stream)),
+    ws = _empty((need,), torch.uint8, x, stream) if need else None
+    _swz._check(_L.swz_linear_fp8(x.data_ptr(), code, ldx, W, y.data_ptr(), ldy, ycode, M, N, K,
+                                  None if ws is None else ws.data_ptr(), need, _handle(stream, x)),
                 "swz_linear_fp8")
     return y
 
@@ -285,9 +301,10 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
     """(dx, dw) of linear_fp8_forward: dx = dy W (M x K; default dy's type)
     and dw = dy^T x (N x K; default fp32), dy quantised in row blocks along N
     and along the rows; None in place of one that is not needed."""
-    import torch
     qxt, sxt, qwt, swt = saved
-    M, N, ldd = _rows(dy, "dy")
+    if torch is None:
+        _init()
+    M, N, _ = _rows(dy, "dy")
     if M != qxt.shape[1] or N != qwt.shape[1]:
         raise ValueError("dy does not have the shape of the layer's output")
     dx = dw = None
@@ -310,7 +327,8 @@ def fp8_linear(x, w):
     gradient of w in fp32 rounded to w's type."""
     global _function
     if _function is None:
-        import torch
+        if torch is None:
+            _init()
 
         class Fp8Linear(torch.autograd.Function):
             @staticmethod
@@ -339,14 +357,16 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     X = a X + (b A + c A^2) X with A = X X^T (on the right with X^T X when m >
     n), ``coefficients`` = (a, b, c).  ``out`` (G's shape; may be G) or
     ``out_dtype`` (default bf16)."""
-    import torch
+    if torch is None:
+        _init()
     if G.dim() not in (2, 3):
         raise ValueError("G: 2-D or 3-D tensor expected")
+    if not G.is_cuda:
+        raise ValueError("G: CUDA tensor expected")
     code = _code(G.dtype, "G")
     if out is None:
         ycode = _code(out_dtype or torch.bfloat16, "out_dtype")
-        with _on(stream):
-            out = torch.empty(G.shape, dtype=out_dtype or torch.bfloat16, device=G.device)
+        out = _empty(G.shape, out_dtype or torch.bfloat16, G, stream)
     else:
         ycode = _code(out.dtype, "out")
         if out.shape != G.shape:
@@ -364,10 +384,9 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     a, b, c = coefficients
     rc, need = swz_newton_schulz_workspace_size(batch, m, n)
     _swz._check(rc, "swz_newton_schulz_workspace_size")
-    with _on(stream):
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=G.device)
+    ws = _empty((max(need, 1),), torch.uint8, G, stream)
     opts = swz_newton_schulz_opts(tile, debug_flags, timeout_ms)
-    _swz._check(swz_newton_schulz(g.data_ptr(), code, *ld[0], y.data_ptr(), ycode, *ld[1], batch, m,
-                                  n, steps, a, b, c, eps, opts, ws.data_ptr(), need,
-                                  _swz._stream(stream)), "swz_newton_schulz")
+    _swz._check(_L.swz_newton_schulz(g.data_ptr(), code, *ld[0], y.data_ptr(), ycode, *ld[1], batch, m,
+                                     n, steps, a, b, c, eps, opts, ws.data_ptr(), need,
+                                     _handle(stream, G)), "swz_newton_schulz")
     return out
