@@ -98,10 +98,10 @@ struct Params {
   int64_t ld_master, batch_master;
   const uint8_t* g;             // the caller's G
   int64_t ld_g, batch_g;
-  int g_dtype;
+  int g_dtype, g_wide;          // g_wide: rows start on 16 bytes
   uint8_t* y;                   // the caller's result in the last step, else NULL
   int64_t ld_y, batch_y;
-  int y_dtype;
+  int y_dtype, y_wide;
   unsigned int* status;
   uint64_t timeout_ns;
   uint32_t debug_flags;
@@ -121,6 +121,11 @@ __device__ __forceinline__ void store_any(uint8_t* p, int64_t at, float v, int d
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
@@ -157,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + K_::BARS);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0);  // known uniform
+  const uint32_t lane = threadIdx.x % 32;
   const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
   const bool leader = rank == 0;
 
@@ -205,60 +211,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kEpiWarps) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
-      const uint64_t pol = ptx::l2_policy_evict_last();
-      // 128 rows (or columns, MN-major) of an operand from r0, K elements k0 ..
-      auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t r0, int32_t k0,
-                      int32_t b, bool mn) {
-        if (mn) {
+    // The whole warp runs the loop and one elected lane issues (also below):
+    // descriptors and addresses then live in uniform registers.
+    uint32_t stage = 0, phase = 0;
+    bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
+    const uint64_t pol = ptx::l2_policy_evict_last();
+    const uint32_t full0 = PAIR ? ptx::map_to_rank(full_bar(0), 0) : full_bar(0);
+    // 128 rows (or columns, MN-major) of an operand from r0, K elements k0 ..
+    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t r0, int32_t k0,
+                    int32_t b, bool mn) {
+      if (mn) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if constexpr (PAIR)
-              ptx::tma_load_3d_pair(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
-            else
-              ptx::tma_load_3d(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < KA; ++j) {
-            if constexpr (PAIR)
-              ptx::tma_load_3d_pair(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
-            else
-              ptx::tma_load_3d(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
-          }
+        for (int j = 0; j < 2; ++j) {
+          if constexpr (PAIR)
+            ptx::tma_load_3d_pair(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
+          else
+            ptx::tma_load_3d(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
         }
-      };
-      for (uint32_t w = w0; w < p.units && !aborted; w += P) {
-        uint32_t b;
-        const TileCoord t = tile_at(w, b);
-        const int32_t m0 = int32_t((t.m * CG + rank) * BM);
-        const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
-        for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
-          if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) { aborted = true; break; }
-          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
-          if (skip) {
-            skip = false;
-          } else {
-            const uint32_t fb = PAIR ? ptx::map_to_rank(full_bar(stage), 0) : full_bar(stage);
-            const int32_t k0 = int32_t(kb * (64 * KA));
-            load(sA + stage * K_::OP_BYTES, &tmA, fb, m0, k0, int32_t(b), p.a_mn != 0);
-            load(sB + stage * K_::OP_BYTES, &tmB, fb, n0, k0, int32_t(b), p.b_mn != 0);
-          }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      } else {
+#pragma unroll
+        for (int j = 0; j < KA; ++j) {
+          if constexpr (PAIR)
+            ptx::tma_load_3d_pair(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
+          else
+            ptx::tma_load_3d(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
         }
       }
-      for (int i = 0; i < STAGES && !aborted; ++i) {
-        if (!pipe::wait(empty_bar(stage), phase ^ 1u, ctl)) aborted = true;
+    };
+    for (uint32_t w = w0; w < p.units && !aborted; w += P) {
+      uint32_t b;
+      const TileCoord t = tile_at(w, b);
+      const int32_t m0 = int32_t((t.m * CG + rank) * BM);
+      const int32_t n0 = int32_t(t.n * BN + rank * K_::BN_LOCAL);
+      for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
+        const bool ok = pipe::wait(empty_bar(stage), phase ^ 1u, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+        if (pipe::elect_one()) {
+          if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
+          if (!skip) {
+            const int32_t k0 = int32_t(kb * (64 * KA));
+            load(sA + stage * K_::OP_BYTES, &tmA, full0 + 8u * stage, m0, k0, int32_t(b),
+                 p.a_mn != 0);
+            load(sB + stage * K_::OP_BYTES, &tmB, full0 + 8u * stage, n0, k0, int32_t(b),
+                 p.b_mn != 0);
+          }
+        }
+        __syncwarp();
+        skip = false;
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (aborted) pipe::spin_ns(50000);
     }
+    // every stage released: no commit is in flight towards this CTA
+    for (int i = 0; i < STAGES && !aborted; ++i) {
+      const bool ok = pipe::wait(empty_bar(stage), phase ^ 1u, ctl);
+      if (!__all_sync(0xFFFFFFFFu, ok)) aborted = true;
+      if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+    }
+    if (aborted) pipe::spin_ns(50000);  // copies already issued land
     __syncwarp();
   } else if (warp == kEpiWarps + 1) {
     // ---------------- MMA issuer (leader CTA) ----------------
-    if (lane == 0 && leader) {
+    if (leader) {
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool issued = false;
       const uint64_t adesc0 = p.a_mn ? pipe::sdesc128(sA, 64 * KA * 128, 1024)
@@ -267,38 +280,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : pipe::sdesc128(sB, 16, 1024);
       const bool amn = p.a_mn != 0, bmn = p.b_mn != 0;
       for (uint32_t w = w0; w < p.units && !aborted; w += P) {
-        if (!pipe::wait(tempty_bar(acc), acc_phase ^ 1u, ctl)) { aborted = true; break; }
+        bool ok = pipe::wait(tempty_bar(acc), acc_phase ^ 1u, ctl);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
         ptx::tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
-#pragma unroll 4
         for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
-          if (!pipe::wait(full_bar(stage), phase, ctl)) { aborted = true; break; }
+          ok = pipe::wait(full_bar(stage), phase, ctl);
+          if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
           ptx::tc_fence_after();
           const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
           const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
-          // slice kk: 16 elements of K; K-major 32 bytes into atom kk / 4,
-          // MN-major 16 rows of 128 bytes down
+          if (pipe::elect_one()) {
+            // slice kk: 16 elements of K; K-major 32 bytes into atom kk / 4,
+            // MN-major 16 rows of 128 bytes down
 #pragma unroll
-          for (uint32_t kk = 0; kk < uint32_t(4 * KA); ++kk) {
-            const uint32_t km = ((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
-            const uint32_t mn = 128u * kk;
-            ptx::mma<CG, 0>(d, a + (amn ? mn : km), b + (bmn ? mn : km), p.idesc,
-                            kb != 0 || kk != 0);
+            for (uint32_t kk = 0; kk < uint32_t(4 * KA); ++kk) {
+              const uint32_t km = ((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
+              const uint32_t mn = 128u * kk;
+              ptx::mma<CG, 0>(d, a + (amn ? mn : km), b + (bmn ? mn : km), p.idesc,
+                              kb != 0 || kk != 0);
+            }
+            if constexpr (PAIR) ptx::mma_commit_pair(empty_bar(stage), 0x3);
+            else ptx::mma_commit(empty_bar(stage));
+            if (kb + 1 == p.num_kb) {
+              if constexpr (PAIR) ptx::mma_commit_pair(tfull_bar(acc), 0x3);
+              else ptx::mma_commit(tfull_bar(acc));
+            }
           }
+          __syncwarp();
           issued = true;
-          if constexpr (PAIR) ptx::mma_commit_pair(empty_bar(stage), 0x3);
-          else ptx::mma_commit(empty_bar(stage));
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (aborted) break;
-        if constexpr (PAIR) ptx::mma_commit_pair(tfull_bar(acc), 0x3);
-        else ptx::mma_commit(tfull_bar(acc));
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
       if (aborted && issued) {
-        if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
-        else ptx::mma_commit(drain_bar);
+        if (pipe::elect_one()) {
+          if constexpr (PAIR) ptx::mma_commit_pair(drain_bar, 0x1);
+          else ptx::mma_commit(drain_bar);
+        }
         const uint64_t t0 = ptx::global_timer_ns();
         while (!pipe::try_wait(drain_bar, 0) && ptx::global_timer_ns() - t0 < p.timeout_ns) {
         }
@@ -307,108 +327,200 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---------------- epilogue ----------------
+    // A warp takes 32 rows and 64 columns at a time.  What the sums are added
+    // to is loaded before the tile's products are waited for: a chunk's loads
+    // after the wait cost an L2 round trip each, most of a small product's time.
     const uint32_t q = warp & 3u, half = warp >> 2;
     uint32_t acc = 0, acc_phase = 0;
-    for (uint32_t w = w0; w < p.units; w += P) {
+    for (uint32_t w = w0; w < p.units && !aborted; w += P) {
       uint32_t b;
       const TileCoord t = tile_at(w, b);
       const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
-      const int64_t col0 = int64_t(t.n) * BN + half * COLS;
       const bool row_in = row < p.M;
       const Scale sc = p.scale[b];
       const float fx = p.first ? sc.f : sc.down;  // X over the fp16 X's power of two
       const float f = p.mode == kPoly ? p.f : p.mode == kGram ? p.f * fx * fx : p.f * fx;
       const float out_scale = p.mode == kUpdate ? p.out_scale * sc.up : 1.f;
-      const bool ok = pipe::wait(tfull_bar(acc), acc_phase, ctl);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
-      ptx::tc_fence_after();
-      const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc * BN + half * COLS;
+      const float u16 = p.mode == kPoly ? p.u : p.a * p.u * fx;
 #pragma unroll 1
-      for (int c = 0; c < COLS / 16; ++c) {
-        const int64_t col = col0 + c * 16;
-        if (col >= p.N) break;
-        __syncwarp();
-        uint32_t r[16];
-        pipe::tmem_ld16(taddr + c * 16, r);
-        float v[16];
-        // what the sums are added to, while they load
+      for (int h = 0; h < COLS / 64; ++h) {
+        const int64_t col0 = int64_t(t.n) * BN + half * COLS + h * 64;
+        float v[64];
         if (p.mode == kGram) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = 0.f;
-        } else if (!row_in) {
+          for (int j = 0; j < 64; ++j) v[j] = 0.f;
+        } else if (p.mode == kPoly || p.source != kFromG) {
+          const bool from16 = p.mode == kPoly || p.source == kFromF16;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = 0.f;
-        } else if (p.mode == kPoly || p.source == kFromF16) {
-          const float u = p.mode == kPoly ? p.u : p.a * p.u * fx;
-          const uint4* src =
-              reinterpret_cast<const uint4*>(p.in + b * p.batch_in + row * p.ld_in + col);
+          for (int c = 0; c < 4; ++c) {
+            const int64_t col = col0 + c * 16;
+            const bool in = row_in && col < p.N;
+            if (from16) {
+              const uint4* src =
+                  reinterpret_cast<const uint4*>(p.in + b * p.batch_in + row * p.ld_in + col);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 x = src[h];
-            const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+              for (int k = 0; k < 2; ++k) {
+                const uint4 x = in ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&e[j]));
-              v[8 * h + 2 * j] = u * z.x;
-              v[8 * h + 2 * j + 1] = u * z.y;
+                for (int j = 0; j < 4; ++j) {
+                  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&e[j]));
+                  v[c * 16 + 8 * k + 2 * j] = u16 * z.x;
+                  v[c * 16 + 8 * k + 2 * j + 1] = u16 * z.y;
+                }
+              }
+            } else {
+              const float4* src = reinterpret_cast<const float4*>(
+                  p.master_in + b * p.batch_master + row * p.ld_master + col);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 x = in ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[c * 16 + 4 * k] = p.a * x.x;
+                v[c * 16 + 4 * k + 1] = p.a * x.y;
+                v[c * 16 + 4 * k + 2] = p.a * x.z;
+                v[c * 16 + 4 * k + 3] = p.a * x.w;
+              }
             }
           }
-        } else if (p.source == kFromF32) {
-          const float4* src = reinterpret_cast<const float4*>(p.master_in + b * p.batch_master +
-                                                              row * p.ld_master + col);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const float4 x = src[h];
-            v[4 * h] = p.a * x.x;
-            v[4 * h + 1] = p.a * x.y;
-            v[4 * h + 2] = p.a * x.z;
-            v[4 * h + 3] = p.a * x.w;
-          }
         } else {
-          const int64_t at = b * p.batch_g + row * p.ld_g + col;
+          // G: rows that start on 16 bytes eight values at a time, others with
+          // a lane a column
+          const float g1 = p.a * sc.p1, g2 = sc.p2 * sc.f;
+          const int es = p.g_dtype == SWZ_F32 ? 4 : 2;
+          const uint8_t* g = p.g + (b * p.batch_g) * es;
+          if (p.g_wide) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            v[j] = col + j < p.N
-                       ? p.a * (load_any(p.g, at + j, p.g_dtype) * sc.p1 * sc.p2 * sc.f)
-                       : 0.f;
+            for (int c = 0; c < 8; ++c) {
+              const int64_t col = col0 + c * 8;
+              const int left = row_in && col < p.N ? int(min(p.N - col, int64_t(8))) : 0;
+              const uint8_t* src = g + (row * p.ld_g + col) * es;
+              float* to = v + c * 8;
+              uint32_t x[8];
+              if (p.g_dtype == SWZ_F32) {
+                f8::load8<f8::F32>(src, left, true, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[j] = f8::F32::value(x, j);
+              } else {
+                f8::load8<f8::Bf16>(src, left, true, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  to[j] = p.g_dtype == SWZ_BF16 ? f8::Bf16::value(x, j) : f8::F16::value(x, j);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float x[32];
+              const int64_t col = col0 + c * 32 + lane, r0 = row - lane;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                x[i] = col < p.N && r0 + i < p.M
+                           ? load_any(g, (r0 + i) * p.ld_g + col, p.g_dtype)
+                           : 0.f;
+              pipe::transpose32(x, lane);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[c * 32 + i] = x[i];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 64; ++j) v[j] = v[j] * g1 * g2;
         }
-        pipe::tmem_ld_wait16(r);
+        if (h == 0) {
+          const bool ok = pipe::wait(tfull_bar(acc), acc_phase, ctl);
+          if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
+          ptx::tc_fence_after();
+        }
+        __syncwarp();
+        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc * BN + half * COLS + h * 64;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = fmaf(f, __uint_as_float(r[j]), v[j]);
-        if (!row_in) continue;
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(taddr + c * 32, r);
+          pipe::tmem_ld_wait32(r);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[c * 32 + j] = fmaf(f, __uint_as_float(r[j]), v[c * 32 + j]);
+        }
+        if (h + 1 == COLS / 64) {  // the tile is in registers
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) pipe::arrive_at(ptx::map_to_rank(tempty_bar(acc), 0));
+            else ptx::mbar_arrive(tempty_bar(acc));
+          }
+        }
         if (p.y) {
-          const int64_t at = b * p.batch_y + row * p.ld_y + col;
+          // the result: rows that start on 16 bytes by the row, others with a
+          // lane a column
+          const int es = p.y_dtype == SWZ_F32 ? 4 : 2;
+          uint8_t* y = p.y + (b * p.batch_y) * es;
+          if (p.y_wide) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (col + j < p.N) store_any(p.y, at + j, v[j], p.y_dtype);
+            for (int c = 0; c < 8; ++c) {
+              const int64_t col = col0 + c * 8;
+              if (!row_in || col >= p.N) continue;
+              uint8_t* to = y + (row * p.ld_y + col) * es;
+              const float* x = v + c * 8;
+              if (col + 8 > p.N) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (col + j < p.N) store_any(to, j, x[j], p.y_dtype);
+              } else if (p.y_dtype == SWZ_F32) {
+                reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+                reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+              } else {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  o[j] = p.y_dtype == SWZ_BF16 ? bf2_bits(x[2 * j], x[2 * j + 1])
+                                               : half2_bits(x[2 * j], x[2 * j + 1]);
+                *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float x[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = v[c * 32 + i];
+              pipe::transpose32(x, lane);
+              const int64_t col = col0 + c * 32 + lane, r0 = row - lane;
+              if (col < p.N)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (r0 + i < p.M) store_any(y, (r0 + i) * p.ld_y + col, x[i], p.y_dtype);
+              __syncwarp();
+            }
+          }
           continue;
         }
-        if (p.master_out) {
-          float4* dst = reinterpret_cast<float4*>(p.master_out + b * p.batch_master +
-                                                  row * p.ld_master + col);
 #pragma unroll
-          for (int h = 0; h < 4; ++h)
-            dst[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+        for (int c = 0; c < 4; ++c) {
+          const int64_t col = col0 + c * 16;
+          if (!row_in || col >= p.N) continue;
+          const float* x = v + c * 16;
+          if (p.master_out) {
+            float4* dst = reinterpret_cast<float4*>(p.master_out + b * p.batch_master +
+                                                    row * p.ld_master + col);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          }
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = half2_bits(x[2 * j] * out_scale, x[2 * j + 1] * out_scale);
+          __half* out = p.out + b * p.batch_out;
+          pipe::st_global_32b(out + row * p.ld_out + col, o);
+          if (sym && t.m != t.n) {
+            // the other half: lanes are neighbours along its rows
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (col + j < p.N)
+                reinterpret_cast<uint16_t*>(out)[(col + j) * p.ld_out + row] =
+                    uint16_t(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+          }
         }
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = half2_bits(v[2 * j] * out_scale, v[2 * j + 1] * out_scale);
-        __half* out = p.out + b * p.batch_out;
-        pipe::st_global_32b(out + row * p.ld_out + col, o);
-        if (sym && t.m != t.n) {
-          // the other half: lanes are neighbours along its rows
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (col + j < p.N)
-              reinterpret_cast<uint16_t*>(out)[(col + j) * p.ld_out + row] =
-                  uint16_t(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
-        }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) pipe::arrive_at(ptx::map_to_rank(tempty_bar(acc), 0));
-        else ptx::mbar_arrive(tempty_bar(acc));
       }
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
@@ -427,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // values times 2^-80 and 2^80 -- so that no finite G overflows and none that
 // matters underflows; per CTA in fp32 by thread, then in double, in a fixed
 // order.
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256, kNormUnroll = 4;
 
 struct NormArgs {
   const uint8_t* g;
@@ -450,21 +562,29 @@ __global__ void __launch_bounds__(kNormThreads) ns_norm_kernel(const NormArgs p)
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
   const uint32_t b = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
   const uint32_t chunks = (uint32_t(p.n) + 7u) / 8u;  // of 8 values of a row
-  const uint64_t total = uint64_t(chunks) * uint32_t(p.m);
-  const uint64_t beg = total * part / p.parts, end = total * (part + 1) / p.parts;
+  const uint32_t total = chunks * uint32_t(p.m);      // at most 2^28 + m
+  const uint32_t beg = uint32_t(uint64_t(total) * part / p.parts);
+  const uint32_t end = uint32_t(uint64_t(total) * (part + 1) / p.parts);
   const uint8_t* g = p.g + b * p.batch_g * T::kBytes;
   float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-  for (uint64_t i = beg + threadIdx.x; i < end; i += kNormThreads) {
-    const uint32_t r = uint32_t(i / chunks), c = uint32_t(i - uint64_t(r) * chunks);
-    uint32_t w[T::kWords];
-    f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes, p.n - int(c * 8), p.wide != 0, w);
+#pragma unroll 1
+  for (uint32_t i0 = beg + threadIdx.x; i0 < end; i0 += kNormThreads * kNormUnroll) {
+    uint32_t w[kNormUnroll][T::kWords];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float v = T::value(w, j), lo = v * 0x1p-80f, hi = v * 0x1p80f;
-      s0 = fmaf(v, v, s0);
-      s1 = fmaf(lo, lo, s1);
-      s2 = fmaf(hi, hi, s2);
+    for (int k = 0; k < kNormUnroll; ++k) {
+      const uint32_t i = i0 + k * kNormThreads, r = i / chunks, c = i - r * chunks;
+      f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes,
+                   i < end ? p.n - int(c * 8) : 0, p.wide != 0, w[k]);
     }
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = T::value(w[k], j), lo = v * 0x1p-80f, hi = v * 0x1p80f;
+        s0 = fmaf(v, v, s0);
+        s1 = fmaf(lo, lo, s1);
+        s2 = fmaf(hi, hi, s2);
+      }
   }
   double d[3] = {s0, s1, s2};
 #pragma unroll
@@ -502,39 +622,51 @@ __global__ void __launch_bounds__(kNormThreads) ns_start_kernel(const NormArgs p
       if (!(d[0] < 1e36)) norm = sqrt(d[1]) * 0x1p80;
       else if (d[0] > 1e-30) norm = sqrt(d[0]);
       else norm = sqrt(d[2]) * 0x1p-80;
-      const double root = sqrt(double(p.m) * double(p.n));
+      // the largest power of two 2^e with norm * 2^e <= sqrt(m n), or half it
       int e = 0;
-      if (norm > 0.0 && norm < 1e300) e = int(floor(log2(root / norm)));
+      if (norm > 0.0 && norm < 1e300)
+        e = ilogb(double(p.m) * double(p.n)) / 2 - ilogb(norm) - 1;
       const double div = norm + p.eps;
-      sc.p1 = float(exp2(double(e / 2)));
-      sc.p2 = float(exp2(double(e - e / 2)));
-      sc.f = div > 0.0 ? float(exp2(-double(e)) / div) : (div == 0.0 ? 0.f : float(div));
+      sc.p1 = ldexpf(1.f, e / 2);
+      sc.p2 = ldexpf(1.f, e - e / 2);
+      sc.f = div > 0.0 ? float(ldexp(1.0, -e) / div) : (div == 0.0 ? 0.f : float(div));
       // X grows from |G| / (|G| + eps) by known factors, its bound by others
-      const double share = norm / div;
       int z = 0;
-      if (share > 0.0 && share < p.headroom) z = int(floor(log2(p.headroom / share)));
-      if (z > 126) z = 126;
-      sc.up = float(exp2(double(z)));
-      sc.down = float(exp2(-double(z)));
+      if (norm > 0.0 && norm < div * p.headroom) z = ilogb(p.headroom) + ilogb(div) - ilogb(norm) - 2;
+      z = z < 0 ? 0 : z > 126 ? 126 : z;
+      sc.up = ldexpf(1.f, z);
+      sc.down = ldexpf(1.f, -z);
       if (part == 0) p.scale[b] = sc;
     }
   }
   __syncthreads();
   const float p1 = sc.p1, p2 = sc.p2;
   const uint32_t chunks = (uint32_t(p.n) + 7u) / 8u;
-  const uint64_t total = uint64_t(chunks) * uint32_t(p.m);
-  const uint64_t beg = total * part / p.parts, end = total * (part + 1) / p.parts;
+  const uint32_t total = chunks * uint32_t(p.m);
+  const uint32_t beg = uint32_t(uint64_t(total) * part / p.parts);
+  const uint32_t end = uint32_t(uint64_t(total) * (part + 1) / p.parts);
   const uint8_t* g = p.g + b * p.batch_g * T::kBytes;
   __half* x = p.x + b * p.batch_x;
-  for (uint64_t i = beg + threadIdx.x; i < end; i += kNormThreads) {
-    const uint32_t r = uint32_t(i / chunks), c = uint32_t(i - uint64_t(r) * chunks);
-    uint32_t w[T::kWords];
-    f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes, p.n - int(c * 8), p.wide != 0, w);
-    uint32_t o[4];
+#pragma unroll 1
+  for (uint32_t i0 = beg + threadIdx.x; i0 < end; i0 += kNormThreads * kNormUnroll) {
+    uint32_t w[kNormUnroll][T::kWords];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      o[j] = half2_bits(T::value(w, 2 * j) * p1 * p2, T::value(w, 2 * j + 1) * p1 * p2);
-    *reinterpret_cast<uint4*>(x + int64_t(r) * p.ld_x + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < kNormUnroll; ++k) {
+      const uint32_t i = i0 + k * kNormThreads, r = i / chunks, c = i - r * chunks;
+      f8::load8<T>(g + (int64_t(r) * p.ld_g + c * 8) * T::kBytes,
+                   i < end ? p.n - int(c * 8) : 0, p.wide != 0, w[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kNormUnroll; ++k) {
+      const uint32_t i = i0 + k * kNormThreads, r = i / chunks, c = i - r * chunks;
+      if (i >= end) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = half2_bits(T::value(w[k], 2 * j) * p1 * p2, T::value(w[k], 2 * j + 1) * p1 * p2);
+      *reinterpret_cast<uint4*>(x + int64_t(r) * p.ld_x + c * 8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
@@ -543,7 +675,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_start_kernel(const NormArgs p
 // ---------------------------------------------------------------------------
 static uint64_t round_up(uint64_t a, uint64_t b) { return (a + b - 1) / b * b; }
 
-constexpr uint32_t kMaxParts = 128;  // CTAs that share a matrix's norm
+constexpr uint32_t kMaxParts = 1024;  // CTAs that share a matrix's norm
 
 struct Layout {
   int64_t ldx, ldd;                        // elements
@@ -666,11 +798,11 @@ static int product(const Operand& A, const Operand& B, uint64_t batch, uint64_t 
     const uint64_t tm = (M + t - 1) / t, tn = (N + t - 1) / t;
     return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
   };
-  // in units of the time of a 128-wide tile on one SM: a pair's tile takes
-  // twice that
+  // in units of the time of a 128-wide tile on one SM: a pair's tile, four times
+  // the work on two SMs, takes 1.7 times that
   const uint64_t t128 = (tiles(128) + dev.num_sms - 1) / dev.num_sms;
   const uint64_t t256 = (tiles(256) + dev.num_sms / 2 - 1) / (dev.num_sms / 2) * 2;
-  const bool pair = tile ? tile == 256 : t256 <= t128;
+  const bool pair = tile ? tile == 256 : t256 * 17 <= t128 * 20;
   const uint64_t bn = pair ? 256 : 128;
   const int ka = pair ? 1 : 2;
   CUtensorMap map[2];
@@ -730,7 +862,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   if (!G || ga % uintptr_t(gs) != 0 || (m > 1 && ldg < n) ||
       (batch > 1 && batch_stride_g < (m - 1) * ldg + n))
     return SWZ_EINVAL;
-  if (!Y || reinterpret_cast<uintptr_t>(Y) % uintptr_t(ys) != 0 || (m > 1 && ldy < n) ||
+  const uintptr_t ya = reinterpret_cast<uintptr_t>(Y);
+  if (!Y || ya % uintptr_t(ys) != 0 || (m > 1 && ldy < n) ||
       (batch > 1 && batch_stride_y < (m - 1) * ldy + n))
     return SWZ_EINVAL;
   // the range of singular values, step by step, gives the powers of two
@@ -766,9 +899,9 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   na.n = n;
   na.wide = ga % 16 == 0 && (m == 1 || (na.ld_g * gs) % 16 == 0) &&
             (batch == 1 || (na.batch_g * gs) % 16 == 0);
-  // at least 1024 chunks of 8 values a CTA, and no more CTAs than fill the GPU
+  // no more CTAs than fill the GPU
   const uint64_t chunks = (uint64_t(n) + 7) / 8 * uint64_t(m);
-  uint64_t parts = (chunks + 1023) / 1024;
+  uint64_t parts = (chunks + 1023) / 1024;  // one round of kNormUnroll chunks a thread
   const uint64_t fill = (uint64_t(dev.num_sms) * 4 + batch - 1) / batch;
   if (parts > fill) parts = fill;
   if (parts > kMaxParts) parts = kMaxParts;
@@ -793,6 +926,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   base.ld_g = na.ld_g;
   base.batch_g = na.batch_g;
   base.g_dtype = dtype;
+  base.g_wide = na.wide;
   base.ld_master = L.ldx;
   base.batch_master = int64_t(m) * L.ldx;
   base.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
@@ -866,6 +1000,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
       p.ld_y = m > 1 ? ldy : n;
       p.batch_y = batch > 1 ? batch_stride_y : 0;
       p.y_dtype = y_dtype;
+      p.y_wide = ya % 16 == 0 && (m == 1 || (p.ld_y * ys) % 16 == 0) &&
+                 (batch == 1 || (p.batch_y * ys) % 16 == 0);
     } else {
       ex = room(hi[i + 1] * 1.01, 12);
       p.out = xs[(i + 1) & 1];
