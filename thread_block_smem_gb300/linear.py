@@ -96,6 +96,7 @@ def swz_newton_schulz_workspace_size(batch, m, n):
 # A call on small tensors costs the host more than the GPU, so what every call
 # needs is looked up once: torch, the type codes, the library.
 torch = None
+_u64 = ctypes.c_uint64
 _codes = _f8_codes = _f8_types = _L = None
 
 
@@ -151,9 +152,9 @@ def _handle(stream, x):
 
 def _empty(shape, dtype, x, stream):
     if stream is None:
-        return x.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=x.device)
     with _on(stream):
-        return x.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=x.device)
 
 
 def _block(block):
@@ -192,7 +193,7 @@ def _matrix(q, scales, block, what):
     want = (_blocks(k), m) if block == SWZ_BLOCK_ROW else (_blocks(m), _blocks(k))
     if scales.shape != want:
         raise ValueError(f"{what}: scales of shape {want} expected, got {tuple(scales.shape)}")
-    _, _, lds = _rows(scales, f"{what} scales")
+    _, _, lds = _rows(scales, what)
     return swz_fp8_matrix(at, ld, scales.data_ptr(), lds, fmt, block), m, k
 
 
@@ -277,12 +278,15 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
     if K != K2:
         raise ValueError("inner dimensions differ")
     y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x, stream)
-    rc, need = swz_linear_fp8_workspace_size(M, N, K)
-    _swz._check(rc, "swz_linear_fp8_workspace_size")
-    ws = _empty((need,), torch.uint8, x, stream) if need else None
-    _swz._check(_L.swz_linear_fp8(x.data_ptr(), code, ldx, W, y.data_ptr(), ldy, ycode, M, N, K,
-                                  None if ws is None else ws.data_ptr(), need, _handle(stream, x)),
-                "swz_linear_fp8")
+    need = _u64()
+    rc = _L.swz_linear_fp8_workspace_size(M, N, K, need)
+    if rc == 0:
+        need = need.value
+        ws = _empty(need, torch.uint8, x, stream) if need else None
+        rc = _L.swz_linear_fp8(x.data_ptr(), code, ldx, W, y.data_ptr(), ldy, ycode, M, N, K,
+                               ws.data_ptr() if need else None, need, _handle(stream, x))
+    if rc:
+        raise _swz.SwzError(rc, "swz_linear_fp8")
     return y
 
 
