@@ -59,6 +59,19 @@ def test_shapes(swz, shape, tile):
         check(Y, G)
 
 
+# the one-kernel form's ranges: 1 to 8 ranks, 64 to 256 columns each, both ways round
+@pytest.mark.parametrize("shape", [(128, 64), (40, 129), (128, 257), (300, 128), (64, 513), (1024, 33),
+                                   (100, 1025), (128, 2048), (2048, 128), (5, 1999), (128, 2049),
+                                   (3, 90, 700), (2, 700, 90)])
+def test_one_kernel_shapes(swz, shape):
+    G = normal(shape, torch.float32, sum(shape))
+    Y = swz.newton_schulz(G.cuda(), out_dtype=torch.float32)
+    swz.check_status()
+    check(Y, G)
+    other = swz.newton_schulz(G.cuda(), out_dtype=torch.float32, tile=128)
+    check(other, G)
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 10])
 @pytest.mark.parametrize("shape", [(60, 200), (200, 60)])
 def test_steps(swz, shape, steps):
@@ -164,9 +177,10 @@ def test_stream_and_graph(swz):
     assert torch.equal(out, swz.newton_schulz(G2))
 
 
-@pytest.mark.parametrize("tile", [128, 256])
-def test_timeout_is_reported(swz, tile):
-    G = normal((300, 200), torch.float32, 8).cuda()
+@pytest.mark.parametrize("tile,shape", [(128, (300, 200)), (256, (300, 200)), (0, (100, 60)),
+                                        (0, (100, 600))])
+def test_timeout_is_reported(swz, tile, shape):
+    G = normal(shape, torch.float32, 8).cuda()
     want = swz.newton_schulz(G)
     swz.newton_schulz(G, tile=tile, debug_flags=swz.SWZ_DEBUG_SKIP_FIRST_LOAD, timeout_ms=20)
     with pytest.raises(swz.SwzError) as e:

@@ -21,8 +21,10 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libswz.so")
 SOURCES = ["capi.cu", "transpose.cu", "gemm.cu", "l2_model.cpp", "noalloc.cu", "die.cu",
            "host_pipeline.cu", "gemm_mma_sync.cu", "tc_rate.cu", "ops.cu", "quantize.cu",
-           "gemm_fp8.cu", "gemm_fp8_rows.cu", "linear_fp8.cu", "newton_schulz.cu"]
-HEADERS = ["common.h", "ptx.cuh", "tile_order.cuh", "ops.h", "pipe.cuh", "f8.cuh"]
+           "gemm_fp8.cu", "gemm_fp8_rows.cu", "linear_fp8.cu", "newton_schulz.cu",
+           "newton_schulz_small.cu"]
+HEADERS = ["common.h", "ptx.cuh", "tile_order.cuh", "ops.h", "pipe.cuh", "f8.cuh",
+           "newton_schulz.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

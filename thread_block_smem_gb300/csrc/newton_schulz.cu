@@ -34,6 +34,7 @@
 
 #include "common.h"
 #include "f8.cuh"
+#include "newton_schulz.cuh"
 #include "ops.h"
 #include "pipe.cuh"
 #include "tile_order.cuh"
@@ -67,13 +68,6 @@ enum Mode : int {
 // X as the a X term reads it
 enum Source : int { kFromG = 0, kFromF32 = 1, kFromF16 = 2 };
 
-// per matrix of the batch: X = G * p1 * p2 * f, and the first fp16 X is G * p1
-// * p2; a later fp16 X is X times the step's power of two times `up`, a power
-// of two above 1 when |G| is so far below eps that X is tiny (down = 1 / up)
-struct Scale {
-  float p1, p2, f, up, down;
-};
-
 struct Params {
   int mode;
   uint32_t a_mn, b_mn;          // operands given K x rows
@@ -106,23 +100,6 @@ struct Params {
   uint64_t timeout_ns;
   uint32_t debug_flags;
 };
-
-__device__ __forceinline__ float load_any(const uint8_t* p, int64_t at, int dtype) {
-  if (dtype == SWZ_F32) return __ldg(reinterpret_cast<const float*>(p) + at);
-  if (dtype == SWZ_BF16)
-    return __bfloat162float(__ushort_as_bfloat16(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
-  return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
-}
-__device__ __forceinline__ void store_any(uint8_t* p, int64_t at, float v, int dtype) {
-  if (dtype == SWZ_F32) reinterpret_cast<float*>(p)[at] = v;
-  else if (dtype == SWZ_BF16) reinterpret_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
-  else reinterpret_cast<__half*>(p)[at] = __float2half_rn(v);
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 v = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 __device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -549,7 +526,7 @@ struct NormArgs {
   uint32_t parts;        // CTAs of a matrix
   double* partial;       // [batch][parts][3]
   double eps;
-  double headroom;       // |G| / (|G| + eps) below this leaves room to scale X up
+  double headroom;       // see make_scale
   Scale* scale;
   __half* x;             // first fp16 X
   int64_t ld_x, batch_x;
@@ -617,25 +594,7 @@ __global__ void __launch_bounds__(kNormThreads) ns_start_kernel(const NormArgs p
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) d[k] += __shfl_xor_sync(0xFFFFFFFFu, d[k], o);
     if (threadIdx.x == 0) {
-      // the scale whose squares neither overflowed nor underflowed
-      double norm;
-      if (!(d[0] < 1e36)) norm = sqrt(d[1]) * 0x1p80;
-      else if (d[0] > 1e-30) norm = sqrt(d[0]);
-      else norm = sqrt(d[2]) * 0x1p-80;
-      // the largest power of two 2^e with norm * 2^e <= sqrt(m n), or half it
-      int e = 0;
-      if (norm > 0.0 && norm < 1e300)
-        e = ilogb(double(p.m) * double(p.n)) / 2 - ilogb(norm) - 1;
-      const double div = norm + p.eps;
-      sc.p1 = ldexpf(1.f, e / 2);
-      sc.p2 = ldexpf(1.f, e - e / 2);
-      sc.f = div > 0.0 ? float(ldexp(1.0, -e) / div) : (div == 0.0 ? 0.f : float(div));
-      // X grows from |G| / (|G| + eps) by known factors, its bound by others
-      int z = 0;
-      if (norm > 0.0 && norm < div * p.headroom) z = ilogb(p.headroom) + ilogb(div) - ilogb(norm) - 2;
-      z = z < 0 ? 0 : z > 126 ? 126 : z;
-      sc.up = ldexpf(1.f, z);
-      sc.down = ldexpf(1.f, -z);
+      sc = make_scale(d, double(p.m) * double(p.n), p.eps, p.headroom);
       if (part == 0) p.scale[b] = sc;
     }
   }
@@ -850,7 +809,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
                                  uint64_t workspace_bytes, void* stream) {
   swz_newton_schulz_opts o = {};
   if (opts) o = *opts;
-  if (!sizes_ok(batch, m, n) || steps < 1 || steps > 64) return SWZ_EINVAL;
+  if (!sizes_ok(batch, m, n) || steps < 1 || steps > kMaxSteps) return SWZ_EINVAL;
   for (int d : {dtype, y_dtype})
     if (d != SWZ_F16 && d != SWZ_BF16 && d != SWZ_F32) return SWZ_EINVAL;
   if (!(eps >= 0.0) || !isfinite(eps) || !isfinite(a) || !isfinite(b) || !isfinite(c))
@@ -868,7 +827,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     return SWZ_EINVAL;
   // the range of singular values, step by step, gives the powers of two
   // and how far below them X can stay: hi over the largest growth, in all steps
-  double hi[65], grown = 1.0, headroom = 1.0;
+  double hi[kMaxSteps + 1], grown = 1.0, headroom = 1.0;
   hi[0] = 1.0;
   for (int i = 0; i < steps; ++i) {
     hi[i + 1] = 1.01 * poly_max(a, b, c, hi[i]);
@@ -879,6 +838,17 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     grown *= 1.01 * g;
     if (grown > 0) headroom = fmin(headroom, hi[i + 1] / grown);
   }
+  // powers of two that keep X, A and B in the range of fp16, by step
+  int ex[kMaxSteps], ea[kMaxSteps], eb[kMaxSteps];
+  for (int i = 0; i < steps; ++i) {
+    const double h2 = hi[i] * hi[i] * 1.01;
+    ex[i] = i == 0 ? 0 : room(hi[i] * 1.01, 12);  // the first X goes by its Scale
+    ea[i] = room(h2, 14);
+    // largest |b t + c t^2| on [0, h2]
+    double bmax = fabs(h2 * (b + c * h2));
+    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < h2) bmax = fmax(bmax, b * b / (4 * fabs(c)));
+    eb[i] = room(1.01 * bmax, 14);
+  }
   const Layout L = layout(uint64_t(batch), uint64_t(m), uint64_t(n));
   const uintptr_t wsa = reinterpret_cast<uintptr_t>(d_workspace);
   if (!wsa || (wsa & 255u) || workspace_bytes < L.total) return SWZ_EINVAL;
@@ -887,8 +857,41 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   if (rc != SWZ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  const uint64_t timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
   const bool wide = m <= n;
   const uint64_t d = uint64_t(wide ? m : n);
+
+  const bool small = o.tile == 0 && d <= kSmallSide && (wide ? n : m) <= kSmallLong;
+  if (small) {
+    SmallParams p{};
+    p.g = static_cast<const uint8_t*>(G);
+    p.ld_g = m > 1 ? ldg : n;
+    p.batch_g = batch > 1 ? batch_stride_g : 0;
+    p.g_dtype = dtype;
+    p.y = static_cast<uint8_t*>(Y);
+    p.ld_y = m > 1 ? ldy : n;
+    p.batch_y = batch > 1 ? batch_stride_y : 0;
+    p.y_dtype = y_dtype;
+    p.wide = wide;
+    p.d = int(d);
+    p.len = wide ? n : m;
+    p.steps = steps;
+    p.eps = eps;
+    p.headroom = headroom;
+    p.debug_flags = o.debug_flags;
+    p.timeout_ns = timeout_ns;
+    rc = op_status_word(&p.status);
+    if (rc != SWZ_OK) return rc;
+    for (int i = 0; i < steps; ++i) {
+      p.fa[i] = float(exp2(double(ea[i] - 2 * ex[i])));
+      p.ub[i] = float(b * exp2(double(eb[i] - ea[i])));
+      p.fb[i] = float(c * exp2(double(eb[i] - 2 * ea[i])));
+      p.k1[i] = float(exp2(double(-eb[i] - ex[i])));
+      p.sx[i] = float(exp2(double(ex[i])));
+      p.ad[i] = float(a * exp2(double(eb[i])));
+    }
+    return launch_small(p, batch, s);
+  }
 
   NormArgs na{};
   na.g = static_cast<const uint8_t*>(G);
@@ -929,7 +932,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   base.g_wide = na.wide;
   base.ld_master = L.ldx;
   base.batch_master = int64_t(m) * L.ldx;
-  base.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  base.timeout_ns = timeout_ns;
   base.debug_flags = o.debug_flags;
   base.scale = na.scale;
   rc = op_status_word(&base.status);
@@ -941,19 +944,11 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   float* const master = reinterpret_cast<float*>(ws + L.master);
   // steps that take the a X term in fp32 (the first takes G itself in any case)
   const int masters = steps - 2;
-  int ex = 0;                     // the fp16 X is X * 2^ex (after the first step)
   for (int i = 0; i < steps; ++i) {
     __half* const x = xs[i & 1];
     const Operand xk{x, uint64_t(m), uint64_t(n), L.ldx, false};   // rows of X along K
     const Operand xm{x, uint64_t(m), uint64_t(n), L.ldx, true};
     const Operand ak{Am, d, d, L.ldd, false}, bk{Bm, d, d, L.ldd, false};
-    const double h2 = hi[i] * hi[i] * 1.01;
-    const int ea = room(h2, 14);
-    // largest |b t + c t^2| on [0, h2]
-    double bmax = fabs(h2 * (b + c * h2));
-    if (c != 0 && -b / (2 * c) > 0 && -b / (2 * c) < h2) bmax = fmax(bmax, b * b / (4 * fabs(c)));
-    const int eb = room(1.01 * bmax, 14);
-
     Params p = base;
     p.mode = kGram;
     p.M = p.N = int(d);
@@ -961,7 +956,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     p.ld_out = L.ldd;
     p.batch_out = int64_t(d) * L.ldd;
     p.first = i == 0;
-    p.f = float(exp2(double(ea - (i == 0 ? 0 : 2 * ex))));
+    p.f = float(exp2(double(ea[i] - 2 * ex[i])));
     rc = wide ? product(xk, xk, uint64_t(batch), uint64_t(n), p, dev, o.tile, s)
               : product(xm, xm, uint64_t(batch), uint64_t(m), p, dev, o.tile, s);
     if (rc != SWZ_OK) return rc;
@@ -976,8 +971,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     p.out = Bm;
     p.ld_out = L.ldd;
     p.batch_out = int64_t(d) * L.ldd;
-    p.u = float(b * exp2(double(eb - ea)));
-    p.f = float(c * exp2(double(eb - 2 * ea)));
+    p.u = float(b * exp2(double(eb[i] - ea[i])));
+    p.f = float(c * exp2(double(eb[i] - 2 * ea[i])));
     rc = product(ak, ak, uint64_t(batch), d, p, dev, o.tile, s);
     if (rc != SWZ_OK) return rc;
 
@@ -988,8 +983,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     p.N = n;
     p.first = i == 0;
     p.a = float(a);
-    p.u = float(exp2(-double(ex)));
-    p.f = float(exp2(-double(eb) - (i == 0 ? 0.0 : double(ex))));
+    p.u = float(exp2(-double(ex[i])));
+    p.f = float(exp2(double(-eb[i] - ex[i])));
     p.source = i == 0 ? kFromG : i < masters ? kFromF32 : kFromF16;
     p.in = x;
     p.ld_in = L.ldx;
@@ -1003,11 +998,10 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
       p.y_wide = ya % 16 == 0 && (m == 1 || (p.ld_y * ys) % 16 == 0) &&
                  (batch == 1 || (p.batch_y * ys) % 16 == 0);
     } else {
-      ex = room(hi[i + 1] * 1.01, 12);
       p.out = xs[(i + 1) & 1];
       p.ld_out = L.ldx;
       p.batch_out = int64_t(m) * L.ldx;
-      p.out_scale = float(exp2(double(ex)));
+      p.out_scale = float(exp2(double(ex[i + 1])));
       p.master_out = i + 1 < masters ? master : nullptr;
     }
     rc = wide ? product(bk, xm, uint64_t(batch), d, p, dev, o.tile, s)
