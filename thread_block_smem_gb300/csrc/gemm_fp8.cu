@@ -468,7 +468,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       free_slot();
       if (aborted) break;
       if (PAIR || p.split == 1) {
-        if (p.c_align >= 16) {
+        if ((BROW || !PAIR) && p.c_align >= 32 && col0 + COLS <= p.N) {
+          // Whole lines of C: 32 rows of 128 bytes (one of 16-bit values, two
+          // of fp32) at a time.  2 to 5 % of 8192^3; the pair with square blocks,
+          // whose sums' loop it leaves fewer registers, is 5 % slower with it.
+          static_assert(COLS == 64, "a row of 16-bit results is 128 bytes");
+          const int64_t r0 = row - lane + (lane / 4) * 4;
+          const int parts = p.c_dtype == SWZ_F32 ? 2 : 1;
+          const int64_t line = p.ldc * (p.c_dtype == SWZ_F32 ? 4 : 2);
+          uint8_t* const at = static_cast<uint8_t*>(p.C) + r0 * line +
+                              col0 * (p.c_dtype == SWZ_F32 ? 4 : 2) + (lane % 4) * 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h >= parts) break;
+            uint32_t o[32];
+            if (p.c_dtype == SWZ_F32) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                float a, b;
+                pipe::unpack2(acc[h * 16 + j], a, b);
+                o[2 * j] = __float_as_uint(a);
+                o[2 * j + 1] = __float_as_uint(b);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                float a, b;
+                pipe::unpack2(acc[j], a, b);
+                o[j] = pack_out(a, b, p.c_dtype);
+              }
+            }
+            pipe::quad_transpose(o, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (r0 + j < p.M) pipe::st_global_32b(at + j * line + h * 128, o + 8 * j);
+          }
+        } else if (p.c_align >= 16) {
 #pragma unroll
           for (int c = 0; c < COLS / 16; ++c) {
             const int64_t n = col0 + c * 16;

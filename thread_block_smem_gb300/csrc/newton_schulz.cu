@@ -95,7 +95,7 @@ struct Params {
   int g_dtype, g_wide;          // g_wide: rows start on 16 bytes
   uint8_t* y;                   // the caller's result in the last step, else NULL
   int64_t ld_y, batch_y;
-  int y_dtype, y_wide;
+  int y_dtype, y_wide, y_lines; // rows start on 16 bytes, on 32
   unsigned int* status;
   uint64_t timeout_ns;
   uint32_t debug_flags;
@@ -314,6 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const TileCoord t = tile_at(w, b);
       const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
       const bool row_in = row < p.M;
+      // rows of 128 bytes as a warp loads and stores them (quad_transpose)
+      const int64_t line0 = row - lane + (lane / 4) * 4;
+      const uint32_t piece = lane % 4;
       const Scale sc = p.scale[b];
       const float fx = p.first ? sc.f : sc.down;  // X over the fp16 X's power of two
       const float f = p.mode == kPoly ? p.f : p.mode == kGram ? p.f * fx * fx : p.f * fx;
@@ -326,38 +329,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.mode == kGram) {
 #pragma unroll
           for (int j = 0; j < 64; ++j) v[j] = 0.f;
-        } else if (p.mode == kPoly || p.source != kFromG) {
-          const bool from16 = p.mode == kPoly || p.source == kFromF16;
+        } else if (p.mode == kPoly || p.source == kFromF16) {
+          uint32_t x[32];
+          const __half* src = p.in + b * p.batch_in + line0 * p.ld_in + col0 + piece * 16;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int64_t col = col0 + c * 16;
-            const bool in = row_in && col < p.N;
-            if (from16) {
-              const uint4* src =
-                  reinterpret_cast<const uint4*>(p.in + b * p.batch_in + row * p.ld_in + col);
+          for (int j = 0; j < 4; ++j) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint4 x = in ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+            for (int k = 0; k < 8; ++k) x[8 * j + k] = 0u;
+            if (line0 + j < p.M && col0 + piece * 16 < p.N)
+              pipe::ld_global_8(src + j * p.ld_in, x + 8 * j);
+          }
+          pipe::quad_transpose(x, lane);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&e[j]));
-                  v[c * 16 + 8 * k + 2 * j] = u16 * z.x;
-                  v[c * 16 + 8 * k + 2 * j + 1] = u16 * z.y;
-                }
-              }
-            } else {
-              const float4* src = reinterpret_cast<const float4*>(
-                  p.master_in + b * p.batch_master + row * p.ld_master + col);
+          for (int j = 0; j < 32; ++j) {
+            const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&x[j]));
+            v[2 * j] = u16 * z.x;
+            v[2 * j + 1] = u16 * z.y;
+          }
+        } else if (p.source == kFromF32) {
+          const float* src = p.master_in + b * p.batch_master + line0 * p.ld_master + col0 + piece * 8;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 x = in ? src[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-                v[c * 16 + 4 * k] = p.a * x.x;
-                v[c * 16 + 4 * k + 1] = p.a * x.y;
-                v[c * 16 + 4 * k + 2] = p.a * x.z;
-                v[c * 16 + 4 * k + 3] = p.a * x.w;
-              }
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[8 * j + k] = 0u;
+              if (line0 + j < p.M && col0 + c * 32 + piece * 8 < p.N)
+                pipe::ld_global_8(src + j * p.ld_master + c * 32, x + 8 * j);
             }
+            pipe::quad_transpose(x, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[c * 32 + j] = p.a * __uint_as_float(x[j]);
           }
         } else {
           // G: rows that start on 16 bytes eight values at a time, others with
@@ -365,7 +368,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float g1 = p.a * sc.p1, g2 = sc.p2 * sc.f;
           const int es = p.g_dtype == SWZ_F32 ? 4 : 2;
           const uint8_t* g = p.g + (b * p.batch_g) * es;
-          if (p.g_wide) {
+          if (p.g_wide && col0 + 64 <= p.N) {
+            // whole lines: one of 16-bit values, two of fp32
+            const uint8_t* src = g + (line0 * p.ld_g + col0) * es + piece * 32;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (c == 1 && es == 2) break;
+              uint32_t x[32];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[8 * j + k] = 0u;
+                if (line0 + j < p.M) pipe::ld_global_8(src + j * p.ld_g * es + c * 128, x + 8 * j);
+              }
+              pipe::quad_transpose(x, lane);
+              if (es == 4) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[c * 32 + j] = __uint_as_float(x[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                  v[j] = p.g_dtype == SWZ_BF16 ? f8::Bf16::value(x, j) : f8::F16::value(x, j);
+              }
+            }
+          } else if (p.g_wide) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const int64_t col = col0 + c * 8;
@@ -431,7 +457,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           // lane a column
           const int es = p.y_dtype == SWZ_F32 ? 4 : 2;
           uint8_t* y = p.y + (b * p.batch_y) * es;
-          if (p.y_wide) {
+          if (p.y_lines && col0 + 64 <= p.N) {
+            uint8_t* to = y + (line0 * p.ld_y + col0) * es + piece * 32;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (c == 1 && es == 2) break;
+              uint32_t x[32];
+              if (es == 4) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(v[c * 32 + j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  x[j] = p.y_dtype == SWZ_BF16 ? bf2_bits(v[2 * j], v[2 * j + 1])
+                                               : half2_bits(v[2 * j], v[2 * j + 1]);
+              }
+              pipe::quad_transpose(x, lane);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (line0 + j < p.M) pipe::st_global_32b(to + j * p.ld_y * es + c * 128, x + 8 * j);
+            }
+          } else if (p.y_wide) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const int64_t col = col0 + c * 8;
@@ -471,33 +517,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           continue;
         }
+        if (p.master_out) {
+          float* dst = p.master_out + b * p.batch_master + line0 * p.ld_master + col0 + piece * 8;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int64_t col = col0 + c * 16;
-          if (!row_in || col >= p.N) continue;
-          const float* x = v + c * 16;
-          if (p.master_out) {
-            float4* dst = reinterpret_cast<float4*>(p.master_out + b * p.batch_master +
-                                                    row * p.ld_master + col);
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          }
-          uint32_t o[8];
+            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(v[c * 32 + j]);
+            pipe::quad_transpose(x, lane);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o[j] = half2_bits(x[2 * j] * out_scale, x[2 * j + 1] * out_scale);
-          __half* out = p.out + b * p.batch_out;
-          pipe::st_global_32b(out + row * p.ld_out + col, o);
-          if (sym && t.m != t.n) {
-            // the other half: lanes are neighbours along its rows
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (col + j < p.N)
-                reinterpret_cast<uint16_t*>(out)[(col + j) * p.ld_out + row] =
-                    uint16_t(j & 1 ? o[j / 2] >> 16 : o[j / 2]);
+            for (int j = 0; j < 4; ++j)
+              if (line0 + j < p.M && col0 + c * 32 + piece * 8 < p.N)
+                pipe::st_global_32b(dst + j * p.ld_master + c * 32, x + 8 * j);
           }
         }
+        uint32_t o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          o[j] = half2_bits(v[2 * j] * out_scale, v[2 * j + 1] * out_scale);
+        __half* out = p.out + b * p.batch_out;
+        if (sym && t.m != t.n) {
+          // The other half: lanes are neighbours along its rows.  Two lanes
+          // swap a value of each column pair, so that each stores two rows'
+          // values of one of the columns (one value a store took twice as long)
+          __half* const to = out + (col0 + (lane & 1u)) * p.ld_out + (row & ~int64_t(1));
+          const bool in = (row & ~int64_t(1)) < p.M;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t got =
+                __shfl_xor_sync(0xFFFFFFFFu, (lane & 1u) ? o[k] & 0xFFFFu : o[k] >> 16, 1);
+            const uint32_t two = (lane & 1u) ? got | (o[k] & 0xFFFF0000u)
+                                             : (o[k] & 0xFFFFu) | (got << 16);
+            if (in && col0 + 2 * k + (lane & 1u) < p.N)
+              *reinterpret_cast<uint32_t*>(to + 2 * k * p.ld_out) = two;
+          }
+        }
+        __syncwarp();
+        pipe::quad_transpose(o, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (line0 + j < p.M && col0 + piece * 16 < p.N)
+            pipe::st_global_32b(out + (line0 + j) * p.ld_out + col0 + piece * 16, o + 8 * j);
       }
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
@@ -997,6 +1057,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
       p.y_dtype = y_dtype;
       p.y_wide = ya % 16 == 0 && (m == 1 || (p.ld_y * ys) % 16 == 0) &&
                  (batch == 1 || (p.batch_y * ys) % 16 == 0);
+      p.y_lines = p.y_wide && ya % 32 == 0 && (m == 1 || (p.ld_y * ys) % 32 == 0) &&
+                  (batch == 1 || (p.batch_y * ys) % 32 == 0);
     } else {
       p.out = xs[(i + 1) & 1];
       p.ld_out = L.ldx;

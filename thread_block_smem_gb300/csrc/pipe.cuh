@@ -239,8 +239,38 @@ __device__ __forceinline__ void transpose32(float (&v)[32], uint32_t lane) {
   }
 }
 
+// Rows of 128 bytes held a row a lane (four pieces of 32 bytes, v[8 c ..] the
+// c-th), to and from the order in which a warp stores and loads them: lane l
+// then has piece l mod 4 of the rows 4 (l / 4) + j, v[8 j ..] the j-th.  An
+// access of the warp is 8 whole lines instead of a quarter of 32, which costs
+// the load-store unit a quarter of the time.  Its own inverse.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[32], uint32_t lane) {
+#pragma unroll
+  for (uint32_t s = 2; s > 0; s /= 2) {
+    const bool high = (lane & s) != 0;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c) {
+      if (c & s) continue;
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        uint32_t &a = v[8 * c + k], &b = v[8 * (c | s) + k];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? a : b, s);
+        if (high) a = got;
+        else b = got;
+      }
+    }
+  }
+}
+
+// Eight words from a 16-byte aligned global address.
+__device__ __forceinline__ void ld_global_8(const void* p, uint32_t* v) {
+  const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
 // 32 bytes to a 32-byte aligned global address in one instruction.
-__device__ __forceinline__ void st_global_32b(void* p, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
