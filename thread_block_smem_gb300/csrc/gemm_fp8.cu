@@ -5,27 +5,35 @@
 // A (M x K) has row blocks (1 x 128); B (N x K) square (128 x 128) or row
 // blocks.  Both K-major, e4m3 or e5m2 each; C fp32, bf16 or fp16.
 //
-// Mathematics and split: the tensor core sums the 128 products of a block
-// exactly scaled operands in fp32; the sum of a block is scaled and added to
-// fp32 accumulators in registers.  So every block of K is an MMA accumulation
-// of its own, and its tile is read back from TMEM, multiplied and added.
-//   * One CTA per SM.  BN / 16 summing warps (warp w: TMEM lanes 32 (w mod 4)
-//     .., columns 64 (w / 4) .. of the tile), then a TMA producer, a warp for
-//     TMEM allocation and (one lane) MMA issue, and one for the scales.  Half
-//     the summing warps with 128 columns each could not hide TMEM's latency:
-//     @@
-//   * The scales go through a ring of shared memory of their own, 12 blocks
-//     deep: loaded by the summing warps themselves, two blocks ahead,
-//     each block cost an L2 round trip (876 SM cycles for a 128 x 128 tile
-//     whose MMAs take 256).  4-byte copies: rows of scales start anywhere.
-//   * TMEM holds 512 / BN tiles in turn, so the tensor core runs ahead of the
-//     readers; a stage of shared memory is one block of K (128 bytes a row).
-//   * CTA pair (256 x 256): each CTA loads its 128 rows of A and half of B
-//     and sums 128 x 256 of C; one CTA: 128 x 128.
+// Mathematics and split: the tensor core sums a block's 128 products in fp32;
+// the sum is scaled and added to fp32 accumulators in registers.  So every
+// block of K is an MMA accumulation of its own, and its tile is read back from
+// TMEM, multiplied and added.
+//   * One CTA per SM, 12 warps: 0-7 the sums (warp w: TMEM lanes 32 (w mod 4)
+//     .., columns 64 (w / 4) .. of the tile), 8 TMA producer, 9 and 10 MMA
+//     issue (9 also TMEM allocation), 11 scales.
+//   * Tiles of 128 columns: TMEM holds four in turn, so the tensor core runs
+//     ahead of the readers; a stage of shared memory is one block of K (128
+//     bytes a row).  CTA pair: 256 x 128 (each CTA 128 rows of A and 64 of B),
+//     one CTA: 128 x 128.  256-column tiles leave two TMEM buffers: a block's
+//     MMAs (512 cycles) then wait for a whole hand-over, 8192^3 in 467 us
+//     against 410-425.
+//   * Scales go through a ring of shared memory of their own, 12 blocks deep:
+//     loaded by the summing warps themselves, two blocks ahead, each block cost
+//     an L2 round trip.  4-byte copies: rows of scales start anywhere.
 //   * split: a cluster of 2, 4 or 8 CTAs shares one 128 x 128 tile by ranges
 //     of K and adds the partial tiles through distributed shared memory in
 //     rank order (deterministic, no workspace): for few tiles.
 //   * tiles are dealt out by the framework's tile orders, w = cluster + i P.
+//
+// What bounds it: the summing warps.  A 128 x 128 tile's MMAs take 256 cycles
+// a block; waits, TMEM loads, release and 64 FMAs a thread take 440 to 480, and
+// 16 warps of half the columns the same.  With a quarter of the MMAs 8192^3
+// takes 392 us, with half the operand traffic as well the same.  Measured at
+// 8192^3, bf16 result: 410-425 us, 2.6-2.7 PFLOP/s, 0.70 of twice the measured
+// bf16 peak; B in row blocks (a scale a column: twice the arithmetic, and 16
+// shared-memory reads) 650 us.  A variant for row blocks in TMEM's 16-lane
+// order, which reads a quarter of the scales, took 697.
 #include <mutex>
 #include <type_traits>
 
@@ -38,33 +46,31 @@
 namespace swz {
 namespace gemm8 {
 
-constexpr int BM = 128, BK = 128;
+constexpr int BM = 128, BN = 128, BK = 128;
 constexpr int kMath = 8;       // summing warps
 constexpr int kIssuers = 2;    // warps that issue MMAs, a block of K each in turn
 constexpr int kThreads = (kMath + 2 + kIssuers) * 32;
-// Registers of the pair's kernel: 384 threads are launched with 168 each,
-// 64512 in all; the four warps that only issue copies and MMAs give some up
-// for the summing warps (128 sums and 64 columns in flight): 256 * 208 + 128 *
-// 88 = 64512.
-constexpr int kMathRegs = 208, kIssueRegs = 88;
 constexpr int kScaleKb = 4;    // blocks of K whose scales share a slot of the ring
 
-template <int BN, bool PAIR>
+constexpr int COLS = 4 * BN / kMath;  // columns a summing warp holds
+static_assert(COLS == 64, "two TMEM loads of 32 columns");
+
+template <bool PAIR>
 struct Cfg {
   static constexpr int CG = PAIR ? 2 : 1;
-  static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // rows of B this CTA loads
+  static constexpr int BN_LOCAL = BN / CG;  // rows of B this CTA loads
   static constexpr int A_BYTES = BM * BK, B_BYTES = BN_LOCAL * BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = PAIR && BN == 128 ? 8 : 6;
-  static constexpr int NBUF = 512 / BN;
-  static constexpr int COLS = 4 * BN / kMath;     // columns a summing warp holds
+  static constexpr int STAGES = PAIR ? 8 : 6;
+  static constexpr int NBUF = 512 / BN;   // tiles of TMEM
   static constexpr int SLOTS = 3;         // ring of scales: 128 of A's rows, then B's,
   static constexpr int SLOT = BM + BN;    // floats, of kScaleKb blocks
   static constexpr int BARS = 2 * STAGES + 2 * NBUF + 2 * SLOTS + kIssuers;
   static constexpr int SMEM_BYTES =
       1024 + STAGES * STAGE_BYTES + SLOTS * kScaleKb * SLOT * 4 + BARS * 8 + 16;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(STAGES * STAGE_BYTES >= BM * BN * 4 || PAIR, "a partial tile fits the ring");
+  static_assert(STAGES % kIssuers == 0 && NBUF % kIssuers == 0, "an issuer keeps its stages");
+  static_assert(STAGES * STAGE_BYTES >= BM * BN * 4, "a partial tile fits the ring");
 };
 
 struct Params {
@@ -137,12 +143,12 @@ __device__ __forceinline__ void store16(const Params& p, int64_t row, int n, con
   }
 }
 
-template <int BN, bool PAIR, bool BROW>
+template <bool PAIR, bool BROW>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA,
                     const __grid_constant__ CUtensorMap tmB, const Params p) {
-  using K_ = Cfg<BN, PAIR>;
-  constexpr int CG = K_::CG, STAGES = K_::STAGES, NBUF = K_::NBUF, COLS = K_::COLS;
+  using K_ = Cfg<PAIR>;
+  constexpr int CG = K_::CG, STAGES = K_::STAGES, NBUF = K_::NBUF;
   constexpr uint32_t SLOTS = K_::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -220,9 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
   bool aborted = false;
 
-  if (warp >= kMath) {
-   if constexpr (PAIR && BN == 256) pipe::regs_dec<kIssueRegs>();
-   if (warp == kMath) {
+  if (warp == kMath) {
     // ---------------- TMA producer ----------------
     uint32_t stage = 0, phase = 0;
     bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (aborted) pipe::spin_ns(50000);  // copies already issued land
     __syncwarp();
-   } else if (warp <= kMath + kIssuers) {
+  } else if (warp > kMath && warp <= kMath + kIssuers) {
     // ---------------- MMA issuers (leader CTA) ----------------
     // The whole warp runs the loop and one elected lane issues: descriptors
     // then live in uniform registers.  With the loop inside one lane's branch
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-   } else {
+  } else if (warp > kMath + kIssuers) {
     // ---------------- scales ----------------
     uint32_t slot = 0, phase = 0;
     const uint32_t ring0 = ptx::smem_u32(ring);
@@ -356,10 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     pipe::copies_wait();
     __syncwarp();
-   }
   } else {
     // ---------------- sums ----------------
-    if constexpr (PAIR && BN == 256) pipe::regs_inc<kMathRegs>();
     const uint32_t q = warp & 3u, part = warp >> 2;  // rows 32 q .., columns COLS part ..
     uint32_t buf = 0, buf_phase = 0, slot = 0, slot_phase = 0;
     const uint32_t tfull0 = tfull_bar(0), sfull0 = sfull_bar(0), sempty0 = sempty_bar(0);
@@ -619,11 +621,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int BN, bool PAIR, bool BROW>
+template <bool PAIR, bool BROW>
 static int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& prm,
                   uint32_t programs, cudaStream_t stream) {
-  using K_ = Cfg<BN, PAIR>;
-  auto kern = gemm_fp8_kernel<BN, PAIR, BROW>;
+  using K_ = Cfg<PAIR>;
+  auto kern = gemm_fp8_kernel<PAIR, BROW>;
   static std::mutex mu;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -747,7 +749,7 @@ int swz::gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int
   if (ch.split > kb) return SWZ_EUNSUPPORTED;  // an empty range of K
   const bool pair = ch.tile == 256;
   const uint64_t sm = ceil_div(uint64_t(M), pair ? 256 : 128);
-  const uint64_t sn = ceil_div(uint64_t(N), 128);
+  const uint64_t sn = ceil_div(uint64_t(N), BN);
   const uint64_t cl = pair ? 2 : ch.split;
   if (sm * sn * cl > uint64_t(INT32_MAX)) return SWZ_EINVAL;
   if ((o.order == SWZ_MORTON || o.order == SWZ_XOR) &&
@@ -792,8 +794,8 @@ int swz::gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int
   }
   const bool brow = B->block == SWZ_BLOCK_ROW;
   if (pair)
-    return brow ? launch<128, true, true>(ta, tb, prm, uint32_t(programs), s)
-                : launch<128, true, false>(ta, tb, prm, uint32_t(programs), s);
-  return brow ? launch<128, false, true>(ta, tb, prm, uint32_t(programs), s)
-              : launch<128, false, false>(ta, tb, prm, uint32_t(programs), s);
+    return brow ? launch<true, true>(ta, tb, prm, uint32_t(programs), s)
+                : launch<true, false>(ta, tb, prm, uint32_t(programs), s);
+  return brow ? launch<false, true>(ta, tb, prm, uint32_t(programs), s)
+              : launch<false, false>(ta, tb, prm, uint32_t(programs), s);
 }

@@ -829,7 +829,7 @@ static int product(const Operand& A, const Operand& B, uint64_t batch, uint64_t 
   for (int i = 0; i < 2; ++i) {
     const Operand& o = *ops[i];
     const int rc = encode_half(&map[i], o.p, batch, o.rows, o.cols, uint64_t(o.ld),
-                               o.rows * uint64_t(o.ld), 64, o.mn ? 64u * ka : 128u, true);
+                               o.rows * uint64_t(o.ld), 64, o.mn ? 64u * ka : 128u);
     if (rc != SWZ_OK) return rc;
   }
   const uint64_t units = tiles(bn);

@@ -71,8 +71,7 @@ int encode_bytes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
 }
 
 int encode_half(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t cols,
-                uint64_t ld, uint64_t batch_stride, uint32_t box_cols, uint32_t box_rows,
-                bool swizzle) {
+                uint64_t ld, uint64_t batch_stride, uint32_t box_cols, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return cuda_fail(cudaErrorNotSupported);
   const cuuint64_t dims[3] = {cols, rows, batch};
@@ -82,7 +81,7 @@ int encode_half(CUtensorMap* map, const void* base, uint64_t batch, uint64_t row
   const CUresult r =
       fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box,
          estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SWZ_OK : cuda_fail(cudaErrorInvalidValue);
 }

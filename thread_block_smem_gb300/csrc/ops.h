@@ -23,11 +23,10 @@ int encode_bytes(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
                  uint32_t box_rows);
 
 // The same for batch matrices of 16-bit elements (ld and batch stride in
-// elements), boxes of box_cols (64 or fewer) x box_rows of one matrix; swizzle
-// of 128 bytes or none.
+// elements), boxes of box_cols (64 or fewer) x box_rows of one matrix, 128-byte
+// swizzle.
 int encode_half(CUtensorMap* map, const void* base, uint64_t batch, uint64_t rows, uint64_t cols,
-                uint64_t ld, uint64_t batch_stride, uint32_t box_cols, uint32_t box_rows,
-                bool swizzle);
+                uint64_t ld, uint64_t batch_stride, uint32_t box_cols, uint32_t box_rows);
 
 // swz_gemm_fp8; `early_b`: the kernel before in the stream is the quantiser of
 // A, launched by the same caller, and B may be read while it runs.

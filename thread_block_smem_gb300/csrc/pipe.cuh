@@ -187,18 +187,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// This warpgroup's registers per thread, out of what the block was launched
-// with (all four warps execute the same one, each in its role's branch: where
-// the branches meet again the compiler keeps to the smaller number).
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Asynchronous copy of one float to shared memory, zero when !in (`any`: a
 // valid address, not read then); copies_arrive arrives on `bar` (one of 32
 // lanes) when this thread's copies so far have landed.
