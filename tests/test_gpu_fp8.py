@@ -362,3 +362,27 @@ def test_refusals(swz):
     y, saved = swz.linear_fp8_forward(x, x)
     with pytest.raises(ValueError):
         swz.linear_fp8_backward(x, saved)
+
+
+def test_second_derivative_is_refused(swz):
+    """The gradient is made of the library's calls, which torch cannot differentiate."""
+    x = torch.randn(40, 64, device="cuda").bfloat16().requires_grad_()
+    w = torch.randn(48, 64, device="cuda").bfloat16().requires_grad_()
+    dx, = torch.autograd.grad(swz.fp8_linear(x, w).float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.float().sum().backward()
+
+
+def test_layer_checks_its_operands(swz):
+    x = torch.randn(40, 64, device="cuda").bfloat16()
+    w = torch.randn(48, 64, device="cuda").bfloat16()
+    with pytest.raises(ValueError):
+        swz.linear_fp8_forward(x, w[:, :48].contiguous())
+    with pytest.raises(TypeError):
+        swz.linear_fp8_forward(x, w, out_dtype=torch.float64)
+    y, saved = swz.linear_fp8_forward(x, w)
+    with pytest.raises(ValueError):
+        swz.linear_fp8_backward(y[:, :40].contiguous(), saved)
+    qxt, sxt, qwt, swt = saved
+    with pytest.raises(ValueError):
+        swz.linear_fp8_backward(y, (qxt, sxt[:, :63], qwt, swt))

@@ -220,27 +220,50 @@ def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
     nearest even."""
     if torch is None:
         _init()
+    q, s, qt, st, M, K = _quantize(x, _block(block), fmt, transposed, stream)
+    q = q if q.shape[1] == K else q.narrow(1, 0, K)
+    if not transposed:
+        return q, s
+    return q, s, (qt if qt.shape[1] == M else qt.narrow(1, 0, M)), st
+
+
+def _quantize(x, b, fmt, transposed, stream):
+    """(q, scales, qt, scales_t, M, K), q and qt with whole rows of a multiple of 16 bytes."""
     M, K, ldx = _rows(x, "x")
-    code, b = _code(x.dtype, "x"), _block(block)
-    f8 = _f8_types.get(fmt)
-    if f8 is None:
+    code, f = _code(x.dtype, "x"), FORMATS.get(fmt)
+    if f is None:
         raise ValueError("fmt must be 'e4m3' or 'e5m2'")
+    f8 = _f8_types[fmt]
     kb, mb = (K + 127) // 128, (M + 127) // 128
     ldq, ldt = (K + 15) // 16 * 16, (M + 15) // 16 * 16
     q = _empty((M, ldq), f8, x, stream)
     s = _empty((mb, kb) if b else (kb, M), torch.float32, x, stream)
-    if not transposed:
-        _swz._check(_L.swz_quantize_fp8(
-            x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), ldq, s.data_ptr(),
-            kb if b else M, None, 0, None, 0, _handle(stream, x)), "swz_quantize_fp8")
-        return (q if ldq == K else q.narrow(1, 0, K)), s
-    qt = _empty((K, ldt), f8, x, stream)
-    st = _empty((kb, mb) if b else (mb, K), torch.float32, x, stream)
-    _swz._check(_L.swz_quantize_fp8(
-        x.data_ptr(), code, ldx, M, K, b, FORMATS[fmt], q.data_ptr(), ldq, s.data_ptr(),
-        kb if b else M, qt.data_ptr(), ldt, st.data_ptr(), mb if b else K, _handle(stream, x)),
-        "swz_quantize_fp8")
-    return (q if ldq == K else q.narrow(1, 0, K)), s, (qt if ldt == M else qt.narrow(1, 0, M)), st
+    qt = st = None
+    to = (None, 0, None, 0)
+    if transposed:
+        qt = _empty((K, ldt), f8, x, stream)
+        st = _empty((kb, mb) if b else (mb, K), torch.float32, x, stream)
+        to = (qt.data_ptr(), ldt, st.data_ptr(), mb if b else K)
+    rc = _L.swz_quantize_fp8(x.data_ptr(), code, ldx, M, K, b, f, q.data_ptr(), ldq, s.data_ptr(),
+                             kb if b else M, *to, _handle(stream, x))
+    if rc:
+        raise _swz.SwzError(rc, "swz_quantize_fp8")
+    return q, s, qt, st, M, K
+
+
+def _own(q, s, fmt, block):
+    """swz_fp8_matrix of what _quantize made: nothing to check."""
+    return swz_fp8_matrix(q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1], fmt, block)
+
+
+def _product(A, B, M, N, K, dtype, x, stream):
+    """C = A B^T (M x N of `dtype`) of checked operands, in the default order."""
+    code = _code(dtype, "out_dtype")
+    C = _empty((M, N), dtype, x, stream)
+    rc = _L.swz_gemm_fp8(A, B, C.data_ptr(), N, code, M, N, K, None, _handle(stream, x))
+    if rc:
+        raise _swz.SwzError(rc, "swz_gemm_fp8")
+    return C
 
 
 def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order="serpentine",
@@ -294,10 +317,16 @@ def linear_fp8_forward(x, w, *, out_dtype=None, stream=None):
     """(y, saved) of a layer in training: y = x W^T with x (M x K) quantised in
     row blocks and w (N x K) in square ones; ``saved`` holds x^T and W^T in 8
     bits for linear_fp8_backward."""
-    qx, sx, qxt, sxt = quantize_fp8(x, "row", transposed=True, stream=stream)
-    qw, sw, qwt, swt = quantize_fp8(w, "square", transposed=True, stream=stream)
-    y = gemm_fp8(qx, sx, qw, sw, out_dtype=out_dtype or x.dtype, stream=stream)
-    return y, (qxt, sxt, qwt, swt)
+    if torch is None:
+        _init()
+    qx, sx, qxt, sxt, M, K = _quantize(x, SWZ_BLOCK_ROW, "e4m3", True, stream)
+    qw, sw, qwt, swt, N, K2 = _quantize(w, SWZ_BLOCK_SQUARE, "e4m3", True, stream)
+    if K != K2:
+        raise ValueError("inner dimensions differ")
+    y = _product(_own(qx, sx, SWZ_E4M3, SWZ_BLOCK_ROW), _own(qw, sw, SWZ_E4M3, SWZ_BLOCK_SQUARE),
+                 M, N, K, out_dtype or x.dtype, x, stream)
+    return y, (qxt if qxt.shape[1] == M else qxt.narrow(1, 0, M), sxt,
+               qwt if qwt.shape[1] == N else qwt.narrow(1, 0, N), swt)
 
 
 def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None, dw_dtype=None,
@@ -313,12 +342,15 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
         raise ValueError("dy does not have the shape of the layer's output")
     dx = dw = None
     if need_dx or need_dw:
-        out = quantize_fp8(dy, "row", transposed=need_dw, stream=stream)
+        q, s, qt, st, _, _ = _quantize(dy, SWZ_BLOCK_ROW, "e4m3", need_dw, stream)
         if need_dx:
-            dx = gemm_fp8(out[0], out[1], qwt, swt, out_dtype=dx_dtype or dy.dtype, stream=stream)
+            W, K, _ = _matrix(qwt, swt, SWZ_BLOCK_SQUARE, "saved")
+            dx = _product(_own(q, s, SWZ_E4M3, SWZ_BLOCK_ROW), W, M, K, N, dx_dtype or dy.dtype,
+                          dy, stream)
         if need_dw:
-            dw = gemm_fp8(out[2], out[3], qxt, sxt, b_block="row",
-                          out_dtype=dw_dtype or torch.float32, stream=stream)
+            X, K, _ = _matrix(qxt, sxt, SWZ_BLOCK_ROW, "saved")
+            dw = _product(_own(qt, st, SWZ_E4M3, SWZ_BLOCK_ROW), X, N, K, M,
+                          dw_dtype or torch.float32, dy, stream)
     return dx, dw
 
 
@@ -328,7 +360,7 @@ _function = None
 def fp8_linear(x, w):
     """y = x W^T with its gradient, for torch.autograd: x (..., K), w (N, K);
     forward and backward as linear_fp8_forward / linear_fp8_backward, the
-    gradient of w in fp32 rounded to w's type."""
+    gradient of w in fp32 rounded to w's type.  A second derivative raises."""
     global _function
     if _function is None:
         if torch is None:
@@ -343,6 +375,7 @@ def fp8_linear(x, w):
                 return y
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
                 dy = dy if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1] else dy.contiguous()
                 return linear_fp8_backward(
