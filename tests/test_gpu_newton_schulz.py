@@ -209,3 +209,13 @@ def test_refusals(swz):
         with pytest.raises(swz.SwzError) as e:
             swz.newton_schulz(G, **kw)
         assert e.value.code == swz.SWZ_EUNSUPPORTED
+
+
+# stacks around what one wave of the one-kernel form holds, and well above it
+@pytest.mark.parametrize("shape", [(14, 128, 1100), (40, 100, 1030), (153, 64, 64), (700, 33, 40),
+                                   (80, 200, 120)])
+def test_stacks_of_small_matrices(swz, shape):
+    G = normal(shape, torch.float32, shape[0])
+    Y = swz.newton_schulz(G.cuda(), out_dtype=torch.float32)
+    swz.check_status()
+    check(Y, G)

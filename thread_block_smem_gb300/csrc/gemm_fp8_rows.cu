@@ -16,6 +16,7 @@
 //     the same call, B's first stages are loaded while it still runs: it lets
 //     this kernel start only after everything before it has completed.
 #include <mutex>
+#include <type_traits>
 
 #include "common.h"
 #include "f8.cuh"
@@ -48,11 +49,21 @@ struct RowsParams {
   const float *sa, *sb;
   int64_t ldsa, ldsb;
   int M, N, c_dtype, b_square, early_b;
+  int c_quads;  // four results of a row are one aligned store
   uint32_t num_kb, idesc, split;
   uint32_t debug_flags;
   unsigned int* status;
   uint64_t timeout_ns;
 };
+
+__device__ __forceinline__ uint32_t pack2_out(float a, float b, int dtype) {
+  if (dtype == SWZ_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 __device__ __forceinline__ void store_out(void* C, int64_t at, float v, int dtype) {
   if (dtype == SWZ_F32) static_cast<float*>(C)[at] = v;
@@ -287,7 +298,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
         // partial tile over the ring (every load has been consumed): row j of
         // C, 128 columns
 #pragma unroll
-        for (int j = 0; j < BN; ++j) reinterpret_cast<float*>(smem)[j * 128 + r] = acc[j];
+        for (int j = 0; j < BN; ++j)
+          if (j < p.M) reinterpret_cast<float*>(smem)[j * 128 + r] = acc[j];
       }
     }
   }
@@ -296,20 +308,53 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     __syncwarp();
     ptx::cluster_sync();
     if (warp < 4 && !aborted) {
-      // rank r of S stores the rows r, r + S, .. of C
-      const uint32_t r = warp * 32 + lane;
-      for (uint32_t j = rank; j < uint32_t(BN) && int(j) < p.M; j += p.split) {
-        float v = 0.f;
-        for (uint32_t i = 0; i < p.split; ++i) {
-          float x;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                       : "=f"(x)
-                       : "r"(ptx::map_to_rank(sB + (j * 128 + r) * 4, i))
-                       : "memory");
-          v += x;
+      // Rank r of S stores the rows r, r + S, .. of C: a warp a row, a lane four
+      // columns, and all of a warp's remote reads (about 1 us each) in flight
+      // at once.
+      auto reduce = [&](auto ranks) {
+        constexpr uint32_t S = decltype(ranks)::value;
+        constexpr uint32_t RW = BN / (4 * S) > 0 ? BN / (4 * S) : 1;  // rows of a warp
+        float f[RW][S][4];
+#pragma unroll
+        for (uint32_t k = 0; k < RW; ++k) {
+          const uint32_t j = (rank + S * (warp + 4 * k)) % BN;  // stored only where below M
+#pragma unroll
+          for (uint32_t i = 0; i < S; ++i)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(f[k][i][0]), "=f"(f[k][i][1]), "=f"(f[k][i][2]), "=f"(f[k][i][3])
+                         : "r"(ptx::map_to_rank(sB + (j * 128 + lane * 4) * 4, i))
+                         : "memory");
         }
-        if (n0 + r < p.N) store_out(p.C, int64_t(j) * p.ldc + n0 + r, v, p.c_dtype);
-      }
+        const int64_t n = n0 + lane * 4;
+#pragma unroll
+        for (uint32_t k = 0; k < RW; ++k) {
+          const uint32_t j = rank + S * (warp + 4 * k);
+          if (int(j) >= p.M) continue;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = f[k][0][e];
+#pragma unroll
+            for (uint32_t i = 1; i < S; ++i) v[e] += f[k][i][e];
+          }
+          const int64_t at = int64_t(j) * p.ldc + n;
+          if (p.c_quads && n + 4 <= p.N) {
+            if (p.c_dtype == SWZ_F32)
+              *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            else
+              *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + at) =
+                  make_uint2(pack2_out(v[0], v[1], p.c_dtype), pack2_out(v[2], v[3], p.c_dtype));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (n + e < p.N) store_out(p.C, at + e, v[e], p.c_dtype);
+          }
+        }
+      };
+      if (p.split == 2) reduce(std::integral_constant<uint32_t, 2>{});
+      else if (p.split == 4) reduce(std::integral_constant<uint32_t, 4>{});
+      else reduce(std::integral_constant<uint32_t, 8>{});
     }
     __syncwarp();
     ptx::cluster_sync();  // no CTA leaves while its partial tile is read
@@ -378,6 +423,8 @@ int gemm_fp8_rows(const swz_fp8_matrix& A, const swz_fp8_matrix& B, void* C, int
   p.M = M;
   p.N = N;
   p.c_dtype = c_dtype;
+  const uintptr_t es = c_dtype == SWZ_F32 ? 4 : 2;
+  p.c_quads = ((reinterpret_cast<uintptr_t>(C) | (M > 1 ? uintptr_t(ldc) * es : 0)) % (4 * es)) == 0;
   p.b_square = B.block == SWZ_BLOCK_SQUARE;
   p.early_b = early_b;
   p.num_kb = uint32_t((int64_t(K) + 127) / 128);

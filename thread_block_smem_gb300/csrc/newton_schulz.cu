@@ -921,7 +921,11 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   const bool wide = m <= n;
   const uint64_t d = uint64_t(wide ? m : n);
 
-  const bool small = o.tile == 0 && d <= kSmallSide && (wide ? n : m) <= kSmallLong;
+  bool small = o.tile == 0 && d <= kSmallSide && (wide ? n : m) <= kSmallLong;
+  if (small) {
+    rc = small_pays(batch, wide ? n : m, &small);
+    if (rc != SWZ_OK) return rc;
+  }
   if (small) {
     SmallParams p{};
     p.g = static_cast<const uint8_t*>(G);

@@ -83,6 +83,7 @@ struct SmallParams {
   float fa[kMaxSteps], ub[kMaxSteps], fb[kMaxSteps], k1[kMaxSteps], sx[kMaxSteps], ad[kMaxSteps];
 };
 
+int small_pays(int batch, int len, bool* pays);
 int launch_small(SmallParams p, int batch, cudaStream_t stream);
 
 }  // namespace ns

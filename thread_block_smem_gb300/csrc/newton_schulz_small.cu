@@ -467,37 +467,66 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
   if (warp == 0) ptx::tmem_dealloc<1>(tmem, kSmallTmem);
 }
 
-int launch_small(SmallParams p, int batch, cudaStream_t stream) {
-  static std::mutex mu;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  SWZ_CUDA_TRY(cudaGetDevice(&dev));
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr_set[dev]) {
-      SWZ_CUDA_TRY(cudaFuncSetAttribute(ns_small_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
-      attr_set[dev] = true;
-    }
-  }
-  // as few ranks as hold the long side, 128 columns a rank while that is
-  // enough: an exchange over more of them costs more than the columns
-  p.ranks = 1;
-  while (p.ranks < 8 && int64_t(p.ranks) * 128 < p.len) p.ranks *= 2;
-  p.cols = uint32_t((((int64_t(p.len) + p.ranks - 1) / p.ranks) + 63) / 64 * 64);
+// As few ranks as hold the long side, 128 columns a rank while that is enough:
+// an exchange over more of them costs more than the columns.
+static uint32_t ranks_of(int len) {
+  uint32_t ranks = 1;
+  while (ranks < 8 && int64_t(ranks) * 128 < len) ranks *= 2;
+  return ranks;
+}
+
+static cudaLaunchConfig_t config(int batch, uint32_t ranks, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(batch) * p.ranks);
+  cfg.gridDim = dim3(unsigned(batch) * ranks);
   cfg.blockDim = dim3(kSmallWarps * 32);
   cfg.dynamicSmemBytes = kSmallSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.ranks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Waves of matrices that run at a time, each 55 us and 4 for a rank more,
+// against the products' launches, whose time grows with the matrices.  Measured
+// (one kernel, launches; us): 128 x 128 44, 67; 1024 of them 404, 349; 128 x 2048
+// 89, 98; 16 of them (two waves) 177, 125; 256 of 64 x 64 64, 98.
+int small_pays(int batch, int len, bool* pays) {
+  static std::mutex mu;
+  static int resident[64][4] = {};  // clusters of 1, 2, 4, 8 at a time
+  int dev = 0;
+  SWZ_CUDA_TRY(cudaGetDevice(&dev));
+  const uint32_t ranks = ranks_of(len);
+  const int at = ranks == 1 ? 0 : ranks == 2 ? 1 : ranks == 4 ? 2 : 3;
+  int fit;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev][at] == 0) {
+      SWZ_CUDA_TRY(cudaFuncSetAttribute(ns_small_kernel,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem));
+      cudaLaunchAttribute attr[2];
+      const cudaLaunchConfig_t cfg = config(1, ranks, attr);
+      SWZ_CUDA_TRY(cudaOccupancyMaxActiveClusters(&resident[dev][at], ns_small_kernel, &cfg));
+      if (resident[dev][at] < 1) resident[dev][at] = 1;
+    }
+    fit = resident[dev][at];
+  }
+  const double waves = double((batch + fit - 1) / fit);
+  *pays = waves * (55.0 + 4.0 * ranks) <= 67.0 + 0.015 * len + batch * (0.12 + 0.00125 * len);
+  return SWZ_OK;
+}
+
+// After small_pays, which prepares the kernel on the device.
+int launch_small(SmallParams p, int batch, cudaStream_t stream) {
+  p.ranks = ranks_of(p.len);
+  p.cols = uint32_t((((int64_t(p.len) + p.ranks - 1) / p.ranks) + 63) / 64 * 64);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = config(batch, p.ranks, attr);
+  cfg.stream = stream;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
   SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, ns_small_kernel, p));
   return SWZ_OK;
