@@ -11,10 +11,16 @@
 //     producer, 5 MMA issue, 6 scales.
 //   * A cluster of 1 to 8 CTAs shares a tile's K; the partial tiles are added
 //     through distributed shared memory in rank order, each rank storing its
-//     share of the rows of C.
+//     share of the rows of C.  With the remote reads of a row after another's
+//     16 rows of 10240 x 4096 took 12.6 us, with all of them in flight 10.9.
 //   * When the kernel before in the stream is the quantiser of A, launched by
 //     the same call, B's first stages are loaded while it still runs: it lets
 //     this kernel start only after everything before it has completed.
+//
+// Measured, in a stream of them, B from memory: one row of 4096 x 4096 6.2 us
+// (2.7 TB/s), 10240 x 4096 10.5 (4.0), 8192 x 8192 13.8 (4.9), 28672 x 4096 22.7
+// (5.2).  About 2.8 us are start, first load and the last block's way out;
+// what follows them runs at the copy bandwidth.
 #include <mutex>
 #include <type_traits>
 
@@ -434,7 +440,8 @@ int gemm_fp8_rows(const swz_fp8_matrix& A, const swz_fp8_matrix& B, void* C, int
   rc = op_status_word(&p.status);
   if (rc != SWZ_OK) return rc;
   // K is shared by as many CTAs as stay resident (two an SM), each with four
-  // blocks or more
+  // blocks or more.  One row of 10240 x 4096, by CTAs of a tile (1, 2, 4, 8):
+  // 12.3, 10.5, 13.7, 15.8 us; of 1024 x 8192: 19.4, 11.4, 7.2, 5.6.
   const uint64_t tiles = (uint64_t(N) + 127) / 128;
   uint32_t s = uint32_t(split);
   if (s == 0)

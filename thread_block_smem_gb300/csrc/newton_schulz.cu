@@ -28,6 +28,12 @@
 // in turn so that an epilogue overlaps the next tile's products.  X as a
 // K x N operand is read N-major from shared memory, X^T X takes both operands
 // so, and nothing is ever transposed in memory.
+//
+// Measured, fp32 G, five steps: 4096 x 4096 970 us (1.42 PFLOP/s of the products
+// computed, 0.75 of the measured bf16 peak), 2048 x 2048 245, 1024 x 1024 131.
+// Below 2048 it is 17 launches of 6 to 10 us that depend on one another: a
+// launch's first load, its last tile's epilogue and the next one's start are not
+// hidden by anything.
 #include <math.h>
 
 #include <mutex>
@@ -817,8 +823,10 @@ static int product(const Operand& A, const Operand& B, uint64_t batch, uint64_t 
     const uint64_t tm = (M + t - 1) / t, tn = (N + t - 1) / t;
     return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
   };
-  // in units of the time of a 128-wide tile on one SM: a pair's tile, four times
-  // the work on two SMs, takes 1.7 times that
+  // In units of the time of a 128-wide tile on one SM: a pair's tile, four times
+  // the work on two SMs, takes 1.7 times that.  Whole calls with 128-wide tiles
+  // and with pairs, fp32: 512 x 512 104 and 165 us, 2048 x 2048 239 and 291,
+  // 4096 x 4096 1260 and 970.
   const uint64_t t128 = (tiles(128) + dev.num_sms - 1) / dev.num_sms;
   const uint64_t t256 = (tiles(256) + dev.num_sms / 2 - 1) / (dev.num_sms / 2) * 2;
   const bool pair = tile ? tile == 256 : t256 * 17 <= t128 * 20;

@@ -1,8 +1,8 @@
 // newton_schulz_small.cu -- swz_newton_schulz for matrices with a short side
 // of up to 128 and a long one of up to 2048: all steps in one kernel.
 //
-// Bound: latency.  Three products a step of a few microseconds each in kernels
-// of their own cost 5 us a launch, 85 us for five steps, whatever the size.
+// Bound: latency.  In kernels of their own three products a step cost 4 to 6 us a
+// launch, 65 to 100 us for five steps, whatever the size.
 // Here a cluster of 1 to 8 CTAs holds a matrix: each CTA has the d short rows
 // of X and up to 256 of its long columns in shared memory and TMEM, and
 //   P = X X^T     is summed over the cluster (each rank adds its share of the
@@ -16,6 +16,11 @@
 // cross product left out; A as one.  The tensor core is idle most of the time
 // here, and matrices this small average over few roundings: one fp16 each was
 // 0.17 % off on 64 x 64, this is 0.06 %.
+//
+// Measured, five steps: 128 x 128 44 us against 67 in kernels of their own, 64 x
+// 512 59 against 67, 128 x 2048 (8 ranks) 89 against 98.  A step takes about
+// 7000 cycles on a cluster, most of them its sum: two barriers and the
+// remote reads between them.
 #include <math.h>
 
 #include <mutex>

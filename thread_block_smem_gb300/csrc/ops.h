@@ -34,7 +34,10 @@ int gemm_fp8(const swz_fp8_matrix* A, const swz_fp8_matrix* B, void* C, int64_t 
              int M, int N, int K, const swz_gemm_fp8_opts* opts, void* stream, bool early_b);
 
 // Its kernel for up to kFewRows rows of A (arguments checked by the caller;
-// split 0: automatic).
+// split 0: automatic).  16 rows, 4096 x 4096: 6.9 us against 9.8 with 128-row
+// tiles, 8192 x 8192 14.5 against 17.0; 32 rows 7.7 against 9.5 and 14.9
+// against 17.1, and of 10240 x 4096 12.3 against 12.4.  The tensor core's N and
+// the accumulators end at 32.
 constexpr int kFewRows = 32;
 int gemm_fp8_rows(const swz_fp8_matrix& A, const swz_fp8_matrix& B, void* C, int64_t ldc,
                   int c_dtype, int M, int N, int K, int split, uint32_t debug_flags,
