@@ -22,21 +22,22 @@
 // only tiles on and above the diagonal are computed, the epilogue writes both
 // halves, which saves a third of the work of a square matrix.
 //
-// Kernel: as the library's GEMM -- one CTA (128 x 128) or a CTA pair (256 x
-// 256) per tile, persistent; warp 8 TMA producer, warp 9 MMA issuer, warps 0-7
+// Kernel: as the library's GEMM -- one CTA (128 x 128 or 128 x 64) or a CTA pair
+// (256 x 256) per tile, persistent; warp 8 TMA producer, warp 9 MMA issuer, warps 0-7
 // epilogue (TMEM lanes 32 (w mod 4) .., columns half w / 4), two tiles of TMEM
 // in turn so that an epilogue overlaps the next tile's products.  X as a
 // K x N operand is read N-major from shared memory, X^T X takes both operands
 // so, and nothing is ever transposed in memory.
 //
-// Measured, fp32 G, five steps: 4096 x 4096 970 us (1.42 PFLOP/s of the products
-// computed, 0.75 of the measured bf16 peak), 2048 x 2048 245, 1024 x 1024 131.
-// Below 2048 it is 17 launches of 6 to 10 us that depend on one another: a
+// Measured, fp32 G, five steps: 4096 x 4096 950-970 us (1.42 PFLOP/s of the products
+// computed, 0.75 of the measured bf16 peak), 2048 x 2048 238, 1024 x 1024 118.
+// Below 2048 it is 17 launches of 5 to 10 us that depend on one another: a
 // launch's first load, its last tile's epilogue and the next one's start are not
 // hidden by anything.
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.h"
 #include "f8.cuh"
@@ -55,10 +56,11 @@ constexpr int kThreads = (kEpiWarps + 2) * 32;
 template <int BN, bool PAIR>
 struct Cfg {
   static constexpr int CG = PAIR ? 2 : 1;
-  static constexpr int KA = BN == 128 ? 2 : 1;         // 64-element atoms of K in a stage
-  static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // = 128 in both shapes
-  static constexpr int OP_BYTES = 128 * 128 * KA;      // an operand's share of a stage
-  static constexpr int STAGE_BYTES = 2 * OP_BYTES;
+  static constexpr int KA = PAIR ? 1 : 2;              // 64-element atoms of K in a stage
+  static constexpr int BN_LOCAL = PAIR ? BN / 2 : BN;  // columns this CTA loads
+  static constexpr int A_BYTES = 128 * 128 * KA, B_BYTES = BN_LOCAL * 128 * KA;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int HALVES = BN == 64 ? 1 : 2;      // columns of a tile, by epilogue warps
   static constexpr int STAGES = 192 * 1024 / STAGE_BYTES;
   static constexpr int BARS = 2 * STAGES + 5;
   static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BARS * 8 + 16;
@@ -112,16 +114,17 @@ __device__ __forceinline__ uint32_t bf2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// tile t of the upper triangle of a T x T grid, rows first
-__device__ __forceinline__ TileCoord upper_tile(uint32_t t, uint32_t T) {
+// tile t of the upper triangle of a grid with T columns, rows first; a row of
+// tiles is as tall as R columns of them
+__device__ __forceinline__ TileCoord upper_tile(uint32_t t, uint32_t T, uint32_t R) {
   uint32_t i = 0, left = t;
-  while (left >= T - i) {
-    left -= T - i;
+  while (left >= T - R * i) {
+    left -= T - R * i;
     ++i;
   }
   TileCoord c;
   c.m = i;
-  c.n = i + left;
+  c.n = R * i + left;
   return c;
 }
 
@@ -130,12 +133,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                    const __grid_constant__ CUtensorMap tmB, const Params p) {
   using K_ = Cfg<BN, PAIR>;
-  constexpr int CG = K_::CG, STAGES = K_::STAGES, KA = K_::KA, COLS = BN / 2;
+  constexpr int CG = K_::CG, STAGES = K_::STAGES, KA = K_::KA, COLS = BN / K_::HALVES;
+  constexpr uint32_t kTall = BN == 64 ? 2 : 1;  // rows of a tile, in its columns
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sA = ptx::smem_u32(smem);
-  const uint32_t sB = sA + STAGES * K_::OP_BYTES;
+  const uint32_t sB = sA + STAGES * K_::A_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * K_::STAGE_BYTES);
   const uint32_t bar0 = ptx::smem_u32(bars);
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (uint32_t a = 0; a < 2; ++a) {
       ptx::mbar_init(tfull_bar(a), 1);
-      ptx::mbar_init(tempty_bar(a), kEpiWarps * CG);
+      ptx::mbar_init(tempty_bar(a), kEpiWarps / 2 * K_::HALVES * CG);
     }
     ptx::mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile_at = [&](uint32_t w, uint32_t& b) -> TileCoord {
     b = w / p.per_matrix;
     const uint32_t t = w - b * p.per_matrix;
-    return sym ? upper_tile(t, p.tiles_m) : tile_of(kSerpentine, t, p.tiles_m, p.tiles_n, 8u);
+    return sym ? upper_tile(t, p.tiles_n, kTall) : tile_of(kSerpentine, t, p.tiles_m, p.tiles_n, 8u);
   };
   // nothing above touches global memory
   ptx::grid_dep_wait();
@@ -200,12 +204,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool skip = (p.debug_flags & SWZ_DEBUG_SKIP_FIRST_LOAD) != 0;
     const uint64_t pol = ptx::l2_policy_evict_last();
     const uint32_t full0 = PAIR ? ptx::map_to_rank(full_bar(0), 0) : full_bar(0);
-    // 128 rows (or columns, MN-major) of an operand from r0, K elements k0 ..
-    auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t r0, int32_t k0,
-                    int32_t b, bool mn) {
+    // R rows (or columns, MN-major) of an operand from r0, K elements k0 ..
+    auto load = [&](auto rows, uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t r0,
+                    int32_t k0, int32_t b, bool mn) {
+      constexpr int R = decltype(rows)::value;
       if (mn) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < R / 64; ++j) {
           if constexpr (PAIR)
             ptx::tma_load_3d_pair(dst + j * (64 * KA * 128), map, bar, r0 + 64 * j, k0, b, pol);
           else
@@ -215,12 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < KA; ++j) {
           if constexpr (PAIR)
-            ptx::tma_load_3d_pair(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
+            ptx::tma_load_3d_pair(dst + j * (R * 128), map, bar, k0 + 64 * j, r0, b, pol);
           else
-            ptx::tma_load_3d(dst + j * (128 * 128), map, bar, k0 + 64 * j, r0, b, pol);
+            ptx::tma_load_3d(dst + j * (R * 128), map, bar, k0 + 64 * j, r0, b, pol);
         }
       }
     };
+    const std::integral_constant<int, BM> a_rows;
+    const std::integral_constant<int, K_::BN_LOCAL> b_rows;
     for (uint32_t w = w0; w < p.units && !aborted; w += P) {
       uint32_t b;
       const TileCoord t = tile_at(w, b);
@@ -233,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (leader) ptx::mbar_arrive_expect_tx(full_bar(stage), CG * K_::STAGE_BYTES);
           if (!skip) {
             const int32_t k0 = int32_t(kb * (64 * KA));
-            load(sA + stage * K_::OP_BYTES, &tmA, full0 + 8u * stage, m0, k0, int32_t(b),
+            load(a_rows, sA + stage * K_::A_BYTES, &tmA, full0 + 8u * stage, m0, k0, int32_t(b),
                  p.a_mn != 0);
-            load(sB + stage * K_::OP_BYTES, &tmB, full0 + 8u * stage, n0, k0, int32_t(b),
+            load(b_rows, sB + stage * K_::B_BYTES, &tmB, full0 + 8u * stage, n0, k0, int32_t(b),
                  p.b_mn != 0);
           }
         }
@@ -271,16 +278,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = pipe::wait(full_bar(stage), phase, ctl);
           if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
           ptx::tc_fence_after();
-          const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
-          const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::OP_BYTES >> 4));
+          const uint64_t a = adesc0 + uint64_t(stage * uint32_t(K_::A_BYTES >> 4));
+          const uint64_t b = bdesc0 + uint64_t(stage * uint32_t(K_::B_BYTES >> 4));
           if (pipe::elect_one()) {
             // slice kk: 16 elements of K; K-major 32 bytes into atom kk / 4,
             // MN-major 16 rows of 128 bytes down
 #pragma unroll
             for (uint32_t kk = 0; kk < uint32_t(4 * KA); ++kk) {
-              const uint32_t km = ((kk / 4) * (128 * 128) + (kk % 4) * 32) >> 4;
+              const uint32_t ka_at = ((kk / 4) * (BM * 128) + (kk % 4) * 32) >> 4;
+              const uint32_t kb_at = ((kk / 4) * (K_::BN_LOCAL * 128) + (kk % 4) * 32) >> 4;
               const uint32_t mn = 128u * kk;
-              ptx::mma<CG, 0>(d, a + (amn ? mn : km), b + (bmn ? mn : km), p.idesc,
+              ptx::mma<CG, 0>(d, a + (amn ? mn : ka_at), b + (bmn ? mn : kb_at), p.idesc,
                               kb != 0 || kk != 0);
             }
             if constexpr (PAIR) ptx::mma_commit_pair(empty_bar(stage), 0x3);
@@ -313,9 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp takes 32 rows and 64 columns at a time.  What the sums are added
     // to is loaded before the tile's products are waited for: a chunk's loads
     // after the wait cost an L2 round trip each, most of a small product's time.
+    // Of 64-wide tiles warps 0-3 take every other one, 4-7 the rest.
     const uint32_t q = warp & 3u, half = warp >> 2;
+    const uint32_t half_col = K_::HALVES == 2 ? half * COLS : 0u;
     uint32_t acc = 0, acc_phase = 0;
     for (uint32_t w = w0; w < p.units && !aborted; w += P) {
+      if (K_::HALVES == 1 && acc != half) {
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+        continue;
+      }
       uint32_t b;
       const TileCoord t = tile_at(w, b);
       const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float u16 = p.mode == kPoly ? p.u : p.a * p.u * fx;
 #pragma unroll 1
       for (int h = 0; h < COLS / 64; ++h) {
-        const int64_t col0 = int64_t(t.n) * BN + half * COLS + h * 64;
+        const int64_t col0 = int64_t(t.n) * BN + half_col + h * 64;
         float v[64];
         if (p.mode == kGram) {
 #pragma unroll
@@ -440,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
         }
         __syncwarp();
-        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc * BN + half * COLS + h * 64;
+        const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc * BN + half_col + h * 64;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t r[32];
@@ -542,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j)
           o[j] = half2_bits(v[2 * j] * out_scale, v[2 * j + 1] * out_scale);
         __half* out = p.out + b * p.batch_out;
-        if (sym && t.m != t.n) {
+        if (sym && t.m != t.n / kTall) {
           // The other half: lanes are neighbours along its rows.  Two lanes
           // swap a value of each column pair, so that each stores two rows'
           // values of one of the columns (one value a store took twice as long)
@@ -814,42 +829,78 @@ struct Operand {
   bool mn;  // given K x rows
 };
 
-// One product: the tile shape by the estimated number of waves, the maps, the launch.
+// tiles of an M x N product in tiles of a rows and b columns (a a multiple of b)
+static uint64_t tiles_of(uint64_t M, uint64_t N, bool sym, uint64_t a, uint64_t b) {
+  const uint64_t tm = (M + a - 1) / a, tn = (N + b - 1) / b;
+  return sym ? tm * tn - a / b * (tm * (tm - 1) / 2) : tm * tn;
+}
+
+// The width of the tiles that all products of a call take: 256 (CTA pairs), 128
+// or 64, by the estimated time of a step in us -- for each product a fixed part,
+// then for each wave of tiles its stages of K, or its epilogue where that is
+// longer.  128-wide tiles read 64 KB for 128 of K, 64-wide ones 48 KB, which is
+// what bounds them.  Whole calls, fp32, five steps, us with 64 / 128 / 256: 512 x
+// 512 90 / 104 / 168, 1024 x 1024 118 / 131 / 202, 600 x 4000 174 / 195 / 255, 2048 x
+// 2048 312 / 238 / 288, 2500 x 2500 559 / 474 / 411, 4096 x 4096 1694 / 1243 / 952.
+// One shape for all three products: a kernel that follows another one in
+// the stream starts about 2.5 us later than one that follows itself, and every
+// mixture measured was slower.
+static int width_for(uint64_t batch, uint64_t d, uint64_t len, uint64_t sms) {
+  struct Shape {
+    int width;
+    uint64_t rows, ctas;
+    double fixed, stage, epilogue;
+  };
+  const Shape shapes[3] = {
+      {64, 128, 1, 4.0, 0.39, 1.1}, {128, 128, 1, 4.0, 0.53, 2.2}, {256, 256, 2, 8.7, 0.64, 4.4}};
+  int best = 0;
+  double least = 0;
+  for (const Shape& s : shapes) {
+    double t = 0;
+    for (int product = 0; product < 3; ++product) {  // A, B, the new X
+      const bool sym = product < 2;
+      const uint64_t K = product == 0 ? len : d, N = sym ? d : len;
+      const uint64_t tiles = batch * tiles_of(d, N, sym, s.rows, uint64_t(s.width));
+      const uint64_t at_once = sms / s.ctas;
+      t += s.fixed + double((tiles + at_once - 1) / at_once) *
+                         fmax(s.stage * double((K + 127) / 128), s.epilogue);
+    }
+    if (best == 0 || t < least) {
+      best = s.width;
+      least = t;
+    }
+  }
+  return best;
+}
+
+// One product: the maps and the launch.
 static int product(const Operand& A, const Operand& B, uint64_t batch, uint64_t K, Params prm,
-                   const DeviceInfo& dev, int tile, cudaStream_t s) {
+                   const DeviceInfo& dev, int width, cudaStream_t s) {
   const uint64_t M = uint64_t(prm.M), N = uint64_t(prm.N);
   const bool sym = prm.mode != kUpdate;
-  auto tiles = [&](uint64_t t) {
-    const uint64_t tm = (M + t - 1) / t, tn = (N + t - 1) / t;
-    return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
-  };
-  // In units of the time of a 128-wide tile on one SM: a pair's tile, four times
-  // the work on two SMs, takes 1.7 times that.  Whole calls with 128-wide tiles
-  // and with pairs, fp32: 512 x 512 104 and 165 us, 2048 x 2048 239 and 291,
-  // 4096 x 4096 1260 and 970.
-  const uint64_t t128 = (tiles(128) + dev.num_sms - 1) / dev.num_sms;
-  const uint64_t t256 = (tiles(256) + dev.num_sms / 2 - 1) / (dev.num_sms / 2) * 2;
-  const bool pair = tile ? tile == 256 : t256 * 17 <= t128 * 20;
-  const uint64_t bn = pair ? 256 : 128;
+  const bool pair = width == 256;
+  const uint64_t bm = pair ? 256 : 128, bn = uint64_t(width);
   const int ka = pair ? 1 : 2;
   CUtensorMap map[2];
   const Operand* ops[2] = {&A, &B};
   for (int i = 0; i < 2; ++i) {
     const Operand& o = *ops[i];
     const int rc = encode_half(&map[i], o.p, batch, o.rows, o.cols, uint64_t(o.ld),
-                               o.rows * uint64_t(o.ld), 64, o.mn ? 64u * ka : 128u);
+                               o.rows * uint64_t(o.ld), 64,
+                               o.mn ? 64u * ka : i == 1 && width == 64 ? 64u : 128u);
     if (rc != SWZ_OK) return rc;
   }
-  const uint64_t units = tiles(bn);
+  const uint64_t units = batch * tiles_of(M, N, sym, bm, bn);
   if (units > uint64_t(INT32_MAX)) return SWZ_EINVAL;
-  prm.tiles_m = uint32_t((M + bn - 1) / bn);
+  prm.tiles_m = uint32_t((M + bm - 1) / bm);
   prm.tiles_n = uint32_t((N + bn - 1) / bn);
   prm.units = uint32_t(units);
   prm.per_matrix = uint32_t(units / batch);
   prm.num_kb = uint32_t((K + 64 * ka - 1) / (64 * ka));
   prm.a_mn = A.mn;
   prm.b_mn = B.mn;
-  prm.idesc = pipe::idesc(0, 0, A.mn, B.mn, int(bn), int(bn));
+  prm.idesc = pipe::idesc(0, 0, A.mn, B.mn, int(bm), int(bn));
+  if (width == 64) return launch<64, false>(map[0], map[1], prm, dev.num_sms, s);
   return pair ? launch<256, true>(map[0], map[1], prm, dev.num_sms, s)
               : launch<128, false>(map[0], map[1], prm, dev.num_sms, s);
 }
@@ -1014,6 +1065,9 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   __half* const Am = reinterpret_cast<__half*>(ws + L.a);
   __half* const Bm = reinterpret_cast<__half*>(ws + L.b);
   float* const master = reinterpret_cast<float*>(ws + L.master);
+  const int width = o.tile ? o.tile
+                           : width_for(uint64_t(batch), d, uint64_t(wide ? n : m),
+                                       uint64_t(dev.num_sms));
   // steps that take the a X term in fp32 (the first takes G itself in any case)
   const int masters = steps - 2;
   for (int i = 0; i < steps; ++i) {
@@ -1029,8 +1083,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     p.batch_out = int64_t(d) * L.ldd;
     p.first = i == 0;
     p.f = float(exp2(double(ea[i] - 2 * ex[i])));
-    rc = wide ? product(xk, xk, uint64_t(batch), uint64_t(n), p, dev, o.tile, s)
-              : product(xm, xm, uint64_t(batch), uint64_t(m), p, dev, o.tile, s);
+    rc = wide ? product(xk, xk, uint64_t(batch), uint64_t(n), p, dev, width, s)
+              : product(xm, xm, uint64_t(batch), uint64_t(m), p, dev, width, s);
     if (rc != SWZ_OK) return rc;
 
     p = base;
@@ -1045,7 +1099,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
     p.batch_out = int64_t(d) * L.ldd;
     p.u = float(b * exp2(double(eb[i] - ea[i])));
     p.f = float(c * exp2(double(eb[i] - 2 * ea[i])));
-    rc = product(ak, ak, uint64_t(batch), d, p, dev, o.tile, s);
+    rc = product(ak, ak, uint64_t(batch), d, p, dev, width, s);
     if (rc != SWZ_OK) return rc;
 
     p = base;
@@ -1078,8 +1132,8 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
       p.out_scale = float(exp2(double(ex[i + 1])));
       p.master_out = i + 1 < masters ? master : nullptr;
     }
-    rc = wide ? product(bk, xm, uint64_t(batch), d, p, dev, o.tile, s)
-              : product(xk, bk, uint64_t(batch), d, p, dev, o.tile, s);
+    rc = wide ? product(bk, xm, uint64_t(batch), d, p, dev, width, s)
+              : product(xk, bk, uint64_t(batch), d, p, dev, width, s);
     if (rc != SWZ_OK) return rc;
   }
   return SWZ_OK;

@@ -2,7 +2,7 @@
 // of up to 128 and a long one of up to 2048: all steps in one kernel.
 //
 // Bound: latency.  In kernels of their own three products a step cost 4 to 6 us a
-// launch, 65 to 100 us for five steps, whatever the size.
+// launch, 55 to 90 us for five steps, whatever the size.
 // Here a cluster of 1 to 8 CTAs holds a matrix: each CTA has the d short rows
 // of X and up to 256 of its long columns in shared memory and TMEM, and
 //   P = X X^T     is summed over the cluster (each rank adds its share of the
@@ -17,10 +17,10 @@
 // here, and matrices this small average over few roundings: one fp16 each was
 // 0.17 % off on 64 x 64, this is 0.06 %.
 //
-// Measured, five steps: 128 x 128 44 us against 67 in kernels of their own, 64 x
-// 512 59 against 67, 128 x 2048 (8 ranks) 89 against 98.  A step takes about
-// 7000 cycles on a cluster, most of them its sum: two barriers and the
-// remote reads between them.
+// Measured, five steps, bf16: 64 x 64 31 us against 55 in kernels of their own, 128 x
+// 128 44 against 58, 128 x 512 60 against 65; at 128 x 1024 and more both take as
+// long.  A step takes about 7000 cycles on a cluster, most of them its sum: two
+// barriers and the remote reads between them.
 #include <math.h>
 
 #include <mutex>
@@ -494,10 +494,11 @@ static cudaLaunchConfig_t config(int batch, uint32_t ranks, cudaLaunchAttribute*
   return cfg;
 }
 
-// Waves of matrices that run at a time, each 55 us and 4 for a rank more,
-// against the products' launches, whose time grows with the matrices.  Measured
-// (one kernel, launches; us): 128 x 128 44, 67; 1024 of them 404, 349; 128 x 2048
-// 89, 98; 16 of them (two waves) 177, 125; 256 of 64 x 64 64, 98.
+// Waves of matrices that run at a time, by the ranks of one, against the
+// products' launches, whose time grows with the matrices.  Measured (one kernel,
+// launches; us): 64 x 64 31, 55; 128 x 128 44, 58; 600 of them 177, 212; 70 of 128 x
+// 256 58, 76; 152 of them (two waves) 116, 106; 128 x 2048 89, 84; 14 of them 94, 111;
+// 64 of them 588, 240.
 int small_pays(int batch, int len, bool* pays) {
   static std::mutex mu;
   static int resident[64][4] = {};  // clusters of 1, 2, 4, 8 at a time
@@ -519,7 +520,8 @@ int small_pays(int batch, int len, bool* pays) {
     fit = resident[dev][at];
   }
   const double waves = double((batch + fit - 1) / fit);
-  *pays = waves * (55.0 + 4.0 * ranks) <= 67.0 + 0.015 * len + batch * (0.12 + 0.00125 * len);
+  const double wave[4] = {44.0, 57.0, 62.0, 60.0 + 0.014 * len};
+  *pays = waves * wave[at] <= 57.0 + 0.0135 * len + batch * (0.12 + 0.0009 * len);
   return SWZ_OK;
 }
 
