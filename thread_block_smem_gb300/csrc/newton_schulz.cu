@@ -30,7 +30,7 @@
 // so, and nothing is ever transposed in memory.
 //
 // Measured, fp32 G, five steps: 4096 x 4096 950-970 us (1.42 PFLOP/s of the products
-// computed, 0.75 of the measured bf16 peak), 2048 x 2048 238, 1024 x 1024 118.
+// computed, 0.75 of the measured bf16 peak), 2048 x 2048 238, 1024 x 1024 112.
 // Below 2048 it is 17 launches of 5 to 10 us that depend on one another: a
 // launch's first load, its last tile's epilogue and the next one's start are not
 // hidden by anything.
@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return sym ? upper_tile(t, p.tiles_n, kTall) : tile_of(kSerpentine, t, p.tiles_m, p.tiles_n, 8u);
   };
   // nothing above touches global memory
-  ptx::grid_dep_wait();
-  if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
+  if (PAIR || warp >= kEpiWarps) ptx::grid_dep_wait();
+  if (threadIdx.x == kEpiWarps * 32) ptx::grid_dep_launch_dependents();
   bool aborted = false;
 
   if (warp == kEpiWarps) {
@@ -325,20 +325,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q = warp & 3u, half = warp >> 2;
     const uint32_t half_col = K_::HALVES == 2 ? half * COLS : 0u;
     uint32_t acc = 0, acc_phase = 0;
-    for (uint32_t w = w0; w < p.units && !aborted; w += P) {
-      if (K_::HALVES == 1 && acc != half) {
+    // A single CTA's warps run their code once before they wait for the kernel
+    // before, with rows past the end, so that nothing is loaded or stored: its
+    // instructions then need not be fetched at the first tile's end (512 x 512
+    // 83 us, 91 without; 1024 x 1024 112 and 119; pairs are 1 % slower with it).
+    bool warm = !PAIR;
+    for (uint32_t w = w0; warm || (w < p.units && !aborted);) {
+      if (K_::HALVES == 1 && !warm && acc != half) {
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
+        w += P;
         continue;
       }
       uint32_t b;
       const TileCoord t = tile_at(w, b);
-      const int64_t row = int64_t(t.m * CG + rank) * BM + q * 32 + lane;
+      const int64_t row = (warm ? int64_t(p.tiles_m) : int64_t(t.m)) * (CG * BM) + rank * BM +
+                          q * 32 + lane;
       const bool row_in = row < p.M;
       // rows of 128 bytes as a warp loads and stores them (quad_transpose)
       const int64_t line0 = row - lane + (lane / 4) * 4;
       const uint32_t piece = lane % 4;
-      const Scale sc = p.scale[b];
+      Scale sc = {};
+      if (!warm) sc = p.scale[b];
       const float fx = p.first ? sc.f : sc.down;  // X over the fp16 X's power of two
       const float f = p.mode == kPoly ? p.f : p.mode == kGram ? p.f * fx * fx : p.f * fx;
       const float out_scale = p.mode == kUpdate ? p.out_scale * sc.up : 1.f;
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j) v[j] = v[j] * g1 * g2;
         }
-        if (h == 0) {
+        if (h == 0 && !warm) {
           const bool ok = pipe::wait(tfull_bar(acc), acc_phase, ctl);
           if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
           ptx::tc_fence_after();
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (h + 1 == COLS / 64) {  // the tile is in registers
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0 && !warm) {
             if constexpr (PAIR) pipe::arrive_at(ptx::map_to_rank(tempty_bar(acc), 0));
             else ptx::mbar_arrive(tempty_bar(acc));
           }
@@ -580,8 +588,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (line0 + j < p.M && col0 + piece * 16 < p.N)
             pipe::st_global_32b(out + (line0 + j) * p.ld_out + col0 + piece * 16, o + 8 * j);
       }
+      if (warm) {
+        warm = false;
+        ptx::grid_dep_wait();
+        continue;
+      }
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
+      w += P;
     }
   }
 
