@@ -386,3 +386,37 @@ def test_layer_checks_its_operands(swz):
     qxt, sxt, qwt, swt = saved
     with pytest.raises(ValueError):
         swz.linear_fp8_backward(y, (qxt, sxt[:, :63], qwt, swt))
+
+
+def far(rows, cols, dtype, elements):
+    """Uninitialised (rows, cols) view whose last row starts `elements` into its buffer."""
+    stride = -(-elements // ((rows - 1) * 64)) * 64
+    flat = torch.empty((rows - 1) * stride + cols, dtype=dtype, device="cuda")
+    return flat.as_strided((rows, cols), (stride, 1))
+
+
+@pytest.mark.parametrize("block", ["row", "square"])
+def test_quantize_far_rows(swz, block):
+    """Rows further apart than 32 bits reach, in elements as in bytes."""
+    x = torch.randn(150, 300, device="cuda").bfloat16()
+    v = far(150, 300, x.dtype, 2 ** 32 + 1000)
+    v.copy_(x)
+    for got, want in zip(swz.quantize_fp8(v, block, transposed=True),
+                         swz.quantize_fp8(x, block, transposed=True)):
+        assert torch.equal(got.view(torch.uint8) if got.element_size() == 1 else got,
+                           want.view(torch.uint8) if want.element_size() == 1 else want)
+
+
+@pytest.mark.parametrize("M,cfg", [(300, dict(tile=256)), (300, dict(tile=128)),
+                                   (300, dict(tile=128, split_k=2)), (17, dict()),
+                                   (17, dict(split_k=2))])
+def test_gemm_fp8_far_rows(swz, M, cfg):
+    qa, sa = swz.quantize_fp8(torch.randn(M, 500, device="cuda"))
+    qb, sb = swz.quantize_fp8(torch.randn(260, 500, device="cuda"), "square")
+    want = swz.gemm_fp8(qa, sa, qb, sb, **cfg)
+    a = far(M, 500, torch.uint8, 2 ** 32 + 1000).view(qa.dtype)
+    a.view(torch.uint8).copy_(qa.view(torch.uint8))
+    out = far(M, 260, torch.bfloat16, 2 ** 31 + 1000)
+    swz.gemm_fp8(a, sa, qb, sb, out=out, **cfg)
+    swz.check_status()
+    assert torch.equal(out, want)

@@ -219,3 +219,35 @@ def test_stacks_of_small_matrices(swz, shape):
     Y = swz.newton_schulz(G.cuda(), out_dtype=torch.float32)
     swz.check_status()
     check(Y, G)
+
+
+@pytest.mark.parametrize("shape", [(100, 60), (300, 200), (200, 520), (600, 520)])
+def test_far_rows(swz, shape):
+    """Rows of G and of the result further apart than 32 bits reach."""
+    G = normal(shape, torch.bfloat16, 1).cuda()
+    want = swz.newton_schulz(G)
+    m, n = shape
+    stride = -(-(2 ** 31 + 1000) // ((m - 1) * 64)) * 64
+    views = []
+    for _ in range(2):
+        flat = torch.empty((m - 1) * stride + n, dtype=torch.bfloat16, device="cuda")
+        views.append(flat.as_strided((m, n), (stride, 1)))
+    views[0].copy_(G)
+    swz.newton_schulz(views[0], out=views[1])
+    swz.check_status()
+    assert torch.equal(views[1], want)
+
+
+@pytest.mark.parametrize("tile", [0, 128, 256])
+@pytest.mark.parametrize("shape", [(33, 2000), (64, 2048), (77, 2246), (2246, 77), (5, 64, 2050),
+                                   (150, 150), (256, 300)])
+def test_short_sides_in_bf16(swz, shape, tile):
+    """A bf16 result is no more than 1.5 times as far off as the exact one
+    rounded once: what comes before the rounding stays below it."""
+    G = normal(shape, torch.bfloat16, 3)
+    Y = swz.newton_schulz(G.cuda(), tile=tile)
+    swz.check_status()
+    want = reference(G)
+    got = Y.cpu().double()
+    for y, w in zip(got.reshape(-1, *got.shape[-2:]), want.reshape(-1, *want.shape[-2:])):
+        assert (y - w).norm() <= 1.5 * (w.bfloat16().double() - w).norm()

@@ -521,7 +521,8 @@ int small_pays(int batch, int len, bool* pays) {
   }
   const double waves = double((batch + fit - 1) / fit);
   const double wave[4] = {44.0, 57.0, 62.0, 60.0 + 0.014 * len};
-  *pays = waves * wave[at] <= 57.0 + 0.0135 * len + batch * (0.12 + 0.0009 * len);
+  // 17 launches take the host 90 us; replayed from a graph they do not wait for it
+  *pays = waves * wave[at] <= fmax(90.0, 57.0 + 0.0135 * len + batch * (0.12 + 0.0009 * len));
   return SWZ_OK;
 }
 
