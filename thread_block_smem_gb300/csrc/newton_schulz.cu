@@ -903,7 +903,7 @@ static uint64_t tiles_of(uint64_t M, uint64_t N, bool sym, uint64_t a, uint64_t 
 // One shape for all three products: a kernel that follows another one in
 // the stream starts about 2.5 us later than one that follows itself, and every
 // mixture measured was slower.
-static int width_for(uint64_t batch, uint64_t d, uint64_t len, uint64_t sms) {
+static int width_for(uint64_t batch, uint64_t d, uint64_t len, bool wide, uint64_t sms) {
   struct Shape {
     int width;
     uint64_t rows, ctas;
@@ -917,8 +917,9 @@ static int width_for(uint64_t batch, uint64_t d, uint64_t len, uint64_t sms) {
     double t = 0;
     for (int product = 0; product < 3; ++product) {  // A, B, the new X
       const bool sym = product < 2;
-      const uint64_t K = product == 0 ? len : d, N = sym ? d : len;
-      const uint64_t tiles = batch * tiles_of(d, N, sym, s.rows, uint64_t(s.width));
+      const uint64_t K = product == 0 ? len : d;
+      const uint64_t M = sym || wide ? d : len, N = sym || !wide ? d : len;
+      const uint64_t tiles = batch * tiles_of(M, N, sym, s.rows, uint64_t(s.width));
       const uint64_t at_once = sms / s.ctas;
       t += s.fixed + double((tiles + at_once - 1) / at_once) *
                          fmax(s.stage * double((K + 127) / 128), s.epilogue);
@@ -1127,7 +1128,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   __half* const Bm = reinterpret_cast<__half*>(ws + L.b);
   float* const master = reinterpret_cast<float*>(ws + L.master);
   const int width = o.tile ? o.tile
-                           : width_for(uint64_t(batch), d, uint64_t(wide ? n : m),
+                           : width_for(uint64_t(batch), d, uint64_t(wide ? n : m), wide,
                                        uint64_t(dev.num_sms));
   // steps that take the a X term in fp32 (the first takes G itself in any case)
   const int masters = steps - 2;
