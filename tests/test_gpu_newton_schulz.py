@@ -251,3 +251,15 @@ def test_short_sides_in_bf16(swz, shape, tile):
     got = Y.cpu().double()
     for y, w in zip(got.reshape(-1, *got.shape[-2:]), want.reshape(-1, *want.shape[-2:])):
         assert (y - w).norm() <= 1.5 * (w.bfloat16().double() - w).norm()
+
+
+# few tiles and a long K, also where it does not divide evenly
+@pytest.mark.parametrize("tile", [0, 128])
+@pytest.mark.parametrize("shape", [(130, 1024), (130, 1153), (200, 3000), (3000, 200), (150, 2049),
+                                   (3, 140, 2200), (600, 4000)])
+def test_long_k(swz, shape, tile):
+    G = normal(shape, torch.float32, 5)
+    Y = swz.newton_schulz(G.cuda(), out_dtype=torch.float32, tile=tile)
+    swz.check_status()
+    check(Y, G)
+    assert torch.equal(Y, swz.newton_schulz(G.cuda(), out_dtype=torch.float32, tile=tile))
