@@ -111,7 +111,7 @@ struct Params {
   int64_t ld_master, batch_master;
   const uint8_t* g;             // the caller's G
   int64_t ld_g, batch_g;
-  int g_dtype, g_wide;          // g_wide: rows start on 16 bytes
+  int g_dtype;
   uint8_t* y;                   // the caller's result in the last step, else NULL
   int64_t ld_y, batch_y;
   int y_dtype, y_wide, y_lines; // rows start on 16 bytes, on 32
@@ -413,66 +413,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) v[c * 32 + j] = a * __uint_as_float(x[j]);
           }
         } else {
-          // G: rows that start on 16 bytes eight values at a time, others with
-          // a lane a column
+          // G, or its fp32 copy: whole lines, one of 16-bit values, two of fp32
           const float g1 = a * sc.p1, g2 = sc.p2 * sc.f;
           const int es = p.g_dtype == SWZ_F32 ? 4 : 2;
-          const uint8_t* g = p.g + (b * p.batch_g) * es;
-          if (p.g_wide && col0 + 64 <= p.N) {
-            // whole lines: one of 16-bit values, two of fp32
-            const uint8_t* src = g + (line0 * p.ld_g + col0) * es + piece * 32;
+          const uint8_t* src =
+              p.g + (b * p.batch_g + line0 * p.ld_g + col0) * es + piece * 32;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (c == 1 && es == 2) break;
-              uint32_t x[32];
+          for (int c = 0; c < 2; ++c) {
+            if (c == 1 && es == 2) break;
+            const int64_t col = col0 + (es == 4 ? c * 32 + piece * 8 : piece * 16);
+            uint32_t x[32];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[8 * j + k] = 0u;
-                if (line0 + j < p.M) pipe::ld_global_8(src + j * p.ld_g * es + c * 128, x + 8 * j);
-              }
-              pipe::quad_transpose(x, lane);
-              if (es == 4) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[c * 32 + j] = __uint_as_float(x[j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                  v[j] = p.g_dtype == SWZ_BF16 ? f8::Bf16::value(x, j) : f8::F16::value(x, j);
-              }
+              for (int k = 0; k < 8; ++k) x[8 * j + k] = 0u;
+              if (line0 + j < p.M && col < p.N)
+                pipe::ld_global_8(src + j * p.ld_g * es + c * 128, x + 8 * j);
             }
-          } else if (p.g_wide) {
+            pipe::quad_transpose(x, lane);
+            if (es == 4) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int64_t col = col0 + c * 8;
-              const int left = row_in && col < p.N ? int(min(p.N - col, int64_t(8))) : 0;
-              const uint8_t* src = g + (row * p.ld_g + col) * es;
-              float* to = v + c * 8;
-              uint32_t x[8];
-              if (p.g_dtype == SWZ_F32) {
-                f8::load8<f8::F32>(src, left, true, x);
+              for (int j = 0; j < 32; ++j) v[c * 32 + j] = __uint_as_float(x[j]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) to[j] = f8::F32::value(x, j);
-              } else {
-                f8::load8<f8::Bf16>(src, left, true, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  to[j] = p.g_dtype == SWZ_BF16 ? f8::Bf16::value(x, j) : f8::F16::value(x, j);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x[32];
-              const int64_t col = col0 + c * 32 + lane, r0 = row - lane;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[i] = col < p.N && r0 + i < p.M
-                           ? load_any(g, (r0 + i) * p.ld_g + col, p.g_dtype)
-                           : 0.f;
-              pipe::transpose32(x, lane);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[c * 32 + i] = x[i];
+              for (int j = 0; j < 64; ++j)
+                v[j] = p.g_dtype == SWZ_BF16 ? f8::Bf16::value(x, j) : f8::F16::value(x, j);
             }
           }
 #pragma unroll
@@ -667,6 +632,7 @@ struct NormArgs {
   double headroom;       // see make_scale
   Scale* scale;
   __half* x;             // first fp16 X
+  float* g32;            // a copy of G, or NULL; both rows as X's
   int64_t ld_x, batch_x;
 };
 
@@ -763,6 +729,13 @@ __global__ void __launch_bounds__(kNormThreads) ns_start_kernel(const NormArgs p
         o[j] = half2_bits(T::value(w[k], 2 * j) * p1 * p2, T::value(w[k], 2 * j + 1) * p1 * p2);
       *reinterpret_cast<uint4*>(x + int64_t(r) * p.ld_x + c * 8) =
           make_uint4(o[0], o[1], o[2], o[3]);
+      if (p.g32) {
+        float4* to = reinterpret_cast<float4*>(p.g32 + b * p.batch_x + int64_t(r) * p.ld_x + c * 8);
+        to[0] = make_float4(T::value(w[k], 0), T::value(w[k], 1), T::value(w[k], 2),
+                            T::value(w[k], 3));
+        to[1] = make_float4(T::value(w[k], 4), T::value(w[k], 5), T::value(w[k], 6),
+                            T::value(w[k], 7));
+      }
     }
   }
 }
@@ -1096,6 +1069,12 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   na.headroom = headroom;
   na.scale = reinterpret_cast<Scale*>(ws + L.scale);
   na.x = reinterpret_cast<__half*>(ws + L.x0);
+  // The first update reads G by whole lines of 64 values.  Rows that do not start
+  // on 16 bytes or are no multiple of a line it reads from an fp32 copy, which is
+  // left where the fp32 X will be.  Element by element in its epilogue it took 49
+  // us instead of 15 at 1001 x 1001, 129 instead of 28 for 14 of 2533 x 199.
+  const bool lines = na.wide && n % 64 == 0;
+  na.g32 = lines ? nullptr : reinterpret_cast<float*>(ws + L.master);
   na.ld_x = L.ldx;
   na.batch_x = int64_t(m) * L.ldx;
   const uint32_t grid = uint32_t(parts) * uint32_t(batch);
@@ -1107,11 +1086,10 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   }
 
   Params base{};
-  base.g = na.g;
-  base.ld_g = na.ld_g;
-  base.batch_g = na.batch_g;
-  base.g_dtype = dtype;
-  base.g_wide = na.wide;
+  base.g = lines ? na.g : reinterpret_cast<const uint8_t*>(na.g32);
+  base.ld_g = lines ? na.ld_g : L.ldx;
+  base.batch_g = lines ? na.batch_g : int64_t(m) * L.ldx;
+  base.g_dtype = lines ? dtype : int(SWZ_F32);
   base.ld_master = L.ldx;
   base.batch_master = int64_t(m) * L.ldx;
   base.timeout_ns = timeout_ns;
