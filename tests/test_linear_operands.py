@@ -1,0 +1,111 @@
+"""What the linear-layer operators refuse or do with their operands before any
+CUDA call (CPU only: tensors are stand-ins, the library's launches are not
+reached)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def swz():
+    from thread_block_smem_gb300 import build
+    build.build()
+    import thread_block_smem_gb300 as m
+    m.lib()
+    return m
+
+
+class Operand:
+    """A row-major CUDA tensor as the entry points see one, without memory."""
+
+    def __init__(self, shape, dtype=torch.bfloat16, device=0, stride=None):
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.device = torch.device("cuda", device)
+        self.is_cuda, self.requires_grad = True, False
+        self._stride = stride or tuple(
+            int(torch.Size(shape[i + 1:]).numel()) for i in range(len(shape)))
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+    def get_device(self):
+        return self.device.index
+
+    def data_ptr(self):
+        return 4096
+
+
+BIG = 2 ** 32 + 8  # an int would hold 8
+
+
+def test_sizes_past_an_int_are_refused_by_the_mirrors(swz):
+    E = swz.SWZ_EINVAL
+    for at in range(3):
+        sizes = [8, 5, 200]
+        sizes[at] = BIG
+        assert swz.swz_linear_fp8_workspace_size(*sizes)[0] == E
+        sizes = [2, 5, 200]
+        sizes[at] = BIG
+        assert swz.swz_newton_schulz_workspace_size(*sizes)[0] == E
+    # the calls below are no-ops (a size of zero) unless a size is refused
+    quantize = [256, 1, 64, 0, 64, 0, 0, 4096, 64, 8192, 8, 0, 0, 0, 0]
+    assert swz.swz_quantize_fp8(*quantize) == swz.SWZ_OK
+    for at in (1, 3, 4, 5, 6):  # dtype, M, K, block, fmt
+        a = list(quantize)
+        a[at] += 2 ** 32
+        assert swz.swz_quantize_fp8(*a) == E, at
+    mat = swz.swz_fp8_matrix(4096, 64, 256, 8, 0, 0)
+    gemm = [mat, mat, 4096, 8, 3, 0, 8, 64]
+    assert swz.swz_gemm_fp8(*gemm) == swz.SWZ_OK
+    for at in (4, 5, 6, 7):
+        a = list(gemm)
+        a[at] += 2 ** 32
+        assert swz.swz_gemm_fp8(*a) == E, at
+    linear = [256, 1, 64, mat, 4096, 8, 1, 0, 8, 64, 65536, 1 << 20]
+    assert swz.swz_linear_fp8(*linear) == swz.SWZ_OK
+    for at in (1, 6, 7, 8, 9):
+        a = list(linear)
+        a[at] += 2 ** 32
+        assert swz.swz_linear_fp8(*a) == E, at
+    update = [256, 3, 64, 0, 4096, 1, 64, 0, 0, 8, 64, 5, 3.4, -4.8, 2.0, 1e-7, None, 65536, 1 << 30]
+    assert swz.swz_newton_schulz(*update) == swz.SWZ_OK
+    for at in (1, 5, 8, 9, 10, 11):
+        a = list(update)
+        a[at] += 2 ** 32
+        assert swz.swz_newton_schulz(*a) == E, at
+
+
+@pytest.mark.parametrize("shape", [(1, BIG), (BIG, 1), (3, 2 ** 31)])
+def test_sizes_past_an_int_are_refused(swz, shape):
+    x = Operand(shape)
+    f8 = Operand(shape, torch.float8_e4m3fn)
+    s = Operand((1, 1), torch.float32)
+    other = Operand((4, 128), torch.float8_e4m3fn)
+    other_s = Operand((1, 1), torch.float32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.quantize_fp8(x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.gemm_fp8(f8, s, other, other_s)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.linear_fp8(x, other, other_s)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.linear_fp8_forward(x, x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.newton_schulz(x, out=x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        swz.newton_schulz(Operand((BIG, 2, 2)), out=Operand((BIG, 2, 2)))
+
+
+def test_options_past_their_type_are_refused(swz):
+    q, s = Operand((4, 128), torch.float8_e4m3fn), Operand((1, 4), torch.float32)
+    qb, sb = q, Operand((1, 1), torch.float32)
+    out = Operand((4, 4))
+    for kw in (dict(order=2 ** 32 + 5), dict(group=BIG), dict(tile=2 ** 32 + 128), dict(split_k=2 ** 32),
+               dict(num_programs=-2 ** 32), dict(timeout_ms=2 ** 32), dict(debug_flags=2 ** 32)):
+        with pytest.raises(ValueError, match="range"):
+            swz.gemm_fp8(q, s, qb, sb, out=out, **kw)
+    for kw in (dict(steps=2 ** 32 + 5), dict(tile=2 ** 32), dict(timeout_ms=2 ** 32)):
+        with pytest.raises(ValueError, match="range"):
+            swz.newton_schulz(Operand((8, 8)), out=Operand((8, 8)), **kw)

@@ -55,24 +55,42 @@ def declare(L):
 
 
 # ---- raw mirrors ----------------------------------------------------------------
+# ctypes hands a C int the low 32 bits of a larger number without a word, so the
+# mirrors refuse what does not fit as the entry points refuse other sizes.
+INT_MAX = 2 ** 31 - 1
+
+
+def _ints(*values):
+    """True when every value fits a C int."""
+    return all(-INT_MAX <= v <= INT_MAX for v in values)
+
+
 def swz_quantize_fp8(x, dtype, ldx, M, K, block, fmt, q, ldq, scales, ld_scales, qt, ldqt,
                      scales_t, ld_scales_t, stream=0):
+    if not _ints(dtype, M, K, block, fmt):
+        return _swz.SWZ_EINVAL
     return _swz.lib().swz_quantize_fp8(x, dtype, ldx, M, K, block, fmt, q, ldq, scales, ld_scales,
                                        qt, ldqt, scales_t, ld_scales_t, stream)
 
 
 def swz_gemm_fp8(A, B, C, ldc, c_dtype, M, N, K, opts=None, stream=0):
+    if not _ints(c_dtype, M, N, K):
+        return _swz.SWZ_EINVAL
     return _swz.lib().swz_gemm_fp8(ctypes.byref(A), ctypes.byref(B), C, ldc, c_dtype, M, N, K,
                                    ctypes.byref(opts) if opts is not None else None, stream)
 
 
 def swz_linear_fp8(x, dtype, ldx, W, y, ldy, y_dtype, M, N, K, workspace, workspace_bytes,
                    stream=0):
+    if not _ints(dtype, y_dtype, M, N, K):
+        return _swz.SWZ_EINVAL
     return _swz.lib().swz_linear_fp8(x, dtype, ldx, ctypes.byref(W), y, ldy, y_dtype, M, N, K,
                                      workspace, workspace_bytes, stream)
 
 
 def swz_linear_fp8_workspace_size(M, N, K):
+    if not _ints(M, N, K):
+        return _swz.SWZ_EINVAL, 0
     b = ctypes.c_uint64(0)
     rc = _swz.lib().swz_linear_fp8_workspace_size(M, N, K, ctypes.byref(b))
     return rc, b.value
@@ -80,6 +98,8 @@ def swz_linear_fp8_workspace_size(M, N, K):
 
 def swz_newton_schulz(G, dtype, ldg, batch_stride_g, Y, y_dtype, ldy, batch_stride_y, batch, m, n,
                       steps, a, b, c, eps, opts, workspace, workspace_bytes, stream=0):
+    if not _ints(dtype, y_dtype, batch, m, n, steps):
+        return _swz.SWZ_EINVAL
     return _swz.lib().swz_newton_schulz(
         G, dtype, ldg, batch_stride_g, Y, y_dtype, ldy, batch_stride_y, batch, m, n, steps, a, b,
         c, eps, ctypes.byref(opts) if opts is not None else None, workspace, workspace_bytes,
@@ -87,6 +107,8 @@ def swz_newton_schulz(G, dtype, ldg, batch_stride_g, Y, y_dtype, ldy, batch_stri
 
 
 def swz_newton_schulz_workspace_size(batch, m, n):
+    if not _ints(batch, m, n):
+        return _swz.SWZ_EINVAL, 0
     b = ctypes.c_uint64(0)
     rc = _swz.lib().swz_newton_schulz_workspace_size(batch, m, n, ctypes.byref(b))
     return rc, b.value
@@ -124,6 +146,8 @@ def _rows(x, what):
     if not x.is_cuda:
         raise ValueError(f"{what}: CUDA tensor expected")
     m, k = x.shape
+    if (m | k) > INT_MAX:
+        raise ValueError(f"{what}: more than 2^31 - 1 rows or columns")
     ld, one = x.stride()
     if one != 1 and k > 1:
         raise ValueError(f"{what}: contiguous rows expected")
@@ -132,6 +156,12 @@ def _rows(x, what):
     if ld < k:
         raise ValueError(f"{what}: rows must not overlap")
     return m, k, ld
+
+
+def _in_range(debug_flags, timeout_ms, *ints):
+    """Refuses options that their C types would cut."""
+    if not (_ints(*ints) and 0 <= debug_flags < 2 ** 32 and 0 <= timeout_ms < 2 ** 32):
+        raise ValueError("option out of range")
 
 
 def _on(stream):
@@ -281,8 +311,10 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
     B, N, K2 = _matrix(b, sb, _block(b_block), "b")
     if K != K2:
         raise ValueError("inner dimensions differ")
+    order = _swz._order(order)
+    _in_range(debug_flags, timeout_ms, order, group, tile, split_k, num_programs)
     C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a, stream)
-    opts = swz_gemm_fp8_opts(_swz._order(order), group, tile, split_k, num_programs, debug_flags,
+    opts = swz_gemm_fp8_opts(order, group, tile, split_k, num_programs, debug_flags,
                              timeout_ms)
     _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
                 "swz_gemm_fp8")
@@ -400,6 +432,9 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
         raise ValueError("G: 2-D or 3-D tensor expected")
     if not G.is_cuda:
         raise ValueError("G: CUDA tensor expected")
+    if max(G.shape) > INT_MAX:
+        raise ValueError("G: more than 2^31 - 1 matrices, rows or columns")
+    _in_range(debug_flags, timeout_ms, steps, tile)
     code = _code(G.dtype, "G")
     if out is None:
         ycode = _code(out_dtype or torch.bfloat16, "out_dtype")
