@@ -14,6 +14,11 @@ def swz():
     return m
 
 
+@pytest.fixture(autouse=True)
+def current_device(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+
+
 class Operand:
     """A row-major CUDA tensor as the entry points see one, without memory."""
 
@@ -109,3 +114,44 @@ def test_options_past_their_type_are_refused(swz):
     for kw in (dict(steps=2 ** 32 + 5), dict(tile=2 ** 32), dict(timeout_ms=2 ** 32)):
         with pytest.raises(ValueError, match="range"):
             swz.newton_schulz(Operand((8, 8)), out=Operand((8, 8)), **kw)
+
+
+def calls(swz, at):
+    """Each operator on operands of which the one named by the key is on device `at[key]`, else 0."""
+    d = lambda name: at.get(name, 0)  # noqa: E731
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    x = Operand((4, 128), device=d("x"))
+    q, s = Operand((4, 128), f8, d("q")), Operand((1, 4), f32, d("s"))
+    w, sw = Operand((4, 128), f8, d("w")), Operand((1, 1), f32, d("sw"))
+    out = Operand((4, 4), device=d("out"))
+    dy = Operand((4, 4), device=d("dy"))
+    saved = (Operand((128, 4), f8, d("qxt"), (16, 1)), Operand((1, 128), f32, d("sxt")),
+             Operand((128, 4), f8, d("qwt"), (16, 1)), Operand((1, 1), f32, d("swt")))
+    return {
+        "quantize_fp8": (("x",), lambda: swz.quantize_fp8(x)),
+        "gemm_fp8": (("q", "s", "w", "sw", "out"), lambda: swz.gemm_fp8(q, s, w, sw, out=out)),
+        "linear_fp8": (("x", "w", "sw", "out"), lambda: swz.linear_fp8(x, w, sw, out=out)),
+        "forward": (("x", "x2"), lambda: swz.linear_fp8_forward(
+            x, Operand((4, 128), device=d("x2")))),
+        "backward": (("dy", "qxt", "sxt", "qwt", "swt"),
+                     lambda: swz.linear_fp8_backward(dy, saved)),
+        "newton_schulz": (("x", "g"), lambda: swz.newton_schulz(
+            x, out=Operand((4, 128), device=d("g")))),
+    }
+
+
+OPERATORS = ["quantize_fp8", "gemm_fp8", "linear_fp8", "forward", "backward", "newton_schulz"]
+
+
+@pytest.mark.parametrize("operator", OPERATORS)
+def test_operands_on_different_devices_are_refused(swz, operator):
+    names = calls(swz, {})[operator][0]
+    for name in names[1:]:
+        with pytest.raises(ValueError, match="device"):
+            calls(swz, {name: 1})[operator][1]()
+
+
+@pytest.mark.parametrize("operator", OPERATORS)
+def test_a_device_that_is_not_current_is_refused(swz, operator):
+    with pytest.raises(ValueError, match="current device"):
+        calls(swz, {name: 1 for name in calls(swz, {})[operator][0]})[operator][1]()

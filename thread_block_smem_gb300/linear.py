@@ -7,7 +7,8 @@ library's kernels).
 shape (rows, K) whose rows start on multiples of 16 bytes (``quantize_fp8``
 makes them so; ``fp8_empty`` allocates one).  Scales are fp32: of ``"row"``
 blocks (1 x 128) a tensor (ceil(K / 128), rows), of ``"square"`` ones (128 x
-128) a tensor (ceil(rows / 128), ceil(K / 128)).
+128) a tensor (ceil(rows / 128), ceil(K / 128)).  All operands of a call are on
+the current device.
 """
 from __future__ import annotations
 
@@ -164,6 +165,19 @@ def _in_range(debug_flags, timeout_ms, *ints):
         raise ValueError("option out of range")
 
 
+def _here(x, *others):
+    """Refuses operands that are not all on the current device: the library
+    launches there, and a default stream's handle does not say whose it is."""
+    dev = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("operands are on different devices")
+    if dev < 0:
+        raise ValueError("CUDA tensors expected")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"operands are on cuda:{dev}, which is not the current device")
+
+
 def _on(stream):
     """Context in which what is allocated belongs to the stream that the call runs on."""
     if stream is None:
@@ -174,7 +188,8 @@ def _on(stream):
 
 
 def _handle(stream, x):
-    """The cudaStream_t that a call runs on (None: the current stream of x's device)."""
+    """The cudaStream_t that a call runs on (None: the current stream of x's
+    device, which _here has found to be the current one)."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(x.device.index)
     return _swz._stream(stream)
@@ -250,6 +265,7 @@ def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
     nearest even."""
     if torch is None:
         _init()
+    _here(x)
     q, s, qt, st, M, K = _quantize(x, _block(block), fmt, transposed, stream)
     q = q if q.shape[1] == K else q.narrow(1, 0, K)
     if not transposed:
@@ -307,6 +323,7 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
     automatic)."""
     if torch is None:
         _init()
+    _here(a, sa, b, sb, out)
     A, M, K = _matrix(a, sa, SWZ_BLOCK_ROW, "a")
     B, N, K2 = _matrix(b, sb, _block(b_block), "b")
     if K != K2:
@@ -327,6 +344,7 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
     ``out_dtype`` (default: x's type)."""
     if torch is None:
         _init()
+    _here(x, qw, sw, out)
     M, K, ldx = _rows(x, "x")
     code = _code(x.dtype, "x")
     W, N, K2 = _matrix(qw, sw, _block(w_block), "qw")
@@ -351,6 +369,7 @@ def linear_fp8_forward(x, w, *, out_dtype=None, stream=None):
     bits for linear_fp8_backward."""
     if torch is None:
         _init()
+    _here(x, w)
     qx, sx, qxt, sxt, M, K = _quantize(x, SWZ_BLOCK_ROW, "e4m3", True, stream)
     qw, sw, qwt, swt, N, K2 = _quantize(w, SWZ_BLOCK_SQUARE, "e4m3", True, stream)
     if K != K2:
@@ -369,6 +388,7 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
     qxt, sxt, qwt, swt = saved
     if torch is None:
         _init()
+    _here(dy, *saved)
     M, N, _ = _rows(dy, "dy")
     if M != qxt.shape[1] or N != qwt.shape[1]:
         raise ValueError("dy does not have the shape of the layer's output")
@@ -430,8 +450,7 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
         _init()
     if G.dim() not in (2, 3):
         raise ValueError("G: 2-D or 3-D tensor expected")
-    if not G.is_cuda:
-        raise ValueError("G: CUDA tensor expected")
+    _here(G, out)
     if max(G.shape) > INT_MAX:
         raise ValueError("G: more than 2^31 - 1 matrices, rows or columns")
     _in_range(debug_flags, timeout_ms, steps, tile)
@@ -447,8 +466,6 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     batch, m, n = g.shape
     ld = []
     for t, what in ((g, "G"), (y, "out")):
-        if not t.is_cuda:
-            raise ValueError(f"{what}: CUDA tensor expected")
         sb, sm, sn = t.stride()
         if (n > 1 and sn != 1) or (m > 1 and sm < n) or (batch > 1 and sb < (m - 1) * sm + n):
             raise ValueError(f"{what}: contiguous rows that do not overlap expected")
