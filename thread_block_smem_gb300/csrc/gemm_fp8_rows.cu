@@ -188,6 +188,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2)
     __syncwarp();
   } else if (warp == 5) {
     // ---------------- MMA issuer ----------------
+    // what the kernel before takes does not count against this one's bound
+    ptx::grid_dep_wait();
     uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 0;
     bool issued = false;
     const uint64_t bdesc = pipe::sdesc128(sB, 16, 1024), adesc = pipe::sdesc128(sA, 16, 1024);
