@@ -29,3 +29,39 @@ def test_the_bound_of_few_rows_does_not_count_the_kernel_before(swz, rows, split
     swz.gemm_fp8(*few, *b, out=out, split_k=split, timeout_ms=1)
     swz.check_status()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 520, 640), (2048, 1024, 512), (17, 512, 384)])
+def test_what_a_kernel_reads_is_what_the_one_before_wrote(swz, M, N, K):
+    # A product into the same buffer again and again, each time quantised and, as a
+    # gradient is, orthogonalised and quantised; every other pass has other operands.
+    ops = []
+    for seed in range(2):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        a = torch.randn(M, K, generator=g, device="cuda")
+        b = torch.randn(N, K, generator=g, device="cuda")
+        ops.append((*swz.quantize_fp8(a), *swz.quantize_fp8(b, "square")))
+    C = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    D = torch.empty(M, N, dtype=torch.float32, device="cuda")
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+
+    def chain(qa, sa, qb, sb, between):
+        out = []
+        swz.gemm_fp8(qa, sa, qb, sb, out=C)
+        between()
+        out += swz.quantize_fp8(C, "row", transposed=True)
+        between()
+        swz.gemm_fp8(qa, sa, qb, sb, out=D)
+        between()
+        swz.newton_schulz(D, out=Y)
+        between()
+        out += swz.quantize_fp8(Y, "square")
+        between()
+        return out
+    want = [chain(*o, torch.cuda.synchronize) for o in ops]
+    got = [chain(*ops[i % 2], lambda: None) for i in range(40)]
+    torch.cuda.synchronize()
+    swz.check_status()
+    for i, results in enumerate(got):
+        for x, w in zip(results, want[i % 2]):
+            assert torch.equal(x.contiguous().view(torch.uint8), w.contiguous().view(torch.uint8)), i

@@ -84,13 +84,16 @@ __device__ __forceinline__ uint32_t max_packed(uint32_t a, uint32_t b) {
 }
 
 // Loads eight values of a row starting at p: `n` of them exist (<= 0: none),
-// the rest read as zero.  `wide`: p is 16-byte aligned when n >= 8.
+// the rest read as zero.  `wide`: p is 16-byte aligned when n >= 8.  Plain
+// loads: the kernel before, which may still run when this one starts, may write
+// what they read, and loads through the read-only path need not stay behind the
+// wait for it.
 template <typename T>
 __device__ __forceinline__ void load8(const uint8_t* p, int n, bool wide, uint32_t* w) {
   if (n >= 8 && wide) {
 #pragma unroll
     for (int j = 0; j < T::kWords / 4; ++j) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
+      const uint4 v = reinterpret_cast<const uint4*>(p)[j];
       w[4 * j] = v.x;
       w[4 * j + 1] = v.y;
       w[4 * j + 2] = v.z;
@@ -104,9 +107,9 @@ __device__ __forceinline__ void load8(const uint8_t* p, int n, bool wide, uint32
   for (int i = 0; i < 8; ++i)
     if (i < n) {
       if constexpr (T::kBytes == 2)
-        w[i / 2] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i & 1));
+        w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i & 1));
       else
-        w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = reinterpret_cast<const uint32_t*>(p)[i];
     }
 }
 

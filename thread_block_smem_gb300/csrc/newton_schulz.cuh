@@ -43,11 +43,11 @@ __device__ __forceinline__ Scale make_scale(const double (&d)[3], double count, 
   return sc;
 }
 
+// plain loads, as f8::load8's; p may also be where the result goes
 __device__ __forceinline__ float load_any(const uint8_t* p, int64_t at, int dtype) {
-  if (dtype == SWZ_F32) return __ldg(reinterpret_cast<const float*>(p) + at);
-  if (dtype == SWZ_BF16)
-    return __bfloat162float(__ushort_as_bfloat16(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
-  return __half2float(__ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(p) + at)));
+  if (dtype == SWZ_F32) return reinterpret_cast<const float*>(p)[at];
+  if (dtype == SWZ_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[at]);
+  return __half2float(reinterpret_cast<const __half*>(p)[at]);
 }
 __device__ __forceinline__ void store_any(uint8_t* p, int64_t at, float v, int dtype) {
   if (dtype == SWZ_F32) reinterpret_cast<float*>(p)[at] = v;
