@@ -586,7 +586,7 @@ typedef struct swz_newton_schulz_opts {
  * A matrix of zeros gives zeros; one with an infinity or NaN a result that is
  * not finite.  d_workspace: 256-byte aligned device scratch of at least
  * swz_newton_schulz_workspace_size bytes, contents free before and after;
- * calls that share it must not overlap.  G and Y may be the same buffer.
+ * calls that share it must not overlap.  Y may lie over G in any way.
  * Limits: m * n <= 2^31, batch <= 65535; SWZ_EUNSUPPORTED for coefficients
  * under which singular values can pass 10^15.  Errors: SWZ_EINVAL,
  * SWZ_EUNSUPPORTED, SWZ_EARCH, SWZ_ECUDA.

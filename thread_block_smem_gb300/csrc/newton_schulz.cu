@@ -947,6 +947,24 @@ static bool sizes_ok(int batch, int m, int n) {
   return batch >= 0 && m >= 0 && n >= 0 && int64_t(m) * n <= (int64_t(1) << 31) && batch <= 65535;
 }
 
+// True when a value of Y may lie where another one of G is: each matrix and each
+// tile reads its own values of G before it writes them, but not another's.  The
+// ranges of views that share rows without sharing columns meet, their values do
+// not.
+static bool lies_across(uintptr_t ga, int64_t gs, int64_t ldg, int64_t bsg, uintptr_t ya,
+                        int64_t ys, int64_t ldy, int64_t bsy, int batch, int m, int n) {
+  auto bytes = [&](int64_t es, int64_t ld, int64_t bs) {
+    return uintptr_t(((batch - 1) * bs + (m - 1) * ld + n) * es);
+  };
+  if (ga >= ya + bytes(ys, ldy, bsy) || ya >= ga + bytes(gs, ldg, bsg)) return false;
+  if (gs != ys || (m > 1 && ldg != ldy) || (batch > 1 && bsg != bsy)) return true;
+  if (ga == ya) return false;
+  const int64_t d = ya > ga ? int64_t(ya - ga) : int64_t(ga - ya);
+  if (m == 1 || d % gs != 0 || (batch > 1 && bsg % ldg != 0)) return true;
+  const int64_t column = d / gs % ldg;
+  return column < n || column + n > ldg;
+}
+
 extern "C" int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes) {
   if (!h_bytes || !sizes_ok(batch, m, n)) return SWZ_EINVAL;
   *h_bytes = batch && m && n ? layout(uint64_t(batch), uint64_t(m), uint64_t(n)).total : 0;
@@ -1012,7 +1030,13 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   const bool wide = m <= n;
   const uint64_t d = uint64_t(wide ? m : n);
 
-  bool small = o.tile == 0 && d <= kSmallSide && (wide ? n : m) <= kSmallLong;
+  // Where Y lies across G, G has to be read before any of Y is written.  The
+  // kernels of their own do so but when their only update reads G itself, the one
+  // kernel when there is no other matrix.
+  const bool across = lies_across(ga, gs, ldg, batch_stride_g, ya, ys, ldy, batch_stride_y, batch,
+                                  m, n);
+  bool small = o.tile == 0 && d <= kSmallSide && (wide ? n : m) <= kSmallLong &&
+               !(across && batch > 1);
   if (small) {
     rc = small_pays(batch, wide ? n : m, &small);
     if (rc != SWZ_OK) return rc;
@@ -1073,7 +1097,7 @@ extern "C" int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t 
   // on 16 bytes or are no multiple of a line it reads from an fp32 copy, which is
   // left where the fp32 X will be.  Element by element in its epilogue it took 49
   // us instead of 15 at 1001 x 1001, 129 instead of 28 for 14 of 2533 x 199.
-  const bool lines = na.wide && n % 64 == 0;
+  const bool lines = na.wide && n % 64 == 0 && !(across && steps == 1);
   na.g32 = lines ? nullptr : reinterpret_cast<float*>(ws + L.master);
   na.ld_x = L.ldx;
   na.batch_x = int64_t(m) * L.ldx;

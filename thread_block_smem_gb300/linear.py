@@ -444,8 +444,8 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     """The orthogonalised update of G (m x n, or a stack batch x m x n; fp16,
     bf16 or fp32, contiguous rows): X = G / (|G|_F + eps), then ``steps`` times
     X = a X + (b A + c A^2) X with A = X X^T (on the right with X^T X when m >
-    n), ``coefficients`` = (a, b, c).  ``out`` (G's shape; may be G) or
-    ``out_dtype`` (default bf16)."""
+    n), ``coefficients`` = (a, b, c).  ``out`` (G's shape; may lie over G in any
+    way) or ``out_dtype`` (default bf16)."""
     if torch is None:
         _init()
     if G.dim() not in (2, 3):
