@@ -65,3 +65,28 @@ def test_what_a_kernel_reads_is_what_the_one_before_wrote(swz, M, N, K):
     for i, results in enumerate(got):
         for x, w in zip(results, want[i % 2]):
             assert torch.equal(x.contiguous().view(torch.uint8), w.contiguous().view(torch.uint8)), i
+
+
+def test_operands_freed_while_another_stream_works_on_them(swz):
+    # the side stream is busy when the calls are made; what they read is freed and
+    # asked for again before it gets there
+    side = torch.cuda.Stream()
+    x, w = torch.randn(256, 512, device="cuda").bfloat16(), torch.randn(384, 512, device="cuda")
+    want = swz.linear_fp8(x, *swz.quantize_fp8(w, "square"))
+    update = swz.newton_schulz(w)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    qw, sw = swz.quantize_fp8(w, "square")
+    one = x + 0
+    two = w + 0
+    side.wait_stream(torch.cuda.current_stream())
+    y = swz.linear_fp8(one, qw, sw, stream=side)
+    z = swz.newton_schulz(two, stream=side)
+    del one, two, qw, sw
+    for _ in range(4):  # what would take the memory over
+        junk = [torch.full_like(x, 7.0), torch.full_like(w, 7.0),
+                torch.full(w.shape, 7, dtype=torch.uint8, device="cuda")]
+    side.synchronize()
+    assert torch.equal(y, want) and torch.equal(z, update) and len(junk) == 3

@@ -41,6 +41,10 @@ class Operand:
     def data_ptr(self):
         return 4096
 
+    def narrow(self, dim, at, n):
+        return Operand([n if i == dim else v for i, v in enumerate(self.shape)], self.dtype, 0,
+                       self._stride)
+
 
 BIG = 2 ** 32 + 8  # an int would hold 8
 
@@ -155,3 +159,88 @@ def test_operands_on_different_devices_are_refused(swz, operator):
 def test_a_device_that_is_not_current_is_refused(swz, operator):
     with pytest.raises(ValueError, match="current device"):
         calls(swz, {name: 1 for name in calls(swz, {})[operator][0]})[operator][1]()
+
+
+class Launches:
+    """Stands in for the library: every call succeeds and is counted."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+class Kept(Operand):
+    """An operand that notes the streams it is used on."""
+
+    def __init__(self, *a, **kw):
+        super().__init__(*a, **kw)
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+    def unsqueeze(self, _):
+        return Kept((1, *self.shape), self.dtype, 0, (0, *self._stride))
+
+
+@pytest.fixture
+def launches(swz, monkeypatch):
+    linear = swz.linear
+    swz.linear._init()
+    fake = Launches()
+    monkeypatch.setattr(linear, "_L", fake)
+    monkeypatch.setattr(linear, "_empty", lambda shape, dtype, x, stream: Operand(
+        shape if isinstance(shape, tuple) else tuple(shape) if hasattr(shape, "__len__") else (shape,),
+        dtype))
+    monkeypatch.setattr(linear, "_handle", lambda stream, x: 0)
+    return fake
+
+
+def test_operands_are_kept_for_the_stream_that_uses_them(swz, launches, monkeypatch):
+    class Stream:
+        cuda_stream = 0
+
+    class ExternalStream(Stream):
+        pass
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", ExternalStream)
+    side = Stream()
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+
+    def operands(*specs):
+        return [Kept(*s) for s in specs]
+
+    def check(tensors):
+        assert launches.calls and all(t.streams == [side] for t in tensors), [t.streams for t in tensors]
+        launches.calls.clear()
+    x, = operands(((4, 128),))
+    swz.quantize_fp8(x, stream=side)
+    check([x])
+    used = operands(((4, 128), f8), ((1, 4), f32), ((4, 128), f8), ((1, 1), f32))
+    out, = operands(((4, 4),))
+    swz.gemm_fp8(*used, out=out, stream=side)
+    check(used + [out])
+    used = operands(((4, 128),), ((4, 128), f8), ((1, 1), f32))
+    out, = operands(((4, 4),))
+    swz.linear_fp8(*used, out=out, stream=side)
+    check(used + [out])
+    used = operands(((4, 128),), ((4, 128),))
+    swz.linear_fp8_forward(*used, stream=side)
+    check(used)
+    used = operands(((4, 4),), ((128, 4), f8, 0, (16, 1)), ((1, 128), f32),
+                    ((128, 4), f8, 0, (16, 1)), ((1, 1), f32))
+    swz.linear_fp8_backward(used[0], used[1:], stream=side)
+    check(used)
+    used = operands(((8, 8),), ((8, 8),))
+    swz.newton_schulz(used[0], out=used[1], stream=side)
+    check(used)
+    # the current stream, and streams that the caller made and may destroy, keep nothing
+    for stream in (None, 0, ExternalStream()):
+        x, = operands(((4, 128),))
+        swz.quantize_fp8(x, stream=stream)
+        assert x.streams == []

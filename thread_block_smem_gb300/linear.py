@@ -8,7 +8,9 @@ shape (rows, K) whose rows start on multiples of 16 bytes (``quantize_fp8``
 makes them so; ``fp8_empty`` allocates one).  Scales are fp32: of ``"row"``
 blocks (1 x 128) a tensor (ceil(K / 128), rows), of ``"square"`` ones (128 x
 128) a tensor (ceil(rows / 128), ceil(K / 128)).  All operands of a call are on
-the current device.
+the current device.  ``stream`` (a torch stream, or a cudaStream_t as an int) is
+what a call runs on instead of the current one; its operands may be freed while a
+torch stream still works on them, and what it returns belongs to that stream.
 """
 from __future__ import annotations
 
@@ -187,6 +189,18 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _keep(stream, *tensors):
+    """Memory of the operands that is freed is not handed out again before
+    `stream` is done with them.  Only for streams of torch's own: others are their
+    maker's, who may destroy them before the operands."""
+    if (stream is None or not isinstance(stream, torch.cuda.Stream) or
+            isinstance(stream, torch.cuda.ExternalStream)):
+        return
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _handle(stream, x):
     """The cudaStream_t that a call runs on (None: the current stream of x's
     device, which _here has found to be the current one)."""
@@ -279,6 +293,7 @@ def _quantize(x, b, fmt, transposed, stream):
     code, f = _code(x.dtype, "x"), FORMATS.get(fmt)
     if f is None:
         raise ValueError("fmt must be 'e4m3' or 'e5m2'")
+    _keep(stream, x)
     f8 = _f8_types[fmt]
     kb, mb = (K + 127) // 128, (M + 127) // 128
     ldq, ldt = (K + 15) // 16 * 16, (M + 15) // 16 * 16
@@ -331,6 +346,7 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
     order = _swz._order(order)
     _in_range(debug_flags, timeout_ms, order, group, tile, split_k, num_programs)
     C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a, stream)
+    _keep(stream, a, sa, b, sb, out)
     opts = swz_gemm_fp8_opts(order, group, tile, split_k, num_programs, debug_flags,
                              timeout_ms)
     _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
@@ -351,6 +367,7 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
     if K != K2:
         raise ValueError("inner dimensions differ")
     y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x, stream)
+    _keep(stream, x, qw, sw, out)
     need = _u64()
     rc = _L.swz_linear_fp8_workspace_size(M, N, K, need)
     if rc == 0:
@@ -392,6 +409,7 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
     M, N, _ = _rows(dy, "dy")
     if M != qxt.shape[1] or N != qwt.shape[1]:
         raise ValueError("dy does not have the shape of the layer's output")
+    _keep(stream, *saved)
     dx = dw = None
     if need_dx or need_dw:
         q, s, qt, st, _, _ = _quantize(dy, SWZ_BLOCK_ROW, "e4m3", need_dw, stream)
@@ -451,6 +469,7 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     if G.dim() not in (2, 3):
         raise ValueError("G: 2-D or 3-D tensor expected")
     _here(G, out)
+    _keep(stream, G, out)
     if max(G.shape) > INT_MAX:
         raise ValueError("G: more than 2^31 - 1 matrices, rows or columns")
     _in_range(debug_flags, timeout_ms, steps, tile)
