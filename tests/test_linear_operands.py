@@ -244,3 +244,40 @@ def test_operands_are_kept_for_the_stream_that_uses_them(swz, launches, monkeypa
         x, = operands(((4, 128),))
         swz.quantize_fp8(x, stream=stream)
         assert x.streams == []
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that the entry points take for one on the device."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def on_device(*shape, dtype=torch.float32, grad=False):
+    t = torch.zeros(shape).to(dtype).as_subclass(OnDevice)
+    return t.requires_grad_() if grad else t
+
+
+def test_a_lost_gradient_is_an_error_in_the_backward(swz, launches, monkeypatch):
+    # linear_fp8, gemm_fp8 and newton_schulz have no gradient; a backward through
+    # them says so instead of leaving their inputs without one
+    monkeypatch.setattr(swz.linear, "_empty",
+                        lambda shape, dtype, x, stream: torch.zeros(shape, dtype=dtype))
+    f8 = torch.float8_e4m3fn
+    q, s = on_device(4, 128, dtype=f8), on_device(1, 4)
+    w, sw = on_device(4, 128, dtype=f8), on_device(1, 1)
+    x, sx = on_device(4, 128, grad=True), on_device(1, 4, grad=True)
+    for call in (lambda: swz.linear_fp8(x, w, sw), lambda: swz.newton_schulz(x),
+                 lambda: swz.gemm_fp8(q, sx, w, sw)):
+        y = call()
+        assert y.requires_grad
+        with pytest.raises(RuntimeError, match="no gradient"):
+            y.float().sum().backward()
+        with torch.no_grad():
+            assert not call().requires_grad
+    # where nothing asks for one, and into a buffer of the caller's, as before
+    assert not swz.gemm_fp8(q, s, w, sw).requires_grad
+    assert not swz.linear_fp8(x.detach(), w, sw).requires_grad
+    out = torch.zeros(4, 4).as_subclass(OnDevice)
+    assert swz.linear_fp8(x, w, sw, out=out) is out and not out.requires_grad

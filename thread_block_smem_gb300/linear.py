@@ -11,6 +11,11 @@ blocks (1 x 128) a tensor (ceil(K / 128), rows), of ``"square"`` ones (128 x
 the current device.  ``stream`` (a torch stream, or a cudaStream_t as an int) is
 what a call runs on instead of the current one; its operands may be freed while a
 torch stream still works on them, and what it returns belongs to that stream.
+
+``fp8_linear`` is the form with a gradient.  ``gemm_fp8``, ``linear_fp8`` and
+``newton_schulz`` have none: a backward through what they return raises
+(``out`` takes values only), and ``linear_fp8_forward`` and ``_backward`` are for
+callers who carry gradients themselves.
 """
 from __future__ import annotations
 
@@ -122,16 +127,29 @@ def swz_newton_schulz_workspace_size(batch, m, n):
 # needs is looked up once: torch, the type codes, the library.
 torch = None
 _u64 = ctypes.c_uint64
-_codes = _f8_codes = _f8_types = _L = None
+_codes = _f8_codes = _f8_types = _L = _NoGradient = None
 
 
 def _init():
-    global torch, _codes, _f8_codes, _f8_types, _L
+    global torch, _codes, _f8_codes, _f8_types, _L, _NoGradient
     import torch as t
     _codes = {t.float16: _swz.SWZ_F16, t.bfloat16: _swz.SWZ_BF16, t.float32: SWZ_F32}
     _f8_codes = {t.float8_e4m3fn: SWZ_E4M3, t.float8_e5m2: SWZ_E5M2}
     _f8_types = {"e4m3": t.float8_e4m3fn, "e5m2": t.float8_e5m2}
     _L = _swz.lib()
+
+    class NoGradient(t.autograd.Function):
+        @staticmethod
+        def forward(ctx, what, y, *inputs):
+            ctx.what = what
+            ctx.mark_dirty(y)
+            return y
+
+        @staticmethod
+        def backward(ctx, *dy):
+            raise RuntimeError(f"{ctx.what} has no gradient (fp8_linear has one)")
+
+    _NoGradient = NoGradient
     torch = t
 
 
@@ -268,6 +286,16 @@ def _output(out, dtype, M, N, x, stream):
     return out, ld, code
 
 
+def _no_gradient(what, y, *inputs):
+    """y, through which a backward raises if one of the inputs asks for a gradient:
+    the library's kernels record none, and without this it would just be missing."""
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if t.requires_grad:
+                return _NoGradient.apply(what, y, *inputs)
+    return y
+
+
 # ---- operators --------------------------------------------------------------------
 def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
     """(q, scales) of x (M x K; fp16, bf16 or fp32, contiguous rows), with
@@ -351,7 +379,7 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
                              timeout_ms)
     _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
                 "swz_gemm_fp8")
-    return C
+    return C if out is not None else _no_gradient("gemm_fp8", C, a, sa, b, sb)
 
 
 def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=None):
@@ -377,7 +405,7 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
                                ws.data_ptr() if need else None, need, _handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_linear_fp8")
-    return y
+    return y if out is not None else _no_gradient("linear_fp8", y, x, qw, sw)
 
 
 def linear_fp8_forward(x, w, *, out_dtype=None, stream=None):
@@ -474,7 +502,8 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
         raise ValueError("G: more than 2^31 - 1 matrices, rows or columns")
     _in_range(debug_flags, timeout_ms, steps, tile)
     code = _code(G.dtype, "G")
-    if out is None:
+    fresh = out is None
+    if fresh:
         ycode = _code(out_dtype or torch.bfloat16, "out_dtype")
         out = _empty(G.shape, out_dtype or torch.bfloat16, G, stream)
     else:
@@ -497,4 +526,4 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     _swz._check(_L.swz_newton_schulz(g.data_ptr(), code, *ld[0], y.data_ptr(), ycode, *ld[1], batch, m,
                                      n, steps, a, b, c, eps, opts, ws.data_ptr(), need,
                                      _handle(stream, G)), "swz_newton_schulz")
-    return out
+    return _no_gradient("newton_schulz", out, G) if fresh else out
