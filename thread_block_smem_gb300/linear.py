@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 
 import thread_block_smem_gb300 as _swz
 
@@ -452,13 +453,19 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
     return dx, dw
 
 
+def _with_rows(t):
+    """t, or a copy of it whose rows are contiguous and apart."""
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
 _function = None
 
 
 def fp8_linear(x, w):
-    """y = x W^T with its gradient, for torch.autograd: x (..., K), w (N, K);
-    forward and backward as linear_fp8_forward / linear_fp8_backward, the
-    gradient of w in fp32 rounded to w's type.  A second derivative raises."""
+    """y = x W^T with its gradient, for torch.autograd: x (..., K) and w (N, K),
+    of any layout (copied where rows are not contiguous); forward and backward
+    as linear_fp8_forward / linear_fp8_backward, the gradient of w in fp32
+    rounded to w's type.  A second derivative raises."""
     global _function
     if _function is None:
         if torch is None:
@@ -467,7 +474,7 @@ def fp8_linear(x, w):
         class Fp8Linear(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, w):
-                y, saved = linear_fp8_forward(x, w)
+                y, saved = linear_fp8_forward(_with_rows(x), _with_rows(w))
                 ctx.save_for_backward(*saved)
                 ctx.w_dtype = w.dtype
                 return y
@@ -475,13 +482,12 @@ def fp8_linear(x, w):
             @staticmethod
             @torch.autograd.function.once_differentiable
             def backward(ctx, dy):
-                dy = dy if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1] else dy.contiguous()
                 return linear_fp8_backward(
-                    dy, ctx.saved_tensors, need_dx=ctx.needs_input_grad[0],
+                    _with_rows(dy), ctx.saved_tensors, need_dx=ctx.needs_input_grad[0],
                     need_dw=ctx.needs_input_grad[1], dw_dtype=ctx.w_dtype)
 
         _function = Fp8Linear
-    flat = x.reshape(-1, x.shape[-1])
+    flat = x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
     return _function.apply(flat, w).reshape(*x.shape[:-1], w.shape[0])
 
 
