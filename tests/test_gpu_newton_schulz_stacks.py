@@ -69,3 +69,50 @@ def test_results_beside_their_input(swz, shape):
         swz.check_status()
         assert torch.equal(left[:, :, n + 8:], want)
         assert torch.equal(left[:, :, :n + 8], buf[:, :, :n + 8])
+
+
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("shape", [(3, 130, 200), (5, 200, 64), (9, 33, 33), (4, 520, 300),
+                                   (2, 300, 640)])
+def test_a_stack_is_its_matrices(swz, shape, tile):
+    # sizes of magnitudes apart, so that a neighbour's scale would show
+    G = normal(shape, torch.float32, 2) * torch.logspace(-6, 6, shape[0]).reshape(-1, 1, 1)
+    G = G.cuda()
+    Y = swz.newton_schulz(G, out_dtype=torch.float32, tile=tile)
+    swz.check_status()
+    for i in range(shape[0]):
+        assert torch.equal(Y[i], swz.newton_schulz(G[i], out_dtype=torch.float32, tile=tile)), i
+
+
+@pytest.mark.parametrize("shape", [(7, 64, 64), (5, 100, 333), (6, 300, 90), (5, 256, 320),
+                                   (40, 100, 1030), (4, 1300, 200)])
+def test_a_stack_in_another_order(swz, shape):
+    G = normal(shape, torch.bfloat16, 2) * torch.logspace(-6, 6, shape[0]).reshape(-1, 1, 1)
+    G = G.bfloat16().cuda()
+    order = torch.randperm(shape[0], generator=torch.Generator().manual_seed(1)).cuda()
+    Y = swz.newton_schulz(G)
+    assert torch.equal(swz.newton_schulz(G[order]), Y[order])
+    swz.check_status()
+
+
+@pytest.mark.parametrize("tile", [0, 128, 256])
+@pytest.mark.parametrize("shape", [(64, 64), (100, 333), (333, 100), (128, 1100), (256, 512),
+                                   (301, 203), (3, 70, 150)])
+def test_half_precision_in_and_out(swz, shape, tile):
+    G = normal(shape, torch.float16, sum(shape))
+    for out in (torch.float16, torch.float32):
+        Y = swz.newton_schulz(G.cuda(), out_dtype=out, tile=tile)
+        swz.check_status()
+        check(Y, G)
+    G = normal(shape, torch.float32, sum(shape))
+    check(swz.newton_schulz(G.cuda(), out_dtype=torch.float16, tile=tile), G)
+
+
+# more tiles than CTA pairs: of the update (81 for 76), and of every product (84 and 144)
+@pytest.mark.parametrize("shape", [(2300, 2310), (4, 1300, 1290)])
+def test_pairs_take_more_than_one_tile(swz, shape):
+    G = normal(shape, torch.float32, 7)
+    Y = swz.newton_schulz(G.cuda(), out_dtype=torch.float32, tile=256)
+    swz.check_status()
+    check(Y, G)
+    assert torch.equal(Y, swz.newton_schulz(G.cuda(), out_dtype=torch.float32, tile=256))
