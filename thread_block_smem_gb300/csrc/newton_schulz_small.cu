@@ -1,8 +1,8 @@
 // newton_schulz_small.cu -- swz_newton_schulz for matrices with a short side
 // of up to 128 and a long one of up to 2048: all steps in one kernel.
 //
-// Bound: latency.  In kernels of their own three products a step cost 4 to 6 us a
-// launch, 55 to 90 us for five steps, whatever the size.
+// Bound: latency.  In kernels of their own three products a step cost 3 to 6 us a
+// launch, 54 to 85 us for five steps, whatever the size.
 // Here a cluster of 1 to 8 CTAs holds a matrix: each CTA has the d short rows
 // of X and up to 256 of its long columns in shared memory and TMEM, and
 //   P = X X^T     is summed over the cluster (each rank adds its share of the
@@ -17,10 +17,13 @@
 // here, and matrices this small average over few roundings: one fp16 each was
 // 0.17 % off on 64 x 64, this is 0.06 %.
 //
-// Measured, five steps, bf16: 64 x 64 31 us against 55 in kernels of their own, 128 x
-// 128 44 against 58, 128 x 512 60 against 65; at 128 x 1024 and more both take as
-// long.  A step takes about 7000 cycles on a cluster, most of them its sum: two
-// barriers and the remote reads between them.
+// Measured, five steps, bf16: 64 x 64 25 us against 54 in kernels of their own, 128 x
+// 128 35 against 56, 128 x 512 51 against 64, 128 x 2048 74 against 85.  From one
+// step and five: 10, 15, 16 and 26 us of these are there whatever the steps --
+// launch, G (value by value: its rows start anywhere), norm, first X, result -- and
+// a step takes 3.1, 4.0, 7.0 and 9.6 us.  A CTA of 128 columns alone takes 4.0 for it;
+// in a cluster its sum adds 2 to 3.5: two barriers and the remote reads between
+// them.
 #include <math.h>
 
 #include <mutex>
@@ -496,9 +499,12 @@ static cudaLaunchConfig_t config(int batch, uint32_t ranks, cudaLaunchAttribute*
 
 // Waves of matrices that run at a time, by the ranks of one, against the
 // products' launches, whose time grows with the matrices.  Measured (one kernel,
-// launches; us): 64 x 64 31, 55; 128 x 128 44, 58; 600 of them 177, 212; 70 of 128 x
-// 256 58, 76; 152 of them (two waves) 116, 106; 128 x 2048 89, 84; 14 of them 94, 111;
-// 64 of them 588, 240.
+// launches; us, five steps): 64 x 64 25, 54; 128 x 128 35, 56; 600 of them 138, 233;
+// 128 x 256 47, 61; 152 of them (two waves) 96, 122; 40 of 100 x 512 (two waves) 102,
+// 96; 128 x 1024 54, 71; 14 of 128 x 1100 67, 105; 128 x 2048 74, 85; 64 of them 375, 250.
+// The rule weighs five steps, the usual number: of a single one the launches
+// take up to 12 us less from 128 columns on (128 x 128 18 to 19, 128 x 512 19 to 23, 128 x
+// 2048 23 to 35).
 int small_pays(int batch, int len, bool* pays) {
   static std::mutex mu;
   static int resident[64][4] = {};  // clusters of 1, 2, 4, 8 at a time
@@ -520,9 +526,8 @@ int small_pays(int batch, int len, bool* pays) {
     fit = resident[dev][at];
   }
   const double waves = double((batch + fit - 1) / fit);
-  const double wave[4] = {44.0, 57.0, 62.0, 60.0 + 0.014 * len};
-  // 17 launches take the host 90 us; replayed from a graph they do not wait for it
-  *pays = waves * wave[at] <= fmax(90.0, 57.0 + 0.0135 * len + batch * (0.12 + 0.0009 * len));
+  const double wave[4] = {35.0, 47.0, 51.0, 44.0 + 0.016 * len};
+  *pays = waves * wave[at] <= 57.0 + 0.0135 * len + batch * (0.12 + 0.0009 * len);
   return SWZ_OK;
 }
 
