@@ -516,7 +516,8 @@ typedef struct swz_fp8_matrix {
  *   F = 448 for e4m3, 57344 for e5m2), q = x * r rounded to nearest even.
  * A block of zeros gives zeros; one that holds an infinity or NaN gives a
  * scale that is not finite and reads back as not finite.  The bytes up to the
- * next multiple of 16 of a row of qt (8 of q) are written as zeros.
+ * next multiple of 16 of a row of qt (8 of q) are written too: zeros, NaN where
+ * their block holds a NaN.
  * M = 0 or K = 0: no-op.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
  */
 int swz_quantize_fp8(const void* x, int dtype, int64_t ldx, int M, int K, int block, int fmt,
@@ -545,8 +546,11 @@ typedef struct swz_gemm_fp8_opts {
  *             * sum over k in kb of  A[m, k] * B[n, k]
  * A: M x K in row blocks; B: N x K in row or square blocks; formats free on
  * each side.  C: M x N, rows ldc elements apart, SWZ_F32, SWZ_BF16 or SWZ_F16
- * (written, never read); sums in fp32, rounded once.  Any M, N, K >= 0 (K = 0
- * writes zeros); rows of C that start on 16 or 32 bytes are stored wider.
+ * (written, never read); sums in fp32, rounded once.  A block's two scales are
+ * multiplied first, in fp32, and their product has to be in its range: e4m3
+ * blocks whose largest magnitudes multiply to 3 * 10^-33 up to 6 * 10^43.  Any M,
+ * N, K >= 0 (K = 0 writes zeros); rows of C that start on 16 or 32 bytes are
+ * stored wider.
  * The result is deterministic; the automatic choice of tile and split depends
  * on the sizes and the SM count only.  Errors: SWZ_EINVAL, SWZ_ENOTBIJECTIVE,
  * SWZ_EUNSUPPORTED (A in square blocks, unknown tile or split, a split of more
@@ -569,7 +573,9 @@ int swz_linear_fp8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
 
 /* Options of swz_newton_schulz; NULL = all zero. */
 typedef struct swz_newton_schulz_opts {
-  int tile;             /* 0 automatic for each product; 128 or 256 (CTA pair) */
+  int tile;             /* 0 automatic: one kernel for all steps where the
+                           matrices are small, else tiles 64, 128 or 256 wide,
+                           the same for all products; 128; 256 (CTA pair)       */
   uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                        */
   uint32_t timeout_ms;  /* bound of every device wait; 0 = 2000 ms             */
 } swz_newton_schulz_opts;
@@ -583,6 +589,8 @@ typedef struct swz_newton_schulz_opts {
  * and Y = X (rows ldy, matrices batch_stride_y apart; y_dtype).  Products
  * with fp16 operands scaled by powers of two and fp32 sums; the a X term in
  * fp32 in all steps but the last two (in the first of any number of steps).
+ * That leaves Y 0.06 to 0.15 % off (Frobenius norm, five steps) besides its own
+ * rounding, which for SWZ_BF16 is 0.17 %.
  * A matrix of zeros gives zeros; one with an infinity or NaN a result that is
  * not finite.  d_workspace: 256-byte aligned device scratch of at least
  * swz_newton_schulz_workspace_size bytes, contents free before and after;

@@ -1,5 +1,5 @@
-// f8.cuh -- the 8-bit block quantisation rule, shared by the quantiser and
-// by the few-row product that quantises its rows on the way.
+// f8.cuh -- the 8-bit block quantisation rule, and the loads of eight values
+// that the quantiser and the orthogonalisation share.
 //
 // A block of 128 (or 128 x 128) values with largest magnitude `amax` is held
 // as q = rn_f8(x * r) with

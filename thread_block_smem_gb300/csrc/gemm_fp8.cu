@@ -31,10 +31,13 @@
 // 16 warps of half the columns the same.  With a quarter of the MMAs 8192^3
 // takes 392 us, with half the operand traffic as well the same.  Measured at
 // 8192^3, bf16 result: 410-425 us, 2.6-2.7 PFLOP/s, 0.70 of twice the measured
-// bf16 peak; B in row blocks 650 us: a scale a column is twice the arithmetic,
-// which costs little (432 us without the reads), and 64 registers a thread and
-// block from shared memory, 512 cycles of the SM's.  TMEM's 16-lane order reads a
-// quarter of the scales, but half as many lanes at a time: 697.
+// bf16 peak (467 in a stream of seconds, at 1.70 GHz under the power cap); tensor
+// pipe 56 % busy, issue slots 50 %.  B in row blocks 650 us: a scale a column is
+// twice the arithmetic, which costs little (432 us without the reads), and 64
+// registers a thread and block from shared memory, whose pipe the counters show
+// busy for 46 % of the time (11 % with square blocks).  TMEM's 16-lane order reads
+// a quarter of the scales, but half as many lanes at a time: 697.  The single-CTA
+// kernels spill 40 bytes a thread, the pairs nothing.
 #include <mutex>
 #include <type_traits>
 

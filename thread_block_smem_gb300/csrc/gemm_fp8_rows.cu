@@ -6,7 +6,7 @@
 // change places: 128 rows of B are the tensor core's M, the rows of A its N
 // (16 or 32).  A block of K is then 16 KB of B through TMA, one small MMA
 // group, and 16 or 32 columns of TMEM to scale and add; the stages of two CTAs keep
-// up to 190 KB of B in flight on an SM.
+// up to 160 KB of B (128 with 32 rows) in flight on an SM.
 //   * 7 warps: 0-3 the sums (TMEM lanes 32 w .., one row of B a thread), 4 TMA
 //     producer, 5 MMA issue, 6 scales.
 //   * A cluster of 1 to 8 CTAs shares a tile's K; the partial tiles are added

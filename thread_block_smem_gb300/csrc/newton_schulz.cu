@@ -33,8 +33,10 @@
 // K x N operand is read N-major from shared memory, X^T X takes both operands
 // so, and nothing is ever transposed in memory.
 //
-// Measured, fp32 G, five steps: 4096 x 4096 950-970 us (1.42 PFLOP/s of the products
-// computed, 0.75 of the measured bf16 peak), 2048 x 2048 238, 1024 x 1024 112.
+// Measured, fp32 G, five steps: 4096 x 4096 945-970 us in short runs (1.42 PFLOP/s of
+// the products computed, 0.75 of the measured bf16 peak) and 1060 in a stream of
+// seconds, at 1.75 GHz under the power cap; 2048 x 2048 238, 1024 x 1024 113.  The pair
+// kernel spills 48 bytes a thread, the 128-wide one 8, the 64-wide one nothing.
 // Below 2048 it is 17 launches of 5 to 10 us that depend on one another: a
 // launch's first load, its last tile's epilogue and the next one's start are not
 // hidden by anything.

@@ -23,7 +23,8 @@
 // launch, G (value by value: its rows start anywhere), norm, first X, result -- and
 // a step takes 3.1, 4.0, 7.0 and 9.6 us.  A CTA of 128 columns alone takes 4.0 for it;
 // in a cluster its sum adds 2 to 3.5: two barriers and the remote reads between
-// them.
+// them.  fp32 G: 24, 31, 48 (100 x 333) and 69 us (2048 x 128); tall bf16 ones take up
+// to 13 us more than wide ones.
 #include <math.h>
 
 #include <mutex>

@@ -12,7 +12,8 @@
 //
 // Measured (bytes read and written; the copy bandwidth is 6.8 TB/s): 8192 x 4096
 // bf16 with x^T, square blocks 22.6 us (5.9 TB/s), row blocks 26.1 (5.1);
-// 8192 x 8192 42.1 (6.4) and 45.9 (5.8); 10240 x 4096 fp32, square, 39.5 (6.4).
+// 8192 x 8192 42.1 (6.4) and 45.9 (5.8), row blocks without x^T 34.6 to 37.2 (5.5 to
+// 5.9); 10240 x 4096 fp32, square, 38.3 (6.6).
 // Row blocks keep a scale for each of a thread's 8 rows and 8 columns and
 // exchange maxima along both: 64 registers against 48, 44 % of the warps
 // resident, and the loads of the next blocks wait for the arithmetic of these.

@@ -497,7 +497,11 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     bf16 or fp32, contiguous rows): X = G / (|G|_F + eps), then ``steps`` times
     X = a X + (b A + c A^2) X with A = X X^T (on the right with X^T X when m >
     n), ``coefficients`` = (a, b, c).  ``out`` (G's shape; may lie over G in any
-    way) or ``out_dtype`` (default bf16)."""
+    way) or ``out_dtype`` (default bf16).
+
+    The products take fp16 operands with fp32 sums, whatever the types of G and
+    the result: after five steps X is 0.06 to 0.15 % off, next to the 0.17 % that a
+    bf16 result's rounding costs."""
     if torch is None:
         _init()
     if G.dim() not in (2, 3):
