@@ -212,7 +212,7 @@ def _keep(stream, *tensors):
     """Memory of the operands that is freed is not handed out again before
     `stream` is done with them.  Only for streams of torch's own: others are their
     maker's, who may destroy them before the operands."""
-    if (stream is None or not isinstance(stream, torch.cuda.Stream) or
+    if (not isinstance(stream, torch.cuda.Stream) or
             isinstance(stream, torch.cuda.ExternalStream)):
         return
     for t in tensors:
@@ -290,10 +290,9 @@ def _output(out, dtype, M, N, x, stream):
 def _no_gradient(what, y, *inputs):
     """y, through which a backward raises if one of the inputs asks for a gradient:
     the library's kernels record none, and without this it would just be missing."""
-    if torch.is_grad_enabled():
-        for t in inputs:
-            if t.requires_grad:
-                return _NoGradient.apply(what, y, *inputs)
+    for t in inputs:
+        if t.requires_grad and torch.is_grad_enabled():
+            return _NoGradient.apply(what, y, *inputs)
     return y
 
 
@@ -322,7 +321,8 @@ def _quantize(x, b, fmt, transposed, stream):
     code, f = _code(x.dtype, "x"), FORMATS.get(fmt)
     if f is None:
         raise ValueError("fmt must be 'e4m3' or 'e5m2'")
-    _keep(stream, x)
+    if stream is not None:
+        _keep(stream, x)
     f8 = _f8_types[fmt]
     kb, mb = (K + 127) // 128, (M + 127) // 128
     ldq, ldt = (K + 15) // 16 * 16, (M + 15) // 16 * 16
@@ -375,7 +375,8 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
     order = _swz._order(order)
     _in_range(debug_flags, timeout_ms, order, group, tile, split_k, num_programs)
     C, ldc, code = _output(out, out_dtype or torch.bfloat16, M, N, a, stream)
-    _keep(stream, a, sa, b, sb, out)
+    if stream is not None:
+        _keep(stream, a, sa, b, sb, out)
     opts = swz_gemm_fp8_opts(order, group, tile, split_k, num_programs, debug_flags,
                              timeout_ms)
     _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
@@ -396,7 +397,8 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
     if K != K2:
         raise ValueError("inner dimensions differ")
     y, ldy, ycode = _output(out, out_dtype or x.dtype, M, N, x, stream)
-    _keep(stream, x, qw, sw, out)
+    if stream is not None:
+        _keep(stream, x, qw, sw, out)
     need = _u64()
     rc = _L.swz_linear_fp8_workspace_size(M, N, K, need)
     if rc == 0:
@@ -438,7 +440,8 @@ def linear_fp8_backward(dy, saved, *, need_dx=True, need_dw=True, dx_dtype=None,
     M, N, _ = _rows(dy, "dy")
     if M != qxt.shape[1] or N != qwt.shape[1]:
         raise ValueError("dy does not have the shape of the layer's output")
-    _keep(stream, *saved)
+    if stream is not None:
+        _keep(stream, *saved)
     dx = dw = None
     if need_dx or need_dw:
         q, s, qt, st, _, _ = _quantize(dy, SWZ_BLOCK_ROW, "e4m3", need_dw, stream)
@@ -507,7 +510,8 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     if G.dim() not in (2, 3):
         raise ValueError("G: 2-D or 3-D tensor expected")
     _here(G, out)
-    _keep(stream, G, out)
+    if stream is not None:
+        _keep(stream, G, out)
     if max(G.shape) > INT_MAX:
         raise ValueError("G: more than 2^31 - 1 matrices, rows or columns")
     _in_range(debug_flags, timeout_ms, steps, tile)
