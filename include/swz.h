@@ -606,6 +606,145 @@ int swz_newton_schulz(const void* G, int dtype, int64_t ldg, int64_t batch_strid
                       uint64_t workspace_bytes, void* stream);
 int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes);
 
+/* ---- 8-bit integers: a scale for each row -------------------------------------
+ * No source page has a counterpart: the product of 8-bit integers with one fp32
+ * scale for each row of either operand (a token of the activations, an output
+ * channel of the weights), and what makes those operands.  A matrix of them is K
+ * contiguous, its base 16-byte aligned and its rows `ld` bytes apart, a multiple
+ * of 16 (what lies beyond the last column of a row is not looked at); element
+ * (m, k) is data[m * ld + k] times scales[m].
+ */
+
+/*
+ * swz_quantize_int8 -- x (M x K, rows ldx elements apart; SWZ_F16, SWZ_BF16 or
+ * SWZ_F32) to q (M x K) and its rows' scales.  For a row with largest magnitude
+ * amax:
+ *   ac = max(amax, 2^-96), r = 127 / ac, scale = ac / 127 (both rounded to fp32),
+ *   q = x * r, the exact product, rounded to the nearest whole number, ties to
+ *   even: -127 .. 127
+ * A row of zeros gives zeros; one that holds an infinity or NaN gives zeros with
+ * the scale NaN.  The bytes up to the next multiple of 8 of a row of q are written
+ * too, with zeros.  M = 0: no-op; K = 0 writes the scales only.  Errors:
+ * SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void* q, int64_t ldq,
+                      float* scales, void* stream);
+
+/* Options of swz_gemm_int8; NULL = serpentine order with strips of 8, the rest
+ * zero. */
+typedef struct swz_gemm_int8_opts {
+  int order, group;     /* tile order as in swz_gemm                            */
+  int tile;             /* 0 automatic; 128: one CTA, 128 x 128 of C; 256: CTA
+                           pair, 256 x 256                                      */
+  int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share the K
+                           of a tile that is not a pair's                       */
+  uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                         */
+  uint32_t timeout_ms;  /* bound of every device wait; 0 = 2000 ms              */
+} swz_gemm_int8_opts;
+
+/*
+ * swz_gemm_int8 -- C = A * B^T:
+ *   C[m, n] = sa[m] * sb[n] * sum over k of A[m, k] * B[n, k]
+ * A: M x K and B: N x K as above, any values -128 .. 127; C: M x N, rows ldc
+ * elements apart, SWZ_F32, SWZ_BF16 or SWZ_F16 (written, never read).  The sum is
+ * exact; it is rounded to fp32 and multiplied by sa * sb, which is rounded to
+ * fp32, and the product is rounded to fp32 and to C's type.  K up to 131071, so
+ * that the sum fits 32 bits; any M, N >= 0 (K = 0 writes zeros).
+ * d_workspace: 16-byte aligned device scratch of at least
+ * swz_gemm_int8_workspace_size bytes, contents free before and after; calls that
+ * share it must not overlap; NULL when the size is 0.  Errors: SWZ_EINVAL,
+ * SWZ_ENOTBIJECTIVE, SWZ_EUNSUPPORTED (unknown tile or split, a split of more
+ * parts than blocks of K), SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const void* B, int64_t ldb,
+                  const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,
+                  const swz_gemm_int8_opts* opts, void* d_workspace, uint64_t workspace_bytes,
+                  void* stream);
+int swz_gemm_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
+
+/*
+ * swz_linear_int8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is
+ * quantised by rows as in swz_quantize_int8 and multiplied by W (N x K; 8-bit
+ * integers with the scales sw) as in swz_gemm_int8.  d_workspace: as there, of
+ * swz_linear_int8_workspace_size bytes.  Errors: as swz_gemm_int8.
+ */
+int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void* W, int64_t ldw,
+                    const float* sw, void* y, int64_t ldy, int y_dtype, int M, int N, int K,
+                    void* d_workspace, uint64_t workspace_bytes, void* stream);
+int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
+
+/* ---- around a linear layer in training ------------------------------------------
+ * The layer norm before it with its gradient, and the norm and clipping of the
+ * gradients after it.  Types are SWZ_F16, SWZ_BF16 or SWZ_F32 each; arithmetic is
+ * fp32, every result is rounded once.
+ */
+
+/*
+ * swz_layer_norm -- by rows of x (M x N, rows ldx elements apart):
+ *   mean = sum x / N, rstd = 1 / sqrt(sum (x - mean)^2 / N + eps)
+ *   y = (x - mean) * rstd * weight + bias      (rows ldy apart)
+ * weight and bias: N values each, NULL for 1 and 0 (their types are then not
+ * used).  mean and rstd (M values each) are written for the gradient.  y may be x
+ * itself where types and rows are the same; otherwise they must not overlap.
+ * M = 0 or N = 0: no-op.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void* weight, int w_dtype,
+                   const void* bias, int b_dtype, double eps, void* y, int y_dtype, int64_t ldy,
+                   float* mean, float* rstd, int M, int N, void* stream);
+
+/*
+ * swz_layer_norm_backward -- with g = dy * weight and xhat = (x - mean) * rstd:
+ *   dx = rstd * (g - sum g / N - xhat * sum (g * xhat) / N)     by rows
+ *   dw = sum of dy * xhat, db = sum of dy                       over the rows
+ * from the operands and results of swz_layer_norm.  dx, dw (N values) and db (N
+ * values; of dw_dtype too) may each be NULL where it is not wanted, not all of
+ * them; dx may be dy or x itself where types and rows are the same.  The sums over
+ * rows are taken in an order that depends on the sizes and the device only (no
+ * atomics).  M = 0 writes zeros to dw and db.  d_workspace (for dw and db):
+ * 16-byte aligned device scratch of at least
+ * swz_layer_norm_backward_workspace_size bytes, contents free before and after;
+ * calls that share it must not overlap.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
+ */
+int swz_layer_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x, int dtype,
+                            int64_t ldx, const void* weight, int w_dtype, const float* mean,
+                            const float* rstd, void* dx, int dx_dtype, int64_t lddx, void* dw,
+                            void* db, int dw_dtype, int M, int N, void* d_workspace,
+                            uint64_t workspace_bytes, void* stream);
+int swz_layer_norm_backward_workspace_size(int M, int N, uint64_t* h_bytes);
+
+/* One gradient of a list (a host array): n contiguous values. */
+typedef struct swz_grad {
+  const void* in;
+  void* out;          /* swz_clip_grad_norm: where the clipped values go; may be
+                         `in` where the types are the same                      */
+  int64_t n;
+  int dtype;          /* of in                                                   */
+  int out_dtype;      /* of out                                                  */
+} swz_grad;
+
+/*
+ * swz_grad_norm -- *norm (device) = sqrt(sum of the squares of all values of the
+ * `count` tensors).  Sums in 64 bits over partial sums of 64 values in fp32, in an
+ * order that depends on the sizes and the device only; squares that would leave
+ * fp32's range are scaled.  An infinity or NaN gives an infinite or NaN norm.
+ *
+ * swz_clip_grad_norm -- the same norm, and every out = in * f in fp32, rounded once,
+ * with f = min(1, max_norm / (norm + eps)) (1 where norm + eps is 0, NaN where the
+ * norm is NaN).  max_norm and eps are at least 0.  No `out` may overlap another
+ * tensor's `in` or `out`, or its own `in` unless it is the same tensor.
+ *
+ * d_workspace: 16-byte aligned device scratch of at least
+ * swz_grad_norm_workspace_size bytes, contents free before and after; calls that
+ * share it must not overlap.  The list is read during the call; captured into a
+ * CUDA graph, its pointers are the graph's.  Errors: SWZ_EINVAL, SWZ_EARCH,
+ * SWZ_ECUDA.
+ */
+int swz_grad_norm(const swz_grad* grads, int count, float* norm, void* d_workspace,
+                  uint64_t workspace_bytes, void* stream);
+int swz_clip_grad_norm(const swz_grad* grads, int count, double max_norm, double eps, float* norm,
+                       void* d_workspace, uint64_t workspace_bytes, void* stream);
+int swz_grad_norm_workspace_size(int count, uint64_t* h_bytes);
+
 /* Synchronises `stream`, then returns and clears the current device's
  * status word: SWZ_OK, or SWZ_ETIMEOUT if a kernel's bounded wait expired
  * since the last check. */

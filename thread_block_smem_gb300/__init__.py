@@ -10,7 +10,10 @@ Two layers:
   * ``tile_map``, ``gemm``, ``transpose``, ``gemm_plan`` -- the same calls on
     torch tensors (pointers and the current stream are taken from them); the
     linear-layer operators (``quantize_fp8``, ``gemm_fp8``, ``linear_fp8`` and
-    its gradient, ``newton_schulz``) are in ``linear.py``.
+    its gradient, ``newton_schulz``) are in ``linear.py``, those in 8-bit integers
+    (``quantize_int8``, ``gemm_int8``, ``linear_int8``) in ``int8.py``, and what
+    stands around a layer in training (``layer_norm``, ``grad_norm``,
+    ``clip_grad_norm``) in ``training.py``.
 """
 from __future__ import annotations
 
@@ -41,7 +44,11 @@ EXPORTS = ["swz_tile_map", "swz_is_bijective", "swz_gemm", "swz_gemm_ex", "swz_g
            "swz_tc_rate_ex",
            "swz_l2_model_bytes", "swz_calibrate", "swz_gemm_die_plan", "swz_quantize_fp8",
            "swz_gemm_fp8", "swz_linear_fp8", "swz_linear_fp8_workspace_size",
-           "swz_newton_schulz", "swz_newton_schulz_workspace_size"]
+           "swz_newton_schulz", "swz_newton_schulz_workspace_size", "swz_quantize_int8",
+           "swz_gemm_int8", "swz_gemm_int8_workspace_size", "swz_linear_int8",
+           "swz_linear_int8_workspace_size", "swz_layer_norm", "swz_layer_norm_backward",
+           "swz_layer_norm_backward_workspace_size", "swz_grad_norm", "swz_clip_grad_norm",
+           "swz_grad_norm_workspace_size"]
 
 
 class SwzError(RuntimeError):
@@ -102,6 +109,8 @@ def lib() -> ctypes.CDLL:
         L.swz_gemm_die_plan.argtypes = [i, i, i, ctypes.POINTER(swz_gemm_opts),
                                         ctypes.POINTER(ctypes.c_int32), i, ip, ip, ip]
         linear.declare(L)
+        int8.declare(L)
+        training.declare(L)
         for name in EXPORTS:
             if name != "swz_strerror":
                 getattr(L, name).restype = ctypes.c_int
@@ -485,3 +494,15 @@ from .linear import (SWZ_BLOCK_ROW, SWZ_BLOCK_SQUARE, SWZ_E4M3, SWZ_E5M2, SWZ_F3
                      swz_gemm_fp8, swz_gemm_fp8_opts, swz_linear_fp8,
                      swz_linear_fp8_workspace_size, swz_newton_schulz, swz_newton_schulz_opts,
                      swz_newton_schulz_workspace_size, swz_quantize_fp8)
+# linear layers in 8-bit integers (int8.py)
+from . import int8  # noqa: E402
+from .int8 import (gemm_int8, int8_empty, linear_int8, quantize_int8,  # noqa: E402,F401
+                   swz_gemm_int8, swz_gemm_int8_opts, swz_gemm_int8_workspace_size,
+                   swz_linear_int8, swz_linear_int8_workspace_size, swz_quantize_int8)
+
+# around a linear layer in training (training.py)
+from . import training  # noqa: E402
+from .training import (clip_grad_norm, grad_norm, layer_norm, layer_norm_backward,  # noqa: E402,F401
+                       layer_norm_forward, swz_clip_grad_norm, swz_grad, swz_grad_norm,
+                       swz_grad_norm_workspace_size, swz_layer_norm, swz_layer_norm_backward,
+                       swz_layer_norm_backward_workspace_size)

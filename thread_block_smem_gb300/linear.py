@@ -171,7 +171,7 @@ def _rows(x, what):
     if (m | k) > INT_MAX:
         raise ValueError(f"{what}: more than 2^31 - 1 rows or columns")
     ld, one = x.stride()
-    if one != 1 and k > 1:
+    if one != 1 and k > 1 and m > 0:
         raise ValueError(f"{what}: contiguous rows expected")
     if m <= 1:
         return m, k, k or 1
