@@ -634,8 +634,9 @@ int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void*
  * zero. */
 typedef struct swz_gemm_int8_opts {
   int order, group;     /* tile order as in swz_gemm                            */
-  int tile;             /* 0 automatic; 128: one CTA, 128 x 128 of C; 256: CTA
-                           pair, 256 x 256                                      */
+  int tile;             /* 0 automatic; 64: all rows of C, which are 64 at most
+                           (automatic there), a share of its columns; 128: one CTA, 128 x
+                           128; 256: CTA pair, 256 x 256                        */
   int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share the K
                            of a tile that is not a pair's                       */
   uint32_t debug_flags; /* SWZ_DEBUG_*; 0 in normal use                         */
@@ -651,7 +652,7 @@ typedef struct swz_gemm_int8_opts {
  * fp32, and the product is rounded to fp32 and to C's type.  K up to 131071, so
  * that the sum fits 32 bits; any M, N >= 0 (K = 0 writes zeros).
  * d_workspace: 16-byte aligned device scratch of at least
- * swz_gemm_int8_workspace_size bytes, contents free before and after; calls that
+ * swz_gemm_int8_workspace_size bytes (of the same sizes and tile), contents free before and after; calls that
  * share it must not overlap; NULL when the size is 0.  Errors: SWZ_EINVAL,
  * SWZ_ENOTBIJECTIVE, SWZ_EUNSUPPORTED (unknown tile or split, a split of more
  * parts than blocks of K), SWZ_EARCH, SWZ_ECUDA.
@@ -660,7 +661,7 @@ int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const void* B, in
                   const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,
                   const swz_gemm_int8_opts* opts, void* d_workspace, uint64_t workspace_bytes,
                   void* stream);
-int swz_gemm_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
+int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes);
 
 /*
  * swz_linear_int8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is

@@ -120,6 +120,18 @@ def test_gemm_tiles(swz, tile, split, m, n, k):
     swz.check_status()
 
 
+@pytest.mark.parametrize("split", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1100), (1, 4096, 4096), (8, 1000, 1024), (9, 3, 20000), (16, 10240, 1500),
+                                   (17, 2000, 4100), (33, 6000, 1111), (64, 129, 8192), (64, 50000, 1030),
+                                   (2, 100000, 1200), (30, 90001, 1024)])
+def test_few_rows(swz, m, n, k, split):
+    """Tiles that one or several CTAs share, several of them a CTA, and ragged ones."""
+    a, sa = int8_rows(swz, m, k, 3)
+    b, sb = int8_rows(swz, n, k, 4)
+    assert bits(swz.gemm_int8(a, sa, b, sb, tile=64, split_k=split), exact_c(a, sa, b, sb, torch.bfloat16))
+    swz.check_status()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_gemm_extreme_sums(swz, m):
     """The largest sums: every product 2^14 over the longest K, and all of one sign."""
@@ -234,9 +246,10 @@ def test_no_gradient(swz):
 
 def test_timeout_is_reported(swz):
     """A load that never arrives: the waits run out, the call ends, the status says so."""
-    for kw in (dict(tile=256), dict(tile=128)):
-        a, sa = int8_rows(swz, 300, 4096, 1)
-        b, sb = int8_rows(swz, 300, 4096, 2)
+    for m, n, kw in ((300, 300, dict(tile=256)), (300, 300, dict(tile=128)), (300, 300, dict(tile=128, split_k=4)),
+                     (20, 300, dict()), (20, 90000, dict()), (3, 300, dict(split_k=4))):
+        a, sa = int8_rows(swz, m, 4096, 1)
+        b, sb = int8_rows(swz, n, 4096, 2)
         swz.gemm_int8(a, sa, b, sb, debug_flags=swz.SWZ_DEBUG_SKIP_FIRST_LOAD, timeout_ms=50, **kw)
         with pytest.raises(swz.SwzError):
             swz.check_status()

@@ -27,7 +27,7 @@
 #include <type_traits>
 
 #include "common.h"
-#include "int8.h"
+#include "int8.cuh"
 #include "ops.h"
 #include "pipe.cuh"
 #include "rows.cuh"
@@ -75,20 +75,6 @@ struct Params {
 };
 
 // ---- widening -------------------------------------------------------------------
-// Four bytes to four fp16 numbers of the same values: byte + 128 in the low bits of
-// 1024's fp16 pattern is 1152 + the value.
-__device__ __forceinline__ void widen4(uint32_t b, uint32_t& lo, uint32_t& hi) {
-  b ^= 0x80808080u;
-  const uint32_t bias = 0x64806480u;  // 1152 twice
-  const uint32_t l = __byte_perm(b, 0x64646464u, 0x4140), h = __byte_perm(b, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&l),
-                            *reinterpret_cast<const __half2*>(&bias));
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            *reinterpret_cast<const __half2*>(&bias));
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
 struct WidenArgs {
   const uint8_t* in[2];
   int64_t ld[2];  // bytes
@@ -574,6 +560,10 @@ static void workspace_split(int M, int N, int K, int64_t* ld, uint64_t* a_bytes,
   *total = *a_bytes + uint64_t(N) * uint64_t(*ld) * 2;
 }
 
+static uint64_t timeout_of(const swz_gemm_int8_opts& o) {
+  return uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+}
+
 // C = A B^T of widened operands; the rest is checked.
 static int product(const void* a16, const void* b16, int64_t ld, const float* sa, const float* sb,
                    void* C, int64_t ldc, int c_dtype, int M, int N, int K,
@@ -620,7 +610,7 @@ static int product(const void* a16, const void* b16, int64_t ld, const float* sa
   const uintptr_t bits = reinterpret_cast<uintptr_t>(C) | (M > 1 ? uintptr_t(ldc) * es : 0);
   prm.c_align = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 1;
   prm.debug_flags = o.debug_flags;
-  prm.timeout_ns = uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
+  prm.timeout_ns = timeout_of(o);
   rc = op_status_word(&prm.status);
   if (rc != SWZ_OK) return rc;
   uint64_t programs = sm * sn * cl;
@@ -632,9 +622,13 @@ static int product(const void* a16, const void* b16, int64_t ld, const float* sa
               : launch<false>(ta, tb, prm, uint32_t(programs), s);
 }
 
-static int check_opts(const swz_gemm_int8_opts& o) {
+// the form for few rows of A (which needs no workspace)
+static bool few_rows(int M, int tile) { return M <= kMaxRows && tile != 128 && tile != 256; }
+
+static int check_opts(const swz_gemm_int8_opts& o, int M) {
   if (!order_is_valid(o.order) || (order_uses_group(o.order) && o.group < 1)) return SWZ_EINVAL;
-  if (o.tile != 0 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
+  if (o.tile != 0 && o.tile != 64 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
+  if (o.tile == 64 && M > kMaxRows) return SWZ_EUNSUPPORTED;
   if (o.split_k != 0 && o.split_k != 1 && o.split_k != 2 && o.split_k != 4 && o.split_k != 8)
     return SWZ_EUNSUPPORTED;
   if (o.tile == 256 && o.split_k > 1) return SWZ_EUNSUPPORTED;
@@ -664,10 +658,10 @@ static bool float_type(int d) { return d == SWZ_F16 || d == SWZ_BF16 || d == SWZ
 using namespace swz;
 using namespace swz::i8;
 
-extern "C" int swz_gemm_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes) {
+extern "C" int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
-  if (M == 0 || N == 0 || K == 0) return SWZ_OK;
+  if (M == 0 || N == 0 || K == 0 || few_rows(M, tile)) return SWZ_OK;
   int64_t ld;
   uint64_t a_bytes;
   workspace_split(M, N, K, &ld, &a_bytes, h_bytes);
@@ -683,7 +677,7 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   o.group = 8;
   if (opts) o = *opts;
   if (M < 0 || N < 0 || K < 0 || K > kMaxK || !float_type(c_dtype)) return SWZ_EINVAL;
-  int rc = check_opts(o);
+  int rc = check_opts(o, M);
   if (rc != SWZ_OK) return rc;
   if (M == 0 || N == 0) return SWZ_OK;
   if (!result_ok(C, ldc, c_dtype, M, N)) return SWZ_EINVAL;
@@ -692,13 +686,20 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   uint64_t a_bytes, total;
   workspace_split(M, N, K, &ld, &a_bytes, &total);
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
-  if (K > 0 && (!ws || !aligned16(ws) || workspace_bytes < total)) return SWZ_EINVAL;
+  if (K > 0 && !few_rows(M, o.tile) && (!ws || !aligned16(ws) || workspace_bytes < total))
+    return SWZ_EINVAL;
   DeviceInfo dev{};
   rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ldc = M > 1 ? ldc : N;
   if (K == 0) return zero_result(C, ldc, c_dtype, M, N, s);
+  if (o.tile == 0 && o.split_k == 0 && M <= kTokens)
+    return gemm_int8_tokens(A, lda, sa, nullptr, 0, 0, B, ldb, sb, C, ldc, c_dtype, M, N, K,
+                            dev.num_sms, s);
+  if (few_rows(M, o.tile))
+    return gemm_int8_rows(A, lda, sa, B, ldb, sb, C, ldc, c_dtype, M, N, K, o.split_k,
+                          o.debug_flags, timeout_of(o), false, dev.num_sms, s);
   WidenArgs w{};
   w.in[0] = static_cast<const uint8_t*>(A);
   w.in[1] = static_cast<const uint8_t*>(B);
@@ -716,17 +717,22 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   return product(ws, ws + a_bytes, ld, sa, sb, C, ldc, c_dtype, M, N, K, o, dev, s);
 }
 
-// workspace of the layer: the scales of x, then x and W as the product has them
+// workspace of the layer: the scales of x, then x as bytes (few rows), or x and W as
+// fp16
 static uint64_t linear_scales_bytes(int M) { return (uint64_t(M) * 4 + 255) & ~uint64_t(255); }
+static int64_t bytes_ld(int K) { return (int64_t(K) + 15) / 16 * 16; }
+static uint64_t linear_bytes(int M, int N, int K) {
+  int64_t ld;
+  uint64_t a_bytes, total;
+  workspace_split(M, N, K, &ld, &a_bytes, &total);
+  return linear_scales_bytes(M) + (M <= kMaxRows ? uint64_t(M) * uint64_t(bytes_ld(K)) : total);
+}
 
 extern "C" int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
   if (M == 0 || N == 0 || K == 0) return SWZ_OK;
-  int64_t ld;
-  uint64_t a_bytes;
-  workspace_split(M, N, K, &ld, &a_bytes, h_bytes);
-  *h_bytes += linear_scales_bytes(M);
+  *h_bytes = linear_bytes(M, N, K);
   return SWZ_OK;
 }
 
@@ -741,20 +747,35 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   if (K > 0 && (!x || reinterpret_cast<uintptr_t>(x) % es != 0 || (M > 1 && ldx < K) ||
                 !int8_rows_ok(W, ldw, sw, K)))
     return SWZ_EINVAL;
-  int64_t ld;
-  uint64_t a_bytes, total;
-  workspace_split(M, N, K, &ld, &a_bytes, &total);
-  const uint64_t sbytes = linear_scales_bytes(M);
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
-  if (K > 0 && (!ws || !aligned16(ws) || workspace_bytes < total + sbytes)) return SWZ_EINVAL;
+  if (K > 0 && (!ws || !aligned16(ws) || workspace_bytes < linear_bytes(M, N, K)))
+    return SWZ_EINVAL;
   DeviceInfo dev{};
   int rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ldy = M > 1 ? ldy : N;
   if (K == 0) return zero_result(y, ldy, y_dtype, M, N, s);
+  if (M <= kTokens && tokens_fused(M, K))
+    return gemm_int8_tokens(nullptr, 0, nullptr, x, dtype, ldx, W, ldw, sw, y, ldy, y_dtype, M, N,
+                            K, dev.num_sms, s);
   float* sx = reinterpret_cast<float*>(ws);
-  ws += sbytes;
+  ws += linear_scales_bytes(M);
+  swz_gemm_int8_opts o = {};
+  o.order = SWZ_SERPENTINE;
+  o.group = 8;
+  if (M <= kMaxRows) {
+    rc = quantize_rows(x, dtype, ldx, M, K, ws, bytes_ld(K), sx, false, s);
+    if (rc != SWZ_OK) return rc;
+    if (M <= kTokens)
+      return gemm_int8_tokens(ws, bytes_ld(K), sx, nullptr, 0, 0, W, ldw, sw, y, ldy, y_dtype, M,
+                              N, K, dev.num_sms, s);
+    return gemm_int8_rows(ws, bytes_ld(K), sx, W, ldw, sw, y, ldy, y_dtype, M, N, K, 0, 0,
+                          timeout_of(o), true, dev.num_sms, s);
+  }
+  int64_t ld;
+  uint64_t a_bytes, total;
+  workspace_split(M, N, K, &ld, &a_bytes, &total);
   rc = quantize_rows(x, dtype, ldx, M, K, ws, ld * 2, sx, true, s);
   if (rc != SWZ_OK) return rc;
   WidenArgs w{};
@@ -767,8 +788,5 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   w.pieces = uint32_t(ceil_div(uint64_t(K), 16));
   rc = launch_widen(w, dev.num_sms, s);
   if (rc != SWZ_OK) return rc;
-  swz_gemm_int8_opts o = {};
-  o.order = SWZ_SERPENTINE;
-  o.group = 8;
   return product(ws, ws + a_bytes, ld, sx, sw, y, ldy, y_dtype, M, N, K, o, dev, s);
 }

@@ -150,7 +150,7 @@ extern "C" int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void*
   const int rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
   FwdArgs a{};
-  a.x = span(x, dtype, ldx, M, N);
+  a.x = rows::span_of(x, dtype, ldx, M, N);
   a.M = M;
   a.N = N;
   a.w = vec(weight, w_dtype);

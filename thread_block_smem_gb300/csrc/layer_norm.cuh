@@ -51,17 +51,6 @@ __device__ __forceinline__ void load_vec(const Vec& v, int64_t k, int64_t n, flo
 inline bool float_type(int d) { return d == SWZ_F16 || d == SWZ_BF16 || d == SWZ_F32; }
 inline int64_t size_of(int d) { return d == SWZ_F32 ? 4 : 2; }
 
-// M rows of N values `ld` elements apart, as the kernels read them.
-inline rows::Span span(const void* x, int dtype, int64_t ld, int M, int N) {
-  const int64_t es = size_of(dtype);
-  rows::Span s{};
-  s.base = static_cast<const uint8_t*>(x);
-  s.ld = (M > 1 ? ld : int64_t(N)) * es;
-  s.end = s.base + (int64_t(M) - 1) * s.ld + int64_t(N) * es;
-  s.wide = aligned16(x) && s.ld % 16 == 0;
-  return s;
-}
-
 inline Vec vec(const void* p, int dtype) {
   Vec v{};
   v.p = static_cast<const uint8_t*>(p);

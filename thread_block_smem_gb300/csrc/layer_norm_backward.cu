@@ -319,8 +319,8 @@ extern "C" int swz_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
     return SWZ_OK;
   }
   BwdArgs a{};
-  a.x = span(x, dtype, ldx, M, N);
-  a.dy = span(dy, dy_dtype, lddy, M, N);
+  a.x = rows::span_of(x, dtype, ldx, M, N);
+  a.dy = rows::span_of(dy, dy_dtype, lddy, M, N);
   a.M = M;
   a.N = N;
   a.w = vec(weight, w_dtype);

@@ -14,7 +14,7 @@
 #include <type_traits>
 
 #include "common.h"
-#include "int8.h"
+#include "int8.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -28,42 +28,6 @@ struct QuantArgs {
   int64_t ldq;  // bytes
   float* s;
 };
-
-template <typename T>
-__device__ __forceinline__ uint32_t chunk_max(const uint32_t* w) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < T::kWords; ++j) m = f8::max_packed<T>(m, w[j] & T::kAbs);
-  if constexpr (T::kBytes == 2) m = max(m & 0xFFFFu, m >> 16);
-  return m;
-}
-
-// eight values to q at p: bytes, or fp16 numbers of the same values
-template <typename T, bool HALF>
-__device__ __forceinline__ void store_q(uint8_t* p, const uint32_t* w, float r, bool bad) {
-  constexpr float kMagic = 12582912.0f;  // 1.5 2^23
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    b[i] = bad ? __float_as_uint(kMagic) : __float_as_uint(__fmaf_rn(T::value(w, i), r, kMagic));
-  if constexpr (HALF) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = __floats2half2_rn(__uint_as_float(b[2 * i]) - kMagic,
-                                          __uint_as_float(b[2 * i + 1]) - kMagic);
-      o[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      o[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
-                         __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
-    *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
-  }
-}
 
 // TPR threads a row (32: each warp a row of its own), NC chunks a thread; NC = 0:
 // any length, in a loop, the row read again for the rounding.
@@ -103,11 +67,9 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) quantize_int8_kernel(co
 #pragma unroll
     for (int i = 1; i < TPR / 32; ++i) m = max(m, part[i]);
   }
-  const uint32_t amax = T::max_bits(m);
-  const bool bad = amax >= 0x7F800000u;
   float r, scale;
-  f8::scale_of(amax, 127.0f, r, scale);
-  if (t == 0) p.s[row] = bad ? __uint_as_float(0x7FC00000u) : scale;
+  const bool bad = row_scale(T::max_bits(m), r, scale);
+  if (t == 0) p.s[row] = scale;
   uint8_t* q = p.q + row * p.ldq;
   if constexpr (NC > 0) {
 #pragma unroll
@@ -150,12 +112,8 @@ static int dispatch(const QuantArgs& a, bool half, cudaStream_t s) {
 
 int quantize_rows(const void* x, int dtype, int64_t ldx, int M, int K, void* q, int64_t ldq,
                   float* scales, bool half, cudaStream_t s) {
-  const int64_t es = dtype == SWZ_F32 ? 4 : 2;
   QuantArgs a{};
-  a.x.base = static_cast<const uint8_t*>(x);
-  a.x.ld = (M > 1 ? ldx : int64_t(K)) * es;
-  a.x.end = a.x.base + (int64_t(M) - 1) * a.x.ld + int64_t(K) * es;
-  a.x.wide = aligned16(x) && a.x.ld % 16 == 0;
+  a.x = rows::span_of(x, dtype, ldx, M, K);
   a.M = M;
   a.K = K;
   a.q = static_cast<uint8_t*>(q);

@@ -31,6 +31,17 @@ struct Span {
   int wide;    // every row starts on 16 bytes
 };
 
+// M rows of N values of a type (SWZ_F16, ...), `ld` elements apart.
+inline Span span_of(const void* x, int dtype, int64_t ld, int M, int N) {
+  const int64_t es = dtype == SWZ_F32 ? 4 : 2;
+  Span s{};
+  s.base = static_cast<const uint8_t*>(x);
+  s.ld = (M > 1 ? ld : int64_t(N)) * es;
+  s.end = s.base + (int64_t(M) - 1) * s.ld + int64_t(N) * es;
+  s.wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && s.ld % 16 == 0;
+  return s;
+}
+
 // The 16-byte piece at byte `s` (1 .. 15, the same for all its words) of the words
 // e[0..7].
 __device__ __forceinline__ void shift_words(const uint32_t (&e)[8], uint32_t s, uint32_t* o) {

@@ -32,7 +32,7 @@ def declare(L):
     L.swz_quantize_int8.argtypes = [vp, i, i64, i, i, vp, i64, vp, vp]
     L.swz_gemm_int8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i, i, i, i,
                                 ctypes.POINTER(swz_gemm_int8_opts), vp, u64, vp]
-    L.swz_gemm_int8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
+    L.swz_gemm_int8_workspace_size.argtypes = [i, i, i, i, ctypes.POINTER(u64)]
     L.swz_linear_int8.argtypes = [vp, i, i64, vp, i64, vp, vp, i64, i, i, i, i, vp, u64, vp]
     L.swz_linear_int8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
 
@@ -61,16 +61,16 @@ def swz_linear_int8(x, dtype, ldx, W, ldw, sw, y, ldy, y_dtype, M, N, K, workspa
                                       workspace, workspace_bytes, stream)
 
 
-def _size(fn, M, N, K):
-    if not _lin._ints(M, N, K):
+def _size(fn, *sizes):
+    if not _lin._ints(*sizes):
         return _swz.SWZ_EINVAL, 0
     b = ctypes.c_uint64(0)
-    rc = fn(M, N, K, ctypes.byref(b))
+    rc = fn(*sizes, ctypes.byref(b))
     return rc, b.value
 
 
-def swz_gemm_int8_workspace_size(M, N, K):
-    return _size(_swz.lib().swz_gemm_int8_workspace_size, M, N, K)
+def swz_gemm_int8_workspace_size(M, N, K, tile=0):
+    return _size(_swz.lib().swz_gemm_int8_workspace_size, M, N, K, tile)
 
 
 def swz_linear_int8_workspace_size(M, N, K):
@@ -152,7 +152,7 @@ def gemm_int8(a, sa, b, sb, *, out=None, out_dtype=None, order="serpentine", gro
         _lin._keep(stream, a, sa, b, sb, out)
     opts = swz_gemm_int8_opts(order, group, tile, split_k, debug_flags, timeout_ms)
     need = _lin._u64()
-    rc = _lin._L.swz_gemm_int8_workspace_size(M, N, K, need)
+    rc = _lin._L.swz_gemm_int8_workspace_size(M, N, K, tile, need)
     if rc == 0:
         need = need.value
         ws = _lin._empty(need, torch.uint8, a, stream) if need else None
