@@ -634,8 +634,9 @@ int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void*
  * zero. */
 typedef struct swz_gemm_int8_opts {
   int order, group;     /* tile order as in swz_gemm                            */
-  int tile;             /* 0 automatic; 64: all rows of C, which are 64 at most
-                           (automatic there), a share of its columns; 128: one CTA, 128 x
+  int tile;             /* 0 automatic; 32: up to 32 rows of C, all of them in every
+                           CTA; 64: 128 columns of C and up to 256 of its rows, B
+                           widened on its way to the tensor core; 128: one CTA, 128 x
                            128; 256: CTA pair, 256 x 256                        */
   int split_k;          /* 0 automatic; 1, 2, 4 or 8 CTAs (a cluster) share the K
                            of a tile that is not a pair's                       */
@@ -655,7 +656,8 @@ typedef struct swz_gemm_int8_opts {
  * swz_gemm_int8_workspace_size bytes (of the same sizes and tile), contents free before and after; calls that
  * share it must not overlap; NULL when the size is 0.  Errors: SWZ_EINVAL,
  * SWZ_ENOTBIJECTIVE, SWZ_EUNSUPPORTED (unknown tile or split, a split of more
- * parts than blocks of K), SWZ_EARCH, SWZ_ECUDA.
+ * parts than blocks of K or of one or two rows, tile 32 with more rows, tile 64
+ * where K is longer than its accumulators have room for), SWZ_EARCH, SWZ_ECUDA.
  */
 int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const void* B, int64_t ldb,
                   const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,

@@ -128,7 +128,29 @@ def test_few_rows(swz, m, n, k, split):
     """Tiles that one or several CTAs share, several of them a CTA, and ragged ones."""
     a, sa = int8_rows(swz, m, k, 3)
     b, sb = int8_rows(swz, n, k, 4)
-    assert bits(swz.gemm_int8(a, sa, b, sb, tile=64, split_k=split), exact_c(a, sa, b, sb, torch.bfloat16))
+    want = exact_c(a, sa, b, sb, torch.bfloat16)
+    # of tile 64 the sums of each 1024 of K have columns of their own for each row (whole
+    # sixteens of them), 256 in all; a part of K has one block of 128 at least
+    rows, blocks, parts = (m + 15) // 16 * 16, (k + 127) // 128, split or 8
+    for tile, refused in ((32, m > 32 or split > blocks),
+                          (64, -(-(-(-blocks // parts)) // 8) * rows > 256 or split > blocks)):
+        if refused:
+            with pytest.raises(swz.SwzError):
+                swz.gemm_int8(a, sa, b, sb, tile=tile, split_k=split)
+        else:
+            assert bits(swz.gemm_int8(a, sa, b, sb, tile=tile, split_k=split), want), tile
+    assert bits(swz.gemm_int8(a, sa, b, sb), want)
+    swz.check_status()
+
+
+@pytest.mark.parametrize("m", [65, 100, 128, 129, 250, 256, 257, 300, 600])
+@pytest.mark.parametrize("n,k", [(130, 1024), (1000, 2500), (4096, 300)])
+def test_batches(swz, m, n, k):
+    a, sa = int8_rows(swz, m, k, 5)
+    b, sb = int8_rows(swz, n, k, 6)
+    want = exact_c(a, sa, b, sb, torch.float16)
+    for kw in (dict(), dict(tile=64), dict(tile=64, split_k=4 if k > 1000 else 2), dict(tile=128), dict(tile=256)):
+        assert bits(swz.gemm_int8(a, sa, b, sb, out_dtype=torch.float16, **kw), want), kw
     swz.check_status()
 
 
@@ -247,7 +269,7 @@ def test_no_gradient(swz):
 def test_timeout_is_reported(swz):
     """A load that never arrives: the waits run out, the call ends, the status says so."""
     for m, n, kw in ((300, 300, dict(tile=256)), (300, 300, dict(tile=128)), (300, 300, dict(tile=128, split_k=4)),
-                     (20, 300, dict()), (20, 90000, dict()), (3, 300, dict(split_k=4))):
+                     (20, 300, dict()), (20, 90000, dict()), (3, 300, dict(tile=64, split_k=4)), (3, 300, dict(tile=32, split_k=4)), (3, 90000, dict(tile=32)), (200, 300, dict(tile=64))):
         a, sa = int8_rows(swz, m, 4096, 1)
         b, sb = int8_rows(swz, n, 4096, 2)
         swz.gemm_int8(a, sa, b, sb, debug_flags=swz.SWZ_DEBUG_SKIP_FIRST_LOAD, timeout_ms=50, **kw)

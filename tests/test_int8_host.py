@@ -55,7 +55,7 @@ def test_gemm_checks(swz):
              {13: 0}, {13: 65537}, {14: 16}, {9: 2 ** 32 + 100}, {11: 2 ** 32 + 64}), E)
     opts = lambda **kw: swz.swz_gemm_int8_opts(**dict(dict(order=5, group=8), **kw))  # noqa: E731
     refused(swz.swz_gemm_int8, good, ({12: opts(order=9)}, {12: opts(order=2, group=0)}), E)
-    refused(swz.swz_gemm_int8, good, ({12: opts(tile=64)}, {12: opts(split_k=3)}, {12: opts(tile=256, split_k=2)}), U)
+    refused(swz.swz_gemm_int8, good, ({12: opts(tile=16)}, {12: opts(split_k=3)}, {12: opts(tile=256, split_k=2)}), U)
     for at in (9, 10):
         a = list(good)
         a[at] = 0

@@ -23,7 +23,8 @@ SOURCES = ["capi.cu", "transpose.cu", "gemm.cu", "l2_model.cpp", "noalloc.cu", "
            "host_pipeline.cu", "gemm_mma_sync.cu", "tc_rate.cu", "ops.cu", "quantize.cu",
            "gemm_fp8.cu", "gemm_fp8_rows.cu", "linear_fp8.cu", "newton_schulz.cu",
            "newton_schulz_small.cu", "quantize_int8.cu", "gemm_int8.cu",
-           "gemm_int8_rows.cu", "gemm_int8_tokens.cu", "layer_norm.cu",
+           "gemm_int8_tokens.cu", "gemm_int8_rows.cu",
+           "gemm_int8_batch.cu", "layer_norm.cu",
            "layer_norm_backward.cu", "grad_norm.cu"]
 HEADERS = ["common.h", "ptx.cuh", "tile_order.cuh", "ops.h", "pipe.cuh", "f8.cuh",
            "newton_schulz.cuh", "rows.cuh", "int8.cuh", "layer_norm.cuh"]

@@ -553,13 +553,9 @@ static Choice choose(uint64_t M, uint64_t N, uint64_t K, uint32_t sms) {
   return c;
 }
 
-// workspace: A, then B, as fp16 in rows of whole 128-byte lines
-static void workspace_split(int M, int N, int K, int64_t* ld, uint64_t* a_bytes, uint64_t* total) {
-  *ld = (int64_t(K) + 63) / 64 * 64;
-  *a_bytes = uint64_t(M) * uint64_t(*ld) * 2;
-  *total = *a_bytes + uint64_t(N) * uint64_t(*ld) * 2;
-}
-
+// workspace: A, then (wide form) B, as fp16 in rows of whole 128-byte lines
+static int64_t wide_ld(int K) { return (int64_t(K) + 63) / 64 * 64; }
+static uint64_t a_bytes_of(int M, int K) { return uint64_t(M) * uint64_t(wide_ld(K)) * 2; }
 static uint64_t timeout_of(const swz_gemm_int8_opts& o) {
   return uint64_t(o.timeout_ms ? o.timeout_ms : 2000u) * 1000000ull;
 }
@@ -622,13 +618,25 @@ static int product(const void* a16, const void* b16, int64_t ld, const float* sa
               : launch<false>(ta, tb, prm, uint32_t(programs), s);
 }
 
-// the form for few rows of A (which needs no workspace)
-static bool few_rows(int M, int tile) { return M <= kMaxRows && tile != 128 && tile != 256; }
+// How a product is made: by dp4a (few tokens), with B widened on its way to the tensor
+// core (batches), or with both operands widened first.
+enum Form { kTokenForm, kRingForm, kBatchForm, kWideForm };
+static Form form_of(int M, int N, int K, int tile) {
+  if (tile == 128 || tile == 256) return kWideForm;
+  // (the tokens' form reads whole pieces of 16 bytes of a row of B)
+  if (tile == 0 && M <= kTokens && K >= 16) return kTokenForm;
+  if (tile == 32 || (tile == 0 && M <= kRingRows)) return kRingForm;
+  if (tile == 64 || (M <= kBatchRows && batch_plan(M, N, K, 0, 1).split)) return kBatchForm;
+  return kWideForm;
+}
 
-static int check_opts(const swz_gemm_int8_opts& o, int M) {
+static uint64_t gemm_bytes(Form f, int M, int N, int K) {
+  return f == kTokenForm || f == kRingForm ? 0 : a_bytes_of(M, K) + (f == kWideForm ? a_bytes_of(N, K) : 0);
+}
+
+static int check_opts(const swz_gemm_int8_opts& o) {
   if (!order_is_valid(o.order) || (order_uses_group(o.order) && o.group < 1)) return SWZ_EINVAL;
-  if (o.tile != 0 && o.tile != 64 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
-  if (o.tile == 64 && M > kMaxRows) return SWZ_EUNSUPPORTED;
+  if (o.tile != 0 && o.tile != 32 && o.tile != 64 && o.tile != 128 && o.tile != 256) return SWZ_EUNSUPPORTED;
   if (o.split_k != 0 && o.split_k != 1 && o.split_k != 2 && o.split_k != 4 && o.split_k != 8)
     return SWZ_EUNSUPPORTED;
   if (o.tile == 256 && o.split_k > 1) return SWZ_EUNSUPPORTED;
@@ -658,13 +666,29 @@ static bool float_type(int d) { return d == SWZ_F16 || d == SWZ_BF16 || d == SWZ
 using namespace swz;
 using namespace swz::i8;
 
+// A and B (either may be NULL) to fp16 in the workspace.
+static int widen(const void* A, int64_t lda, int M, const void* B, int64_t ldb, int N, int K,
+                 uint8_t* ws, int num_sms, cudaStream_t s) {
+  WidenArgs w{};
+  w.in[0] = static_cast<const uint8_t*>(A);
+  w.in[1] = static_cast<const uint8_t*>(B);
+  w.ld[0] = lda;
+  w.ld[1] = ldb;
+  w.out[0] = ws;
+  w.out[1] = ws + a_bytes_of(M, K);
+  w.ldo = wide_ld(K) * 2;
+  w.rows[0] = A ? M : 0;
+  w.rows[1] = B ? N : 0;
+  w.K = K;
+  w.pieces = uint32_t(ceil_div(uint64_t(K), 16));
+  return launch_widen(w, num_sms, s);
+}
+
 extern "C" int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
-  if (M == 0 || N == 0 || K == 0 || few_rows(M, tile)) return SWZ_OK;
-  int64_t ld;
-  uint64_t a_bytes;
-  workspace_split(M, N, K, &ld, &a_bytes, h_bytes);
+  if (M == 0 || N == 0 || K == 0) return SWZ_OK;
+  *h_bytes = gemm_bytes(form_of(M, N, K, tile), M, N, K);
   return SWZ_OK;
 }
 
@@ -677,62 +701,58 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   o.group = 8;
   if (opts) o = *opts;
   if (M < 0 || N < 0 || K < 0 || K > kMaxK || !float_type(c_dtype)) return SWZ_EINVAL;
-  int rc = check_opts(o, M);
+  int rc = check_opts(o);
   if (rc != SWZ_OK) return rc;
   if (M == 0 || N == 0) return SWZ_OK;
   if (!result_ok(C, ldc, c_dtype, M, N)) return SWZ_EINVAL;
   if (K > 0 && (!int8_rows_ok(A, lda, sa, K) || !int8_rows_ok(B, ldb, sb, K))) return SWZ_EINVAL;
-  int64_t ld;
-  uint64_t a_bytes, total;
-  workspace_split(M, N, K, &ld, &a_bytes, &total);
+  const Form f = form_of(M, N, K, o.tile);
+  if ((f == kTokenForm && o.split_k > 1) || (f == kRingForm && M > kRingRows))
+    return SWZ_EUNSUPPORTED;
+  const uint64_t need = K > 0 ? gemm_bytes(f, M, N, K) : 0;
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
-  if (K > 0 && !few_rows(M, o.tile) && (!ws || !aligned16(ws) || workspace_bytes < total))
-    return SWZ_EINVAL;
+  if (need && (!ws || !aligned16(ws) || workspace_bytes < need)) return SWZ_EINVAL;
   DeviceInfo dev{};
   rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ldc = M > 1 ? ldc : N;
   if (K == 0) return zero_result(C, ldc, c_dtype, M, N, s);
-  if (o.tile == 0 && o.split_k == 0 && M <= kTokens)
+  if (f == kTokenForm)
     return gemm_int8_tokens(A, lda, sa, nullptr, 0, 0, B, ldb, sb, C, ldc, c_dtype, M, N, K,
                             dev.num_sms, s);
-  if (few_rows(M, o.tile))
+  if (f == kRingForm)
     return gemm_int8_rows(A, lda, sa, B, ldb, sb, C, ldc, c_dtype, M, N, K, o.split_k,
                           o.debug_flags, timeout_of(o), false, dev.num_sms, s);
-  WidenArgs w{};
-  w.in[0] = static_cast<const uint8_t*>(A);
-  w.in[1] = static_cast<const uint8_t*>(B);
-  w.ld[0] = lda;
-  w.ld[1] = ldb;
-  w.out[0] = ws;
-  w.out[1] = ws + a_bytes;
-  w.ldo = ld * 2;
-  w.rows[0] = M;
-  w.rows[1] = N;
-  w.K = K;
-  w.pieces = uint32_t(ceil_div(uint64_t(K), 16));
-  rc = launch_widen(w, dev.num_sms, s);
+  BatchPlan b{};
+  if (f == kBatchForm) {
+    b = batch_plan(M, N, K, o.split_k, dev.num_sms);
+    if (!b.split) return SWZ_EUNSUPPORTED;
+  }
+  rc = widen(A, lda, M, f == kWideForm ? B : nullptr, ldb, N, K, ws, dev.num_sms, s);
   if (rc != SWZ_OK) return rc;
-  return product(ws, ws + a_bytes, ld, sa, sb, C, ldc, c_dtype, M, N, K, o, dev, s);
+  if (f == kBatchForm)
+    return gemm_int8_batch(ws, wide_ld(K), sa, B, ldb, sb, C, ldc, c_dtype, M, N, K, b,
+                           o.debug_flags, timeout_of(o), s);
+  return product(ws, ws + a_bytes_of(M, K), wide_ld(K), sa, sb, C, ldc, c_dtype, M, N, K, o, dev,
+                 s);
 }
 
-// workspace of the layer: the scales of x, then x as bytes (few rows), or x and W as
-// fp16
+// workspace of the layer: the scales of x, then x as bytes (few tokens too long to be
+// quantised by every CTA) or what the product has
 static uint64_t linear_scales_bytes(int M) { return (uint64_t(M) * 4 + 255) & ~uint64_t(255); }
 static int64_t bytes_ld(int K) { return (int64_t(K) + 15) / 16 * 16; }
-static uint64_t linear_bytes(int M, int N, int K) {
-  int64_t ld;
-  uint64_t a_bytes, total;
-  workspace_split(M, N, K, &ld, &a_bytes, &total);
-  return linear_scales_bytes(M) + (M <= kMaxRows ? uint64_t(M) * uint64_t(bytes_ld(K)) : total);
+static uint64_t linear_bytes(Form f, int M, int N, int K) {
+  if (f == kTokenForm || f == kRingForm)
+    return f == kTokenForm && tokens_fused(M, K) ? 0 : linear_scales_bytes(M) + uint64_t(M) * uint64_t(bytes_ld(K));
+  return linear_scales_bytes(M) + gemm_bytes(f, M, N, K);
 }
 
 extern "C" int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
   if (M == 0 || N == 0 || K == 0) return SWZ_OK;
-  *h_bytes = linear_bytes(M, N, K);
+  *h_bytes = linear_bytes(form_of(M, N, K, 0), M, N, K);
   return SWZ_OK;
 }
 
@@ -747,16 +767,17 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   if (K > 0 && (!x || reinterpret_cast<uintptr_t>(x) % es != 0 || (M > 1 && ldx < K) ||
                 !int8_rows_ok(W, ldw, sw, K)))
     return SWZ_EINVAL;
+  const Form f = form_of(M, N, K, 0);
+  const uint64_t need = K > 0 ? linear_bytes(f, M, N, K) : 0;
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
-  if (K > 0 && (!ws || !aligned16(ws) || workspace_bytes < linear_bytes(M, N, K)))
-    return SWZ_EINVAL;
+  if (need && (!ws || !aligned16(ws) || workspace_bytes < need)) return SWZ_EINVAL;
   DeviceInfo dev{};
   int rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ldy = M > 1 ? ldy : N;
   if (K == 0) return zero_result(y, ldy, y_dtype, M, N, s);
-  if (M <= kTokens && tokens_fused(M, K))
+  if (f == kTokenForm && tokens_fused(M, K))
     return gemm_int8_tokens(nullptr, 0, nullptr, x, dtype, ldx, W, ldw, sw, y, ldy, y_dtype, M, N,
                             K, dev.num_sms, s);
   float* sx = reinterpret_cast<float*>(ws);
@@ -764,29 +785,22 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   swz_gemm_int8_opts o = {};
   o.order = SWZ_SERPENTINE;
   o.group = 8;
-  if (M <= kMaxRows) {
+  if (f == kTokenForm || f == kRingForm) {
     rc = quantize_rows(x, dtype, ldx, M, K, ws, bytes_ld(K), sx, false, s);
     if (rc != SWZ_OK) return rc;
-    if (M <= kTokens)
-      return gemm_int8_tokens(ws, bytes_ld(K), sx, nullptr, 0, 0, W, ldw, sw, y, ldy, y_dtype, M,
-                              N, K, dev.num_sms, s);
-    return gemm_int8_rows(ws, bytes_ld(K), sx, W, ldw, sw, y, ldy, y_dtype, M, N, K, 0, 0,
-                          timeout_of(o), true, dev.num_sms, s);
+    if (f == kRingForm)
+      return gemm_int8_rows(ws, bytes_ld(K), sx, W, ldw, sw, y, ldy, y_dtype, M, N, K, 0, 0,
+                            timeout_of(o), true, dev.num_sms, s);
+    return gemm_int8_tokens(ws, bytes_ld(K), sx, nullptr, 0, 0, W, ldw, sw, y, ldy, y_dtype, M, N,
+                            K, dev.num_sms, s);
   }
-  int64_t ld;
-  uint64_t a_bytes, total;
-  workspace_split(M, N, K, &ld, &a_bytes, &total);
-  rc = quantize_rows(x, dtype, ldx, M, K, ws, ld * 2, sx, true, s);
+  rc = quantize_rows(x, dtype, ldx, M, K, ws, wide_ld(K) * 2, sx, true, s);
   if (rc != SWZ_OK) return rc;
-  WidenArgs w{};
-  w.in[1] = static_cast<const uint8_t*>(W);
-  w.ld[1] = ldw;
-  w.out[1] = ws + a_bytes;
-  w.ldo = ld * 2;
-  w.rows[1] = N;
-  w.K = K;
-  w.pieces = uint32_t(ceil_div(uint64_t(K), 16));
-  rc = launch_widen(w, dev.num_sms, s);
+  if (f == kBatchForm)
+    return gemm_int8_batch(ws, wide_ld(K), sx, W, ldw, sw, y, ldy, y_dtype, M, N, K,
+                           batch_plan(M, N, K, 0, dev.num_sms), 0, timeout_of(o), s);
+  rc = widen(nullptr, 0, M, W, ldw, N, K, ws, dev.num_sms, s);
   if (rc != SWZ_OK) return rc;
-  return product(ws, ws + a_bytes, ld, sx, sw, y, ldy, y_dtype, M, N, K, o, dev, s);
+  return product(ws, ws + a_bytes_of(M, K), wide_ld(K), sx, sw, y, ldy, y_dtype, M, N, K, o, dev,
+                 s);
 }

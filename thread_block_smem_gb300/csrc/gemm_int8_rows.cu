@@ -1,4 +1,4 @@
-// gemm_int8_rows.cu -- swz_gemm_int8 with few rows of A (up to 64: decoding), the
+// gemm_int8_rows.cu -- swz_gemm_int8 with few rows of A (up to 32: decoding), the
 // same exact sums taken as C^T = B * A^T straight from the bytes of B.
 //
 // Bound: reading B once, N * K bytes.  One CTA an SM; each takes R rows of B (any
@@ -22,6 +22,12 @@
 //   * When the kernel before in the stream is the quantiser of A, launched by the
 //     same call, B's first stages are loaded while it still runs: it lets this
 //     kernel start only after everything before it has completed.
+//
+// Measured, in a stream of them, B from memory: 4 rows of 4096 x 4096 5.9 us, 13 rows
+// 6.9, 32 rows 9.2 (12.0 in gemm_int8_batch.cu's form); of 10240 x 4096 10.6, 13.4 and
+// 19.2 (22.5); of 8192 x 8192 14.2, 16.5 and 22.5 (23.5).  What grows with the rows of A
+// is the arithmetic: with every product but the loads left out 13 rows of 10240 x 4096
+// took 10.7 us.  64 rows took 17, 32 and 43 us against 13, 25 and 26.
 #include <mutex>
 
 #include "common.h"
@@ -37,7 +43,7 @@ namespace i8 {
 // warps.
 template <int NT>
 struct RowsCfg {
-  static constexpr int WARPS = NT <= 2 ? 20 : NT == 4 ? 14 : 10;  // that multiply, at most
+  static constexpr int WARPS = NT <= 2 ? 20 : 14;  // that multiply, at most
   static constexpr int THREADS = (WARPS + 1) * 32;
   static constexpr int MAX_R = 16 * WARPS < 256 ? 16 * WARPS : 256;
   static constexpr int A_BYTES = NT * 8 * 128;
@@ -77,6 +83,8 @@ __device__ __forceinline__ void load_widened(uint32_t addr, uint32_t (&h)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) widen4(w[i], h[2 * i], h[2 * i + 1]);
 }
+
+__device__ __forceinline__ uint32_t div_up_dev(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
 template <int NT>
 __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
   const uint32_t at = g * 128 + (((2 * c + half) ^ g) << 4);
   const int es = p.c_dtype == SWZ_F32 ? 4 : 2;
   const uint32_t threads = warps * 32;
-  uint32_t stage = 0, phase = 0, turn = 0;  // of this warp's next block; blocks until then
+  uint32_t stage = group, phase = 0;  // of this warp's next block
   for (uint32_t tile = first_tile; tile < p.tiles; tile += tile_step) {
     float acc[2][NT][4];
     int32_t tot[2][NT][4];
@@ -208,11 +216,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
     };
     uint32_t in_chunk = 0;
 #pragma unroll 1
-    for (uint32_t kb = kb0; kb < kb1 && !aborted; ++kb, ++turn) {
-      if (turn % p.groups != group) {
-        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-        continue;
-      }
+    for (uint32_t kb = kb0 + group; kb < kb1 && !aborted; kb += p.groups) {
       const bool ok = pipe::wait(full0 + 8 * stage, phase, ctl);
       if (!__all_sync(0xFFFFFFFFu, ok)) { aborted = true; break; }
       const uint32_t b = ring0 + stage * stage_bytes + pair * 4096 + at;
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(empty0 + 8 * stage);
-      if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+      stage += p.groups;
+      if (stage >= p.stages) { stage -= p.stages; phase ^= 1u; }
       if (++in_chunk == 16) {  // 64 of K a block
         flush();
         in_chunk = 0;
@@ -292,6 +297,19 @@ __global__ void __launch_bounds__(RowsCfg<NT>::THREADS, 1)
       ptx::cluster_sync();  // no CTA leaves while its partial tile is read
       return;
     }
+    // the next tile's blocks follow this one's: from this warp's block after its last
+    // to the first of the next tile's
+    {
+      const uint32_t n = kb1 - kb0;
+      uint32_t own = group;  // blocks of this tile up to where `stage` stands
+      own += (n > group ? div_up_dev(n - group, p.groups) : 0u) * p.groups;
+      // the distance n + group - own is below the number of groups either way
+      const int move = int(n + group) - int(own);
+      int at_stage = int(stage) + move;
+      if (at_stage >= int(p.stages)) { at_stage -= int(p.stages); phase ^= 1u; }
+      if (at_stage < 0) { at_stage += int(p.stages); phase ^= 1u; }
+      stage = uint32_t(at_stage);
+    }
     // rows of the last group of 32 that the tile does not have, and of A beyond M
     for (uint32_t i = threadIdx.x; i < NT * 8 * line; i += threads)
       if (i / line >= uint32_t(p.M) || i % line >= p.R) part[i] = 0;
@@ -342,11 +360,9 @@ int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, i
                    int split, uint32_t debug_flags, uint64_t timeout_ns, bool early_b,
                    int num_sms, cudaStream_t stream) {
   const uint32_t kb = div_up(uint64_t(K), 128);
-  const uint32_t nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;
-  const uint32_t max_warps = nt <= 2 ? RowsCfg<1>::WARPS : nt == 4 ? RowsCfg<4>::WARPS
-                                                                   : RowsCfg<8>::WARPS;
-  const uint32_t max_r = nt <= 2 ? RowsCfg<1>::MAX_R : nt == 4 ? RowsCfg<4>::MAX_R
-                                                               : RowsCfg<8>::MAX_R;
+  const uint32_t nt = M <= 8 ? 1 : M <= 16 ? 2 : 4;
+  const uint32_t max_warps = nt <= 2 ? RowsCfg<1>::WARPS : RowsCfg<4>::WARPS;
+  const uint32_t max_r = nt <= 2 ? RowsCfg<1>::MAX_R : RowsCfg<4>::MAX_R;
   if (uint32_t(split) > kb) return SWZ_EUNSUPPORTED;  // an empty range of K
   // The split with the least to read for one SM: its tiles times the blocks of K times
   // the rows (a block of less than 28 takes as long as one of 28), and the cluster's
@@ -388,6 +404,7 @@ int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, i
   const uint32_t stage = R * 128 + nt * 1024, part = nt * 8 * (p.pairs * 32 + 4) * 4;
   p.stages = (uint32_t(kRowsSmem) - 1024 - part - 2 * kMaxStages * 8 - 16) / stage;
   if (p.stages > uint32_t(kMaxStages)) p.stages = kMaxStages;
+  if (p.groups > p.stages) p.groups = p.stages;
   p.debug_flags = debug_flags;
   p.timeout_ns = timeout_ns;
   CUtensorMap ta, tb;
@@ -403,8 +420,7 @@ int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, i
   switch (nt) {
     case 1: return launch_rows<1>(ta, tb, p, ctas, stream);
     case 2: return launch_rows<2>(ta, tb, p, ctas, stream);
-    case 4: return launch_rows<4>(ta, tb, p, ctas, stream);
-    default: return launch_rows<8>(ta, tb, p, ctas, stream);
+    default: return launch_rows<4>(ta, tb, p, ctas, stream);
   }
 }
 

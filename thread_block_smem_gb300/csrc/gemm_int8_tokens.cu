@@ -1,19 +1,24 @@
-// gemm_int8_tokens.cu -- swz_gemm_int8 and swz_linear_int8 with one to eight rows of
-// A (a decoding step), the same exact sums by dp4a.
+// gemm_int8_tokens.cu -- swz_gemm_int8 and swz_linear_int8 with one or two rows of A
+// (a decoding step), the same exact sums by dp4a.
 //
 // Bound: reading B once, N * K bytes.  A CTA takes a range of B's rows, the same
 // number for all within one, and a warp of it a slot of K (512 bytes at a time, 16 a
 // lane) of every `groups`-th of these rows.  A lane's 16 bytes of each row of A stay
 // in registers for all of them, so that the inner loop is one load, four dp4a for
-// each row of A, and one sum over the warp (redux) for each.  Eight rows' loads (four
-// beside more than two rows of A) are in flight a warp.  The partial sums of the slots are added in shared memory: whole
+// each row of A, and one sum over the warp (redux) for each.  Eight rows' loads are
+// in flight a warp.  The partial sums of the slots are added in shared memory: whole
 // numbers, in any order.
 //   * The layer quantises x here where it is short: every CTA needs all of it, and a
 //     few thousand values are read and rounded while its first loads of B are under
 //     way; a kernel of its own takes 1.8 us.
 //   * Rates on this GPU, multiply-adds a clock and SM: dp4a 255, mma.sync on 8-bit
-//     integers 252, on fp16 1024.  B at the memory's rate asks for 24 a row of A, so
-//     dp4a has room for eight rows; fp16 would cost a conversion of every byte of B.
+//     integers 252, on fp16 1020.  B at the memory's rate asks for 24 a row of A.
+//
+// Measured, in a stream of them, B from memory: one row of 4096 x 4096 5.4 us
+// (3.1 TB/s; 6.2 with x quantised here), 10240 x 4096 10.1 (4.2), 8192 x 8192 13.2
+// (5.1); of the ring of gemm_int8_rows.cu 5.9, 10.6 and 14.2.  Two rows take 5.9, 11.4
+// and 14.6 and the ring 5.9, 10.6 and 14.2, and a quantiser of its own before it; four
+// rows 7.5, 13.5 and 18.2.
 #include <type_traits>
 
 #include "common.h"
@@ -42,20 +47,6 @@ struct TokParams {
   uint32_t slots, groups;  // of K and of rows, slots * groups = kTokWarps
 };
 
-// 16 bytes of a row from k < K on.  What lies between K and the next multiple of 16
-// is in the row as well (it may be anything: x is zero there), but for the last row
-// of the matrix, whose bytes at K and beyond read as zero.
-__device__ __forceinline__ uint4 load_bytes(const uint8_t* row, int k, int K, bool last) {
-  if (k + 16 <= K || !last) return *reinterpret_cast<const uint4*>(row + k);
-  uint64_t lo = 0, hi = 0;
-#pragma unroll 1
-  for (int e = K - k - 1; e >= 0; --e) {
-    hi = (hi << 8) | (lo >> 56);
-    lo = (lo << 8) | row[k + e];
-  }
-  return make_uint4(uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32));
-}
-
 // the bytes of 16 that lie below K, for those from k on
 __device__ __forceinline__ uint4 keep_below(uint4 v, int k, int K) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -71,7 +62,7 @@ __device__ __forceinline__ uint4 keep_below(uint4 v, int k, int K) {
 template <int MT, typename X>
 __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const TokParams p) {
   constexpr bool FUSED = !std::is_same<X, void>::value;
-  constexpr int kAhead = MT <= 2 ? 8 : 4;  // rows of B whose loads are in flight
+  constexpr int kAhead = 8;  // rows of B whose loads are in flight
   extern __shared__ uint4 tok_smem[];  // FUSED: x as bytes, rows of `pitch`
   __shared__ int32_t part[MT][kTokRows];
   __shared__ float scale[MT];
@@ -86,14 +77,16 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
 
+  // Every load is made, of rows and pieces that are there: rows beyond the range are not
+  // summed, and what is beyond K meets zeros.
   uint4 b[kAhead];
+  const int cut = p.K % 16 ? p.K - p.K % 16 : -1;  // the piece that K cuts
   auto fetch = [&](int n, int k) {
-    const uint8_t* row = p.B + int64_t(n) * p.ldb;
+    if (k >= p.K || k == cut) k = 0;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      b[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (n + i * int(p.groups) < n1 && k < p.K) b[i] = load_bytes(row, k, p.K, n + i * int(p.groups) + 1 == p.N);
-      row += int64_t(p.groups) * p.ldb;
+      const int row = n + i * int(p.groups);
+      b[i] = *reinterpret_cast<const uint4*>(p.B + int64_t(row < n1 ? row : n1 - 1) * p.ldb + k);
     }
   };
   fetch(n0 + int(group), k0);
@@ -153,6 +146,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
         for (int i = 0; i < kAhead; ++i) {
           const int row = n + i * int(p.groups);
           if (row >= end) break;
+          if (k == cut)
+            b[i] = load_bytes(p.B + int64_t(row) * p.ldb, k, p.K, row + 1 == p.N);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             int32_t s = __dp4a(int(b[i].x), int(a[t].x), 0);
@@ -199,15 +194,11 @@ static int launch_tokens(const TokParams& p, int num_sms, cudaStream_t s) {
 
 template <typename X>
 static int launch_rows_of(const TokParams& p, int num_sms, cudaStream_t s) {
-  if (p.M == 1) return launch_tokens<1, X>(p, num_sms, s);
-  if (p.M == 2) return launch_tokens<2, X>(p, num_sms, s);
-  if constexpr (std::is_same<X, void>::value)
-    if (p.M > 4) return launch_tokens<8, X>(p, num_sms, s);
-  return launch_tokens<4, X>(p, num_sms, s);
+  return p.M == 1 ? launch_tokens<1, X>(p, num_sms, s) : launch_tokens<2, X>(p, num_sms, s);
 }
 
 // x short enough to be quantised by every CTA
-bool tokens_fused(int M, int K) { return M <= 4 && int64_t(M) * K <= kTokBytes / 2; }
+bool tokens_fused(int M, int K) { return int64_t(M) * K <= kTokBytes; }
 
 int gemm_int8_tokens(const void* A, int64_t lda, const float* sa, const void* x, int x_dtype,
                      int64_t ldx, const void* B, int64_t ldb, const float* sb, void* C,

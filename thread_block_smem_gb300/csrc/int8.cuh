@@ -18,25 +18,52 @@ constexpr int kMaxK = 131071;
 int quantize_rows(const void* x, int dtype, int64_t ldx, int M, int K, void* q, int64_t ldq,
                   float* scales, bool half, cudaStream_t s);
 
-// The product of up to kMaxRows rows of A, which needs no workspace (arguments
-// checked by the caller; split 0: automatic).  `early_b`: the kernel before in the
-// stream is the quantiser of A, launched by the same caller, and B may be read while
-// it runs.
-constexpr int kMaxRows = 64;
-int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, int64_t ldb,
-                   const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,
-                   int split, uint32_t debug_flags, uint64_t timeout_ns, bool early_b,
-                   int num_sms, cudaStream_t stream);
-
 // The product of up to kTokens rows of A (bytes with the scales sa), or with A NULL
 // the layer of as many rows of x (tokens_fused says where); arguments checked by the
 // caller.
-constexpr int kTokens = 4;
+constexpr int kTokens = 2;
 bool tokens_fused(int M, int K);
 int gemm_int8_tokens(const void* A, int64_t lda, const float* sa, const void* x, int x_dtype,
                      int64_t ldx, const void* B, int64_t ldb, const float* sb, void* C,
                      int64_t ldc, int c_dtype, int M, int N, int K, int num_sms,
                      cudaStream_t stream);
+
+// The product of up to kRingRows rows of A, which needs no workspace (split 0:
+// automatic).  `early_b`: the kernel before in the stream is the quantiser of A,
+// launched by the same call, and B may be read while it runs.
+constexpr int kRingRows = 32;
+int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, int64_t ldb,
+                   const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,
+                   int split, uint32_t debug_flags, uint64_t timeout_ns, bool early_b,
+                   int num_sms, cudaStream_t stream);
+
+// The product of a few to some hundred rows of A, given as fp16 numbers (rows of `ld`
+// elements, written by the kernel that the same call launched before), with B as
+// bytes; arguments checked by the caller.
+constexpr int kBatchRows = 256;
+struct BatchPlan {
+  uint32_t tiles_m, nb, ctas_per_sm, stages, slots, split, tmem_cols;  // split 0: not for it
+  uint64_t tiles;
+};
+BatchPlan batch_plan(int M, int N, int K, int split, int num_sms);
+int gemm_int8_batch(const void* a16, int64_t ld, const float* sa, const void* B, int64_t ldb,
+                    const float* sb, void* C, int64_t ldc, int c_dtype, int M, int N, int K,
+                    const BatchPlan& b, uint32_t debug_flags, uint64_t timeout_ns,
+                    cudaStream_t stream);
+
+// 16 bytes of a row from k < K on.  What lies between K and the next multiple of 16
+// is in the row as well (it may be anything: x is zero there), but for the last row
+// of the matrix, whose bytes at K and beyond read as zero.
+__device__ __forceinline__ uint4 load_bytes(const uint8_t* row, int k, int K, bool last) {
+  if (k + 16 <= K || !last) return *reinterpret_cast<const uint4*>(row + k);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int e = K - k - 1; e >= 0; --e) {
+    hi = (hi << 8) | (lo >> 56);
+    lo = (lo << 8) | row[k + e];
+  }
+  return make_uint4(uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32));
+}
 
 // ---- the quantisation's rule -----------------------------------------------------
 // largest magnitude of a chunk of eight values, as bits of the type
