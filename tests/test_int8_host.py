@@ -103,7 +103,7 @@ def test_layer_norm_checks(swz):
     a = list(good)
     a[17] = 0
     assert swz.swz_layer_norm_backward(*a) == swz.SWZ_OK
-    assert swz.swz_layer_norm_backward_workspace_size(3, 50) == (0, 3 * 2 * 50 * 4)
+    assert swz.swz_layer_norm_backward_workspace_size(3, 50) == (0, 3 * 2 * 56 * 4)
     assert swz.swz_layer_norm_backward_workspace_size(-1, 50)[0] == E
 
 

@@ -5,12 +5,15 @@
 // once.
 //
 // Bound: memory, x and dy read and dx written once.  A CTA takes every P-th row (or
-// every P-th eight rows, a row a warp, where rows are short), and a thread the same
-// columns of each of them, so that its parts of dw and db stay in registers; the
-// P partial rows go to the workspace and a second kernel adds them in order
-// (deterministic, no atomics).  The next row's loads are under way while this one's
-// two sums cross the CTA.  Rows longer than 16384 take dx and the partial sums in
-// two kernels that read both inputs again.
+// every P-th eight rows, a row a warp, where rows have 512 values or less), and a
+// thread the same columns of each of them, so that its parts of dw and db stay in
+// registers; the P partial rows go to the workspace and a second kernel adds them in
+// order (deterministic, no atomics).  The next row's loads are under way while this
+// one's two sums cross the CTA; w comes from L1, where x and dy leave it alone.  As many threads as the row asks for, each with NC
+// chunks of eight columns.  P is a quarter of the rows at most, or one a SM, since each
+// partial row costs as much as two thirds of a row of bf16 inputs.  Rows longer than
+// 16384 take dx and the partial sums in two kernels that read both inputs again.
+#include <algorithm>
 #include <type_traits>
 
 #include "layer_norm.cuh"
@@ -20,6 +23,7 @@ namespace swz {
 namespace norm {
 
 constexpr int kMaxParts = 608;  // partial rows, whatever the device
+static int64_t pitch_of(int N) { return (int64_t(N) + 7) / 8 * 8; }
 
 struct BwdArgs {
   rows::Span x, dy;
@@ -29,104 +33,155 @@ struct BwdArgs {
   uint8_t* dx;  // NULL: not wanted
   int64_t lddx;  // bytes
   int dx_dtype, dx_wide;
-  float* parts;  // (P, 2, N): dw, then db; NULL: neither wanted
+  float* parts;  // (P, 2, pitch): dw, then db; NULL: neither wanted
+  int64_t pitch;
 };
 
-// TPR threads a row (32: each warp rows of its own), NC chunks a thread.
-template <typename X, typename D, int TPR, int NC>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR)
-    layer_norm_backward_kernel(const BwdArgs p) {
-  constexpr int RPC = TPR == 32 ? 8 : 1;  // rows a CTA and turn
-  __shared__ float part[2][2 * (TPR / 32)];
-  __shared__ float both[TPR == 32 ? 2 * NC * 256 : 1];
+// NC chunks a thread; WARP: a row a warp, eight a CTA, otherwise a row the CTA; G: the
+// common case (layer_norm.cuh) or 0.
+template <typename X, typename D, int NC, bool WARP, int G>
+__global__ void __launch_bounds__(WARP ? 256 : 512) layer_norm_backward_kernel(const BwdArgs p) {
+  __shared__ float2 part[2][16];
+  __shared__ ulonglong2 sums[WARP ? NC * 128 : 1];  // of the warps: dw, then db
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
-  const uint32_t t = threadIdx.x % TPR;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int width = WARP ? 32 : int(blockDim.x), warps = WARP ? 1 : int(blockDim.x) / 32;
+  const int t = WARP ? int(lane) : int(threadIdx.x);
   const int es = p.dx_dtype == SWZ_F32 ? 4 : 2;
   const float inv = 1.0f / float(p.N);
 
-  float w[NC][8], dw[NC][8], db[NC][8];
+  uint64_t dw[NC][4], db[NC][4];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    load_vec(p.w, (int64_t(c) * TPR + t) * 8, p.N, 1.0f, w[c]);
+  for (int c = 0; c < NC; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.0f;
-  }
-  uint32_t xw[NC][X::kWords], dw_[NC][D::kWords];
+    for (int i = 0; i < 4; ++i) dw[c][i] = db[c][i] = 0ull;
+  uint32_t xw[NC][X::kWords], dyw[NC][D::kWords];
   float mean = 0.0f, rstd = 0.0f;
   auto fetch = [&](int64_t row) {
+    const uint8_t *x = p.x.base + row * p.x.ld, *dy = p.dy.base + row * p.dy.ld;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t k = (int64_t(c) * TPR + t) * 8;
-      rows::load8<X>(p.x.base + row * p.x.ld + k * X::kBytes, p.N - k, p.x, xw[c]);
-      rows::load8<D>(p.dy.base + row * p.dy.ld + k * D::kBytes, p.N - k, p.dy, dw_[c]);
+      const int k = (c * width + t) * 8;
+      if constexpr (G) {
+        fast_load<X>(x + int64_t(k) * X::kBytes, k < p.N, xw[c]);
+        fast_load<D>(dy + int64_t(k) * D::kBytes, k < p.N, dyw[c]);
+      } else {
+        rows::load8_once<X>(x + int64_t(k) * X::kBytes, p.N - k, p.x, xw[c]);
+        rows::load8_once<D>(dy + int64_t(k) * D::kBytes, p.N - k, p.dy, dyw[c]);
+      }
     }
     mean = p.mean[row];
     rstd = p.rstd[row];
   };
-  const int64_t step = int64_t(gridDim.x) * RPC;
-  int64_t row = int64_t(blockIdx.x) * RPC + threadIdx.x / TPR;
-  if (row < p.M) fetch(row);
+  // With four chunks a thread there are no registers for a row's values beside the next
+  // one's: they are worked out again from the inputs as they were loaded.
+  constexpr bool AHEAD = NC <= 2;
+  const int64_t step = int64_t(gridDim.x) * (WARP ? 8 : 1);
+  int64_t row = WARP ? int64_t(blockIdx.x) * 8 + warp : int64_t(blockIdx.x);
+  if (AHEAD && row < p.M) fetch(row);
   for (uint32_t turn = 0; row < p.M; row += step, turn ^= 1u) {
-    float xhat[NC][8], d[NC][8], s[2] = {0.0f, 0.0f};
+    if (!AHEAD) fetch(row);
+    uint64_t xhat[AHEAD ? NC : 1][4], d[AHEAD ? NC : 1][4], s0 = 0ull, s1 = 0ull;
+    const uint64_t m2 = both(-mean), r2 = both(rstd);
+    auto values = [&](int c, uint64_t (&h)[4], uint64_t (&g)[4], uint64_t (&v)[4]) {
+      uint64_t x[4], w[4];
+      pairs_of<X>(xw[c], x);
+      pairs_of<D>(dyw[c], v);
+      const int k = (c * width + t) * 8;
+      // (beyond the row dy is zero, and so is what it is multiplied by)
+      if constexpr (G) fast_vec<X, G>(p.w.p, k < p.N ? k : 0, w);
+      else load_vec2(p.w, k, p.N, 1.0f, w);
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float h = (X::value(xw[c], i) - mean) * rstd, v = D::value(dw_[c], i);
-        dw[c][i] += v * h;
-        db[c][i] += v;
-        xhat[c][i] = h;
-        d[c][i] = v * w[c][i];
-        s[0] += d[c][i];
-        s[1] += d[c][i] * h;
+      for (int i = 0; i < 4; ++i) {
+        h[i] = pipe::mul2(add2(x[i], m2), r2);
+        g[i] = pipe::mul2(v[i], w[i]);
       }
-    const float rs = rstd;
-    if (row + step < p.M) fetch(row + step);
+    };
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      uint64_t(&h)[4] = xhat[AHEAD ? c : 0];
+      uint64_t(&g)[4] = d[AHEAD ? c : 0];
+      uint64_t v[4];
+      values(c, h, g, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dw[c][i] = pipe::fma2(v[i], h[i], dw[c][i]);
+        db[c][i] = add2(db[c][i], v[i]);
+        s0 = add2(s0, g[i]);
+        s1 = pipe::fma2(g[i], h[i], s1);
+      }
+    }
+    if (AHEAD && row + step < p.M) fetch(row + step);
     if (p.dx) {
-      rows::row_sums<TPR, 2>(s, part[turn]);
-      const float a = s[0] * inv, b = s[1] * inv;
+      float a = rows::warp_sum(sum_of(s0)), b = rows::warp_sum(sum_of(s1));
+      if constexpr (!WARP) {
+        if (lane == 0) part[turn][warp] = make_float2(a, b);
+        __syncthreads();
+        a = b = 0.0f;
+        for (int i = 0; i < warps; ++i) {
+          const float2 u = part[turn][i];
+          a += u.x;
+          b += u.y;
+        }
+      }
+      const uint64_t a2 = both(-a * inv), b2 = both(-b * inv);
       uint8_t* dx = p.dx + row * p.lddx;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int64_t k = (int64_t(c) * TPR + t) * 8;
-        float o[8];
+        const int k = (c * width + t) * 8;
+        uint64_t(&h)[4] = xhat[AHEAD ? c : 0];
+        uint64_t(&g)[4] = d[AHEAD ? c : 0];
+        uint64_t o[4];
+        if (!AHEAD) values(c, h, g, o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = rs * (d[c][i] - a - xhat[c][i] * b);
-        rows::store8(dx + k * es, p.N - k, o, p.dx_dtype, p.dx_wide != 0);
+        for (int i = 0; i < 4; ++i)
+          o[i] = pipe::mul2(pipe::fma2(h[i], b2, add2(g[i], a2)), r2);
+        if constexpr (G) {
+          if (k < p.N) fast_store<X>(dx + int64_t(k) * X::kBytes, o);
+        } else {
+          store_pairs(dx + int64_t(k) * es, p.N - k, o, p.dx_dtype, p.dx_wide != 0);
+        }
       }
     }
   }
   if (!p.parts) return;
-  if constexpr (TPR == 32) {
+  // partial rows of `pitch` values, a multiple of eight: whole chunks are stored
+  float* const out = p.parts + int64_t(blockIdx.x) * 2 * p.pitch;
+  auto put = [&](int k, int e, ulonglong2 v) {  // e: two quads of dw, then of db
+    *reinterpret_cast<ulonglong2*>(out + (e < 2 ? 0 : p.pitch) + k + 4 * (e & 1)) = v;
+  };
+  if constexpr (WARP) {
     // the eight warps' sums, added in order
     for (uint32_t i = 0; i < 8; ++i) {
-      if (threadIdx.x / 32 == i)
+      if (warp == i)
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* at = both + (c * 32 + t) * 8 + e;
-            at[0] = i ? at[0] + dw[c][e] : dw[c][e];
-            at[NC * 256] = i ? at[NC * 256] + db[c][e] : db[c][e];
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t* v = e < 2 ? &dw[c][2 * e] : &db[c][2 * e - 4];
+            ulonglong2& at = sums[(c * 4 + e) * 32 + lane];
+            at = i ? make_ulonglong2(add2(at.x, v[0]), add2(at.y, v[1])) : make_ulonglong2(v[0], v[1]);
           }
       __syncthreads();
     }
-    float* out = p.parts + int64_t(blockIdx.x) * 2 * p.N;
-    for (int k = int(threadIdx.x); k < p.N; k += 256) {
-      out[k] = both[k];
-      out[p.N + k] = both[NC * 256 + k];
-    }
+    if (warp == 0)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int k = (c * 32 + int(lane)) * 8;
+        if (k < p.N)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) put(k, e, sums[(c * 4 + e) * 32 + lane]);
+      }
   } else {
-    float* out = p.parts + int64_t(blockIdx.x) * 2 * p.N;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const int64_t k = (int64_t(c) * TPR + t) * 8;
+      const int k = (c * width + t) * 8;
+      if (k < p.N)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (k + i < p.N) {
-          out[k + i] = dw[c][i];
-          out[p.N + k + i] = db[c][i];
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t* v = e < 2 ? &dw[c][2 * e] : &db[c][2 * e - 4];
+          put(k, e, make_ulonglong2(v[0], v[1]));
         }
     }
   }
@@ -192,64 +247,78 @@ __global__ void __launch_bounds__(256) long_parts_kernel(const BwdArgs p) {
     dw += v * ((x - p.mean[row]) * p.rstd[row]);
     db += v;
   }
-  float* out = p.parts + int64_t(blockIdx.y) * 2 * p.N;
+  float* out = p.parts + int64_t(blockIdx.y) * 2 * p.pitch;
   out[k] = dw;
-  out[p.N + k] = db;
+  out[p.pitch + k] = db;
 }
 
 // ---- the partial rows' sum ----------------------------------------------------------
 struct SumArgs {
   const float* parts;
   int P, N;
+  int64_t pitch;
   uint8_t *dw, *db;  // either may be NULL
   int dtype;
 };
 
-// blockIdx.y: 0 dw, 1 db.  32 columns a CTA, its 8 warps every eighth partial row each.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumArgs p) {
-  __shared__ float part[8][32];
+// blockIdx.y: 0 dw, 1 db.  32 columns a CTA; a warp adds every 32nd partial row, so
+// that a few loads a thread, all in flight, do it.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const SumArgs p) {
+  __shared__ float part[32][32];
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
-  const int64_t k = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
+  const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t k = int64_t(blockIdx.x) * 32 + lane;
   uint8_t* out = blockIdx.y ? p.db : p.dw;
   if (!out) return;
   float s = 0.0f;
   if (k < p.N) {
-    const float* src = p.parts + int64_t(blockIdx.y) * p.N + k;
+    const float* src = p.parts + int64_t(blockIdx.y) * p.pitch + k;
 #pragma unroll 8
-    for (int i = int(threadIdx.x / 32); i < p.P; i += 8) s += src[int64_t(i) * 2 * p.N];
+    for (int i = int(warp); i < p.P; i += 32) s += src[int64_t(i) * 2 * p.pitch];
   }
-  part[threadIdx.x / 32][threadIdx.x % 32] = s;
+  part[warp][lane] = s;
   __syncthreads();
-  if (threadIdx.x < 32 && k < p.N) {
+  if (warp == 0 && k < p.N) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += part[i][lane];
     rows::store1(out + k * (p.dtype == SWZ_F32 ? 4 : 2), s, p.dtype);
   }
 }
 
-template <typename X, typename D, int TPR, int NC>
-static int start(const BwdArgs& a, int* P, int num_sms, cudaStream_t s) {
-  auto kern = layer_norm_backward_kernel<X, D, TPR, NC>;
-  constexpr int threads = TPR == 32 ? 256 : TPR;
+template <typename X, typename D, int NC, bool WARP, int G>
+static int start_kind(const BwdArgs& a, int* P, int num_sms, cudaStream_t s) {
+  const int threads = WARP ? 256 : threads_of(a.N, NC);
   int resident = 0;
-  SWZ_CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, 0));
-  int64_t grid = (int64_t(a.M) + (TPR == 32 ? 7 : 0)) / (TPR == 32 ? 8 : 1);
-  const int64_t cap = int64_t(num_sms) * (resident < 1 ? 1 : resident);
-  if (grid > cap) grid = cap;
-  if (a.parts && grid > kMaxParts) grid = kMaxParts;
-  *P = int(grid);
-  return launch(kern, uint32_t(grid), threads, a, s);
+  const int rc = resident_ctas<layer_norm_backward_kernel<X, D, NC, WARP, G>>(threads, &resident);
+  if (rc != SWZ_OK) return rc;
+  const int64_t rows = WARP ? (int64_t(a.M) + 7) / 8 : int64_t(a.M);
+  int64_t most = int64_t(num_sms) * resident;
+  if (a.parts) {
+    const int64_t few = std::max(int64_t(num_sms), rows / 4);
+    most = std::min(std::min(most, few), int64_t(kMaxParts));
+  }
+  *P = int(std::min(rows, most));
+  return launch(layer_norm_backward_kernel<X, D, NC, WARP, G>, uint32_t(*P), uint32_t(threads), a, s);
+}
+
+template <typename X, typename D, int NC, bool WARP>
+static int start(const BwdArgs& a, int* P, int num_sms, cudaStream_t s) {
+  const int g = kind_of<X>(a.w);
+  if (g == 0 || !a.x.wide || !a.dy.wide || a.N % 8 != 0 ||
+      (a.dx && (!a.dx_wide || a.dx_dtype != code_of<X>())))
+    return start_kind<X, D, NC, WARP, 0>(a, P, num_sms, s);
+  if constexpr (X::kBytes == 2)
+    if (g == 2) return start_kind<X, D, NC, WARP, 2>(a, P, num_sms, s);
+  return start_kind<X, D, NC, WARP, 1>(a, P, num_sms, s);
 }
 
 template <typename X, typename D>
 static int dispatch(const BwdArgs& a, int* P, int num_sms, cudaStream_t s) {
-  if (a.N <= 256) return start<X, D, 32, 1>(a, P, num_sms, s);
-  if (a.N <= 1024) return start<X, D, 32, 4>(a, P, num_sms, s);
-  if (a.N <= 2048) return start<X, D, 128, 2>(a, P, num_sms, s);
-  if (a.N <= 4096) return start<X, D, 256, 2>(a, P, num_sms, s);
-  if (a.N <= 8192) return start<X, D, 512, 2>(a, P, num_sms, s);
-  if (a.N <= 16384) return start<X, D, 512, 4>(a, P, num_sms, s);
+  if (a.N <= 256) return start<X, D, 1, true>(a, P, num_sms, s);
+  if (a.N <= 512) return start<X, D, 2, true>(a, P, num_sms, s);
+  if (a.N <= 8192) return start<X, D, 2, false>(a, P, num_sms, s);
+  if (a.N <= 16384) return start<X, D, 4, false>(a, P, num_sms, s);
   if (a.dx) {
     const int rc = launch(long_dx_kernel<X, D>, uint32_t(a.M), 512, a, s);
     if (rc != SWZ_OK) return rc;
@@ -280,7 +349,7 @@ using namespace swz::norm;
 
 extern "C" int swz_layer_norm_backward_workspace_size(int M, int N, uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0) return SWZ_EINVAL;
-  *h_bytes = uint64_t(M < kMaxParts ? M : kMaxParts) * 2 * uint64_t(N) * 4;
+  *h_bytes = uint64_t(M < kMaxParts ? M : kMaxParts) * 2 * uint64_t(pitch_of(N)) * 4;
   return SWZ_OK;
 }
 
@@ -331,6 +400,7 @@ extern "C" int swz_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
   a.dx_dtype = dx_dtype;
   a.dx_wide = aligned16(dx) && a.lddx % 16 == 0;
   a.parts = sums ? static_cast<float*>(d_workspace) : nullptr;
+  a.pitch = pitch_of(N);
   int P = 0;
   if (dtype == SWZ_BF16) rc = dispatch_dy<rows::Bf16>(a, dy_dtype, &P, dev.num_sms, s);
   else if (dtype == SWZ_F16) rc = dispatch_dy<rows::F16>(a, dy_dtype, &P, dev.num_sms, s);
@@ -340,12 +410,13 @@ extern "C" int swz_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
   g.parts = a.parts;
   g.P = P;
   g.N = N;
+  g.pitch = a.pitch;
   g.dw = static_cast<uint8_t*>(dw);
   g.db = static_cast<uint8_t*>(db);
   g.dtype = dw_dtype;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t((int64_t(N) + 31) / 32), 2);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

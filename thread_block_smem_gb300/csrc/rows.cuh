@@ -62,16 +62,47 @@ __device__ __forceinline__ void ld16(const uint8_t* p, uint32_t* w) {
   w[3] = v.w;
 }
 
+// The same, of what is read once: it leaves L1 to what is read again.
+__device__ __forceinline__ void ld16_once(const uint8_t* p, uint32_t* w) {
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p)
+               : "memory");
+}
+
+// Four words of the first n values at p, from the value `from` on (16-bit: all eight).
+// In loops, as the other rare paths are: unrolled into each chunk they made kernels of
+// a few rows wait for their instructions.
+template <typename T>
+__device__ __forceinline__ uint4 load_some(const uint8_t* p, int n, int from) {
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int i = 7; i >= 0; --i) {
+    const bool in = i < n;
+    if constexpr (T::kBytes == 2) {
+      hi = (hi << 16) | (lo >> 48);
+      lo = (lo << 16) | (in ? uint64_t(reinterpret_cast<const uint16_t*>(p)[i]) : 0u);
+    } else if (i >= from && i < from + 4) {
+      hi = (hi << 32) | (lo >> 32);
+      lo = (lo << 32) | (in ? uint64_t(reinterpret_cast<const uint32_t*>(p)[i]) : 0u);
+    }
+  }
+  return make_uint4(uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32));
+}
+
 // Eight values at p, of which `n` exist (<= 0: none); the others read as zero.
 // Plain loads: what they read may be written by the kernel before, which may
 // still run when this one starts.
-template <typename T>
+template <typename T, bool ONCE = false>
 __device__ __forceinline__ void load8(const uint8_t* p, int64_t n, const Span& m, uint32_t* w) {
   if (n >= 8) {
     const uint32_t s = m.wide ? 0u : uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
     if (s == 0) {
 #pragma unroll
-      for (int j = 0; j < T::kWords / 4; ++j) ld16(p + 16 * j, w + 4 * j);
+      for (int j = 0; j < T::kWords / 4; ++j) {
+        if constexpr (ONCE) ld16_once(p + 16 * j, w + 4 * j);
+        else ld16(p + 16 * j, w + 4 * j);
+      }
       return;
     }
     const uint8_t* q = p - s;
@@ -90,14 +121,23 @@ __device__ __forceinline__ void load8(const uint8_t* p, int64_t n, const Span& m
   }
 #pragma unroll
   for (int j = 0; j < T::kWords; ++j) w[j] = 0u;
+  if (n > 0) {
+    const int some = n < 8 ? int(n) : 8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) {
-      if constexpr (T::kBytes == 2)
-        w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i & 1));
-      else
-        w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    for (int j = 0; j < T::kWords / 4; ++j) {
+      const uint4 v = load_some<T>(p, some, 4 * j);
+      w[4 * j] = v.x;
+      w[4 * j + 1] = v.y;
+      w[4 * j + 2] = v.z;
+      w[4 * j + 3] = v.w;
     }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_once(const uint8_t* p, int64_t n, const Span& m,
+                                           uint32_t* w) {
+  load8<T, true>(p, n, m, w);
 }
 
 __device__ __forceinline__ uint32_t pack16(float a, float b, int dtype) {
@@ -121,6 +161,21 @@ __device__ __forceinline__ float load1(const uint8_t* p, int dtype) {
   return __half2float(*reinterpret_cast<const __half*>(p));
 }
 
+// The values from .. to - 1 of v at p, one by one.
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ void store_some(uint8_t* p, Eight e, int from, int to, int dtype) {
+  const int es = dtype == SWZ_F32 ? 4 : 2;
+#pragma unroll 1
+  for (int i = from; i < to; ++i) {
+    float x = e.v[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) x = i == j ? e.v[j] : x;
+    store1(p + i * es, x, dtype);
+  }
+}
+
 // Stores `n` (unclamped: 8 or more for a whole chunk, <= 0 for none) of the eight
 // values v at p, rounded once.  All lanes of the warp call it together, lane i with
 // the chunk after lane i - 1's.
@@ -142,9 +197,12 @@ __device__ __forceinline__ void store8(uint8_t* p, int64_t n, const float (&v)[8
       if (f32) *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
       return;
     }
+    if (n > 0) {
+      Eight x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) store1(p + i * (f32 ? 4 : 2), v[i], dtype);
+      for (int i = 0; i < 8; ++i) x.v[i] = v[i];
+      store_some(p, x, 0, int(n), dtype);
+    }
     return;
   }
   // the last 16 bytes of the lane before, then this lane's: `head` bytes of its own
@@ -171,9 +229,13 @@ __device__ __forceinline__ void store8(uint8_t* p, int64_t n, const float (&v)[8
   }
   // the next lane stores this one's last values with its own head, if it is full
   const int to = (lane < 31 && n - 8 >= head) ? whole : 8;
+  const int end = n < to ? int(n) : to;
+  if (from < end) {
+    Eight x;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i >= from && i < to && i < n) store1(p + i * es, v[i], dtype);
+    for (int i = 0; i < 8; ++i) x.v[i] = v[i];
+    store_some(p, x, from, end, dtype);
+  }
 }
 
 // Sum of v over the warp, the same bits in every lane.
