@@ -727,7 +727,7 @@ typedef struct swz_grad {
 
 /*
  * swz_grad_norm -- *norm (device) = sqrt(sum of the squares of all values of the
- * `count` tensors).  Sums in 64 bits over partial sums of 64 values in fp32, in an
+ * `count` tensors).  Sums of 64 values in fp32, above them as if in 48 bits or more, in an
  * order that depends on the sizes and the device only; squares that would leave
  * fp32's range are scaled.  An infinity or NaN gives an infinite or NaN norm.
  *

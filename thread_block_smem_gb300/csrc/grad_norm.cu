@@ -5,11 +5,11 @@
 //
 // The tensors come as a list; a launch carries their pointers and sizes in its
 // parameters (no copy to the device, nothing kept between calls, and a captured
-// launch has its own).  All elements are cut into pieces of kPiece, dealt out
-// to the CTAs.
+// launch has its own).  All elements are cut into pieces, dealt out to the CTAs.
 //
-// Sums: a piece's squares are added in fp32 by each thread (64 of them), everything
-// above in 64 bits, in an order that depends on the sizes alone.  Squares leave
+// Sums: a piece's squares are added in fp32 by each thread (64 of them, two sums of
+// 32), a thread's pieces in two fp32 numbers, everything above in 64 bits, in an order
+// that depends on the sizes alone.  Squares leave
 // fp32's range long before the gradients do, so eight values at a time whose largest
 // magnitude is not within 2^-40 .. 2^50 are squared after a multiplication by 2^80
 // or 2^-80 and kept apart.
@@ -21,15 +21,17 @@
 #include <vector>
 
 #include "common.h"
-#include "ptx.cuh"
+#include "pipe.cuh"
 #include "rows.cuh"
 
 namespace swz {
 namespace grad {
 
 constexpr int kThreads = 256;
-constexpr int kTurns = 8;                          // chunks of eight values a thread and piece
-constexpr int64_t kPiece = int64_t(kThreads) * kTurns * 8;
+// chunks of eight values a thread and piece, of the pass that adds and of that which
+// scales (and has to hold its results)
+constexpr int kAddTurns = 8, kScaleTurns = 4;
+constexpr int64_t piece_of(int turns) { return int64_t(kThreads) * turns * 8; }
 constexpr int kMaxBlocks = 1216;                   // partial sums of one launch
 constexpr int kFew = 32, kMany = 1000;             // tensors a launch carries
 
@@ -54,9 +56,10 @@ struct Table {
 };
 static_assert(sizeof(Table<kMany>) <= 32764, "kernel parameters");
 
-// the tensor that piece `i` belongs to
+// the tensor that piece `i` belongs to; `was`: the one of the piece before
 template <int CAP>
-__device__ __forceinline__ int tensor_of(const Table<CAP>& p, uint32_t i) {
+__device__ __forceinline__ int tensor_of(const Table<CAP>& p, uint32_t i, int was) {
+  if (p.t[was].first <= i && (was + 1 == p.count || i < p.t[was + 1].first)) return was;
   int lo = 0, hi = p.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
@@ -66,52 +69,86 @@ __device__ __forceinline__ int tensor_of(const Table<CAP>& p, uint32_t i) {
   return lo;
 }
 
+__device__ __forceinline__ float sum_of(uint64_t v) {
+  float a, b;
+  pipe::unpack2(v, a, b);
+  return a + b;
+}
+
+// Sums of squares, two at a time: as they are, and of what was scaled down or up.
+struct Squares {
+  uint64_t mid = 0ull, high = 0ull, low = 0ull;
+};
+
 template <typename T>
-__device__ __forceinline__ void add_squares(const uint32_t* w, float& mid, float& high, float& low) {
+__device__ __forceinline__ void add_squares(const uint32_t* w, Squares& s) {
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < T::kWords; ++j) m = f8::max_packed<T>(m, w[j] & T::kAbs);
   if constexpr (T::kBytes == 2) m = max(m & 0xFFFFu, m >> 16);
-  if (m == 0) return;
   const uint32_t bits = T::max_bits(m);
   constexpr uint32_t kLow = (127 - 40) << 23, kHigh = (127 + 50) << 23;
-  if (bits >= kLow && bits < kHigh) {
+  uint64_t v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = T::value(w, i);
-      mid = fmaf(v, v, mid);
-    }
-  } else if (bits < kLow) {
+  for (int i = 0; i < 4; ++i) v[i] = pipe::pack2(T::value(w, 2 * i), T::value(w, 2 * i + 1));
+  if (bits < kHigh && (bits >= kLow || m == 0)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = T::value(w, i) * 0x1p80f;
-      low = fmaf(v, v, low);
-    }
+    for (int i = 0; i < 4; ++i) s.mid = pipe::fma2(v[i], v[i], s.mid);
   } else {
+    const bool up = bits < kLow;
+    const uint64_t f = up ? pipe::pack2(0x1p80f, 0x1p80f) : pipe::pack2(0x1p-80f, 0x1p-80f);
+    uint64_t q = up ? s.low : s.high;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = T::value(w, i) * 0x1p-80f;
-      high = fmaf(v, v, high);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t x = pipe::mul2(v[i], f);
+      q = pipe::fma2(x, x, q);
     }
+    (up ? s.low : s.high) = q;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ double piece_squares(const Tensor& t, int64_t at) {
-  rows::Span m{t.in, t.in + t.n * T::kBytes, 0, t.in_wide};
-  uint32_t w[kTurns][T::kWords];
+// The chunks of a piece that this thread takes: whole ones at 16-byte addresses, or any.
+template <typename T, int TURNS>
+__device__ __forceinline__ void load_piece(const Tensor& t, int64_t at,
+                                           uint32_t (&w)[TURNS][T::kWords]) {
+  const uint8_t* p = t.in + (at + int64_t(threadIdx.x) * 8) * T::kBytes;
+  if (t.in_wide && at + piece_of(TURNS) <= t.n) {
 #pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
+    for (int j = 0; j < TURNS; ++j)
+#pragma unroll
+      for (int i = 0; i < T::kWords / 4; ++i)
+        rows::ld16(p + j * (kThreads * 8 * T::kBytes) + 16 * i, w[j] + 4 * i);
+    return;
+  }
+  rows::Span m{t.in, t.in + t.n * T::kBytes, 0, t.in_wide};
+#pragma unroll
+  for (int j = 0; j < TURNS; ++j) {
     const int64_t k = at + (int64_t(j) * kThreads + threadIdx.x) * 8;
     rows::load8<T>(t.in + k * T::kBytes, t.n - k, m, w[j]);
   }
-  float mid = 0.0f, high = 0.0f, low = 0.0f;
+}
+
+// The pieces' sums of squares in a thread: two fp32 numbers, the second what the first's
+// additions rounded off (64-bit additions, a few a clock and SM, took as long as reading
+// a piece), and in 64 bits what was scaled.
+struct Total {
+  float sum = 0.0f, rest = 0.0f;
+  double scaled = 0.0;
+};
+
+template <typename T>
+__device__ __forceinline__ void piece_squares(const Tensor& t, int64_t at, Total& s) {
+  uint32_t w[kAddTurns][T::kWords];
+  load_piece<T, kAddTurns>(t, at, w);
+  Squares q;
 #pragma unroll
-  for (int j = 0; j < kTurns; ++j) add_squares<T>(w[j], mid, high, low);
-  double s = double(mid);
-  if (low != 0.0f) s += double(low) * 0x1p-160;
-  if (!(high == 0.0f)) s += double(high) * 0x1p160;
-  return s;
+  for (int j = 0; j < kAddTurns; ++j) add_squares<T>(w[j], q);
+  const float x = sum_of(q.mid), sum = s.sum + x, part = sum - s.sum;
+  s.rest += (s.sum - (sum - part)) + (x - part);
+  s.sum = sum;
+  const float low = sum_of(q.low), high = sum_of(q.high);
+  if (low != 0.0f) s.scaled += double(low) * 0x1p-160;
+  if (!(high == 0.0f)) s.scaled += double(high) * 0x1p160;
 }
 
 // Sum over the CTA, the same bits in every thread.
@@ -131,35 +168,53 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
   __shared__ double part[kThreads / 32];
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
-  double s = 0.0;
+  Total total;
+  int which = 0;
   for (uint32_t i = blockIdx.x; i < p.pieces; i += gridDim.x) {
-    const Tensor& t = p.t[tensor_of(p, i)];
-    const int64_t at = int64_t(i - t.first) * kPiece;
-    if (t.in_dtype == SWZ_BF16) s += piece_squares<rows::Bf16>(t, at);
-    else if (t.in_dtype == SWZ_F16) s += piece_squares<rows::F16>(t, at);
-    else s += piece_squares<rows::F32>(t, at);
+    which = tensor_of(p, i, which);
+    const Tensor& t = p.t[which];
+    const int64_t at = int64_t(i - t.first) * piece_of(kAddTurns);
+    if (t.in_dtype == SWZ_BF16) piece_squares<rows::Bf16>(t, at, total);
+    else if (t.in_dtype == SWZ_F16) piece_squares<rows::F16>(t, at, total);
+    else piece_squares<rows::F32>(t, at, total);
   }
-  s = block_sum(s, part);
+  const double s =
+      block_sum(double(total.sum) + double(total.rest) + total.scaled, part);
   if (threadIdx.x == 0) p.mine[blockIdx.x] = s;
 }
 
 template <typename T>
 __device__ __forceinline__ void scale_piece(const Tensor& t, int64_t at, float f) {
-  rows::Span m{t.in, t.in + t.n * T::kBytes, 0, t.in_wide};
+  uint32_t w[kScaleTurns][T::kWords];
+  load_piece<T, kScaleTurns>(t, at, w);
+  const uint64_t f2 = pipe::pack2(f, f);
   const int es = t.out_dtype == SWZ_F32 ? 4 : 2;
-  uint32_t w[kTurns][T::kWords];
+  uint8_t* p = t.out + (at + int64_t(threadIdx.x) * 8) * es;
+  const bool whole = t.out_wide && at + piece_of(kScaleTurns) <= t.n;
 #pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
-    const int64_t k = at + (int64_t(j) * kThreads + threadIdx.x) * 8;
-    rows::load8<T>(t.in + k * T::kBytes, t.n - k, m, w[j]);
-  }
+  for (int j = 0; j < kScaleTurns; ++j) {
+    uint64_t v[4];
 #pragma unroll
-  for (int j = 0; j < kTurns; ++j) {
-    const int64_t k = at + (int64_t(j) * kThreads + threadIdx.x) * 8;
+    for (int i = 0; i < 4; ++i)
+      v[i] = pipe::mul2(pipe::pack2(T::value(w[j], 2 * i), T::value(w[j], 2 * i + 1)), f2);
+    uint8_t* const to = p + int64_t(j) * (kThreads * 8) * es;
+    if (whole && t.out_dtype == SWZ_F32) {
+      reinterpret_cast<ulonglong2*>(to)[0] = make_ulonglong2(v[0], v[1]);
+      reinterpret_cast<ulonglong2*>(to)[1] = make_ulonglong2(v[2], v[3]);
+      continue;
+    }
     float o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = T::value(w[j], i) * f;
-    rows::store8(t.out + k * es, t.n - k, o, t.out_dtype, t.out_wide != 0);
+    for (int i = 0; i < 4; ++i) pipe::unpack2(v[i], o[2 * i], o[2 * i + 1]);
+    if (whole) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = rows::pack16(o[2 * i], o[2 * i + 1], t.out_dtype);
+      *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+      rows::store8(to, t.n - (at + (int64_t(j) * kThreads + threadIdx.x) * 8), o, t.out_dtype,
+                   t.out_wide != 0);
+    }
   }
 }
 
@@ -170,17 +225,25 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
   double s = 0.0;
   for (int i = int(threadIdx.x); i < p.part_count; i += kThreads) s += p.parts[i];
-  const double norm = sqrt(block_sum(s, part));
-  if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = float(norm);
-  // of the norm in 64 bits: one that fp32 cannot hold still clips.  A NaN stays one:
-  // the comparison is false.
-  const double den = norm + p.eps, quotient = den == 0.0 ? 1.0 : p.max_norm / den;
-  const float f = quotient > 1.0 ? 1.0f : float(quotient);
+  s = block_sum(s, part);
+  __shared__ float factor;
+  if (threadIdx.x == 0) {  // 64-bit roots and divisions are slow here: one thread's
+    const double norm = sqrt(s);
+    if (p.norm && blockIdx.x == 0) *p.norm = float(norm);
+    // of the norm in 64 bits: one that fp32 cannot hold still clips.  A NaN stays one:
+    // the comparison is false.
+    const double den = norm + p.eps, quotient = den == 0.0 ? 1.0 : p.max_norm / den;
+    factor = quotient > 1.0 ? 1.0f : float(quotient);
+  }
+  __syncthreads();
+  const float f = factor;
+  int which = p.count - 1;
   for (uint32_t j = blockIdx.x; j < p.pieces; j += gridDim.x) {
     const uint32_t i = p.pieces - 1 - j;
-    const Tensor& t = p.t[tensor_of(p, i)];
+    which = tensor_of(p, i, which);
+    const Tensor& t = p.t[which];
     if (f == 1.0f && t.in == t.out) continue;  // in place, nothing changes
-    const int64_t at = int64_t(i - t.first) * kPiece;
+    const int64_t at = int64_t(i - t.first) * piece_of(kScaleTurns);
     if (t.in_dtype == SWZ_BF16) scale_piece<rows::Bf16>(t, at, f);
     else if (t.in_dtype == SWZ_F16) scale_piece<rows::F16>(t, at, f);
     else scale_piece<rows::F32>(t, at, f);
@@ -233,7 +296,7 @@ static bool apart(const swz_grad* g, int count) {
 }
 
 template <int CAP>
-static void fill(Table<CAP>* p, const swz_grad* g, int from, int to, bool clip) {
+static void fill(Table<CAP>* p, const swz_grad* g, int from, int to, bool clip, int turns) {
   uint64_t pieces = 0;
   p->count = 0;
   for (int i = from; i < to; ++i) {
@@ -247,7 +310,7 @@ static void fill(Table<CAP>* p, const swz_grad* g, int from, int to, bool clip) 
     t.out_dtype = uint8_t(g[i].out_dtype);
     t.in_wide = aligned16(t.in);
     t.out_wide = aligned16(t.out);
-    pieces += uint64_t((g[i].n + kPiece - 1) / kPiece);
+    pieces += uint64_t((g[i].n + piece_of(turns) - 1) / piece_of(turns));
   }
   p->pieces = uint32_t(pieces);
 }
@@ -259,10 +322,10 @@ static int run(const swz_grad* g, int count, bool clip, double max_norm, double 
   p.parts = parts;
   p.max_norm = max_norm;
   p.eps = eps;
-  int blocks = num_sms * 4;
+  int blocks = num_sms * 8;
   if (blocks > kMaxBlocks) blocks = kMaxBlocks;
   for (int from = 0; from < count; from += CAP) {
-    fill(&p, g, from, std::min(count, from + CAP), clip);
+    fill(&p, g, from, std::min(count, from + CAP), clip, kAddTurns);
     if (p.count == 0) continue;
     p.mine = parts + p.part_count;
     const uint32_t grid = std::min(p.pieces, uint32_t(blocks));
@@ -273,7 +336,7 @@ static int run(const swz_grad* g, int count, bool clip, double max_norm, double 
   // the norm alone, or that of no elements, is one CTA's work
   p.norm = norm;
   for (int from = 0; clip && from < count; from += CAP) {
-    fill(&p, g, from, std::min(count, from + CAP), clip);
+    fill(&p, g, from, std::min(count, from + CAP), clip, kScaleTurns);
     if (p.count == 0) continue;
     const int rc = launch(scale_kernel<CAP>, std::min(p.pieces, uint32_t(blocks)), p, s);
     if (rc != SWZ_OK) return rc;
@@ -299,7 +362,7 @@ static int check_and_run(const swz_grad* g, int count, bool clip, double max_nor
     if (clip && (!g[i].out ||
                  reinterpret_cast<uintptr_t>(g[i].out) % uintptr_t(size_of(g[i].out_dtype))))
       return SWZ_EINVAL;
-    pieces += uint64_t((g[i].n + kPiece - 1) / kPiece);
+    pieces += uint64_t((g[i].n + piece_of(kScaleTurns) - 1) / piece_of(kScaleTurns));
     if (pieces > uint64_t(INT32_MAX)) return SWZ_EINVAL;
   }
   try {
