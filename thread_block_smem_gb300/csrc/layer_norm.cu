@@ -31,10 +31,11 @@ struct FwdArgs {
 };
 
 // NC chunks a thread; WARP: a row a warp, eight a CTA, otherwise a row the CTA; G: the
-// common case (layer_norm.cuh) or 0.
-template <typename T, int NC, bool WARP, int G>
-__global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
+// common case (layer_norm.cuh) or 0; MOST: threads of a CTA, at most.
+template <typename T, int NC, bool WARP, int G, int MOST>
+__global__ void __launch_bounds__(MOST, WARP ? 4 : MOST == 256 ? 3 : G && NC == 2 ? 1 : 2)
     layer_norm_kernel(const FwdArgs p) {
+  constexpr bool HOLD = G && NC == 2 && !WARP;  // weight and bias in registers
   __shared__ float2 part[2][16];
   __shared__ float counts[16];
   ptx::grid_dep_wait();
@@ -68,6 +69,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
   const int64_t step = int64_t(gridDim.x) * (WARP ? 8 : 1);
   int64_t row = WARP ? int64_t(blockIdx.x) * 8 + warp : int64_t(blockIdx.x);
   if (row < p.M) fetch(row);
+  uint64_t held[HOLD ? 2 * NC : 1][4];
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int k = (c * width + t) * 8;
+      fast_vec<T, G>(p.w.p, k < p.N ? k : 0, held[2 * c]);
+      fast_vec<T, G>(p.b.p, k < p.N ? k : 0, held[2 * c + 1]);
+    }
+  }
   for (uint32_t turn = 0; row < p.M; row += step, turn ^= 1u) {
     uint64_t v[NC][4], s2 = 0ull, q2 = 0ull;
 #pragma unroll
@@ -129,8 +139,16 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
       uint64_t g[4], b[4], o[4];
       if constexpr (G) {
         if (k >= p.N) continue;
-        fast_vec<T, G>(p.w.p, k, g);
-        fast_vec<T, G>(p.b.p, k, b);
+        if constexpr (HOLD) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g[i] = held[2 * c][i];
+            b[i] = held[2 * c + 1][i];
+          }
+        } else {
+          fast_vec<T, G>(p.w.p, k, g);
+          fast_vec<T, G>(p.b.p, k, b);
+        }
       } else {
         load_vec2(p.w, k, p.N, 1.0f, g);
         load_vec2(p.b, k, p.N, 0.0f, b);
@@ -199,40 +217,35 @@ __global__ void __launch_bounds__(512) long_layer_norm_kernel(const FwdArgs p) {
   }
 }
 
-template <typename T, int NC, bool WARP, int G>
+template <typename T, int NC, bool WARP, int G, int MOST>
 static int start_kind(const FwdArgs& a, int num_sms, cudaStream_t s) {
   const int threads = WARP ? 256 : threads_of(a.N, NC);
   int resident = 0;
-  const int rc = resident_ctas<layer_norm_kernel<T, NC, WARP, G>>(threads, &resident);
+  const int rc = resident_ctas<layer_norm_kernel<T, NC, WARP, G, MOST>>(threads, &resident);
   if (rc != SWZ_OK) return rc;
   const int64_t rows = WARP ? (int64_t(a.M) + 7) / 8 : int64_t(a.M);
   const int64_t most = int64_t(num_sms) * resident;
-  return launch(layer_norm_kernel<T, NC, WARP, G>, uint32_t(rows < most ? rows : most), uint32_t(threads), a, s);
+  return launch(layer_norm_kernel<T, NC, WARP, G, MOST>, uint32_t(rows < most ? rows : most), uint32_t(threads), a, s);
 }
 
-template <typename T, int NC, bool WARP>
+template <typename T, int NC, bool WARP, int MOST>
 static int start(const FwdArgs& a, int num_sms, cudaStream_t s) {
   const int g = kind_of<T>(a.w);
   if (g == 0 || g != kind_of<T>(a.b) || !a.x.wide || !a.y_wide || a.N % 8 != 0 ||
       a.y_dtype != code_of<T>())
-    return start_kind<T, NC, WARP, 0>(a, num_sms, s);
+    return start_kind<T, NC, WARP, 0, MOST>(a, num_sms, s);
   if constexpr (T::kBytes == 2)
-    if (g == 2) return start_kind<T, NC, WARP, 2>(a, num_sms, s);
-  return start_kind<T, NC, WARP, 1>(a, num_sms, s);
+    if (g == 2) return start_kind<T, NC, WARP, 2, MOST>(a, num_sms, s);
+  return start_kind<T, NC, WARP, 1, MOST>(a, num_sms, s);
 }
 
 template <typename T>
 static int dispatch(const FwdArgs& a, int num_sms, cudaStream_t s) {
-  if (a.N <= 256) return start<T, 1, true>(a, num_sms, s);
-  if (a.N <= 512) return start<T, 2, true>(a, num_sms, s);
-  // 64 registers a thread hold four chunks of 16-bit values and the next row's, or two of
-  // fp32
-  if constexpr (T::kBytes == 2) {
-    if (a.N <= 1024) return start<T, 4, true>(a, num_sms, s);
-  } else {
-    if (a.N <= 8192) return start<T, 2, false>(a, num_sms, s);
-  }
-  if (a.N <= 16384) return start<T, 4, false>(a, num_sms, s);
+  if (a.N <= 256) return start<T, 1, true, 256>(a, num_sms, s);
+  if (a.N <= 512) return start<T, 2, true, 256>(a, num_sms, s);
+  if (a.N <= 4096) return start<T, 2, false, 256>(a, num_sms, s);
+  if (a.N <= 8192) return start<T, 2, false, 512>(a, num_sms, s);
+  if (a.N <= 16384) return start<T, 4, false, 512>(a, num_sms, s);
   return launch(long_layer_norm_kernel<T>, uint32_t(a.M), 512, a, s);
 }
 
