@@ -186,6 +186,29 @@ def test_out(swz, dtype, n):
         assert torch.equal(v, want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [300, 1000, 1999, 4096, 9000, 17000])
+def test_gradient_over_its_inputs(swz, dtype, n):
+    """dx over x or over dy (C entry point): the same bits, dw and db among them."""
+    m = 70
+    x, w, _, dy = inputs(m, n, dtype, torch.float32)
+    code = {torch.bfloat16: swz.SWZ_BF16, torch.float16: swz.SWZ_F16, torch.float32: swz.SWZ_F32}[dtype]
+    _, mean, rstd = swz.layer_norm_forward(x, w)
+    want = swz.layer_norm_backward(dy, x, w, mean, rstd)
+    rc, need = swz.swz_layer_norm_backward_workspace_size(m, n)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for over in (0, 1):
+        a, b = x.clone(), dy.clone()
+        to = (a, b)[over]
+        dw, db = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        assert swz.swz_layer_norm_backward(
+            b.data_ptr(), code, n, a.data_ptr(), code, n, w.data_ptr(), swz.SWZ_F32, mean.data_ptr(),
+            rstd.data_ptr(), to.data_ptr(), code, n, dw.data_ptr(), db.data_ptr(), swz.SWZ_F32, m, n,
+            ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == swz.SWZ_OK
+        for got, exact in zip((to, dw, db), want):
+            assert torch.equal(got, exact)
+
+
 def test_empty(swz):
     w = torch.ones(16, device="cuda")
     y, mean, rstd = swz.layer_norm_forward(torch.empty((0, 16), device="cuda"), w)

@@ -319,19 +319,15 @@ static int dispatch(const BwdArgs& a, int* P, int num_sms, cudaStream_t s) {
   if (a.N <= 512) return start<X, D, 2, true>(a, P, num_sms, s);
   if (a.N <= 8192) return start<X, D, 2, false>(a, P, num_sms, s);
   if (a.N <= 16384) return start<X, D, 4, false>(a, P, num_sms, s);
-  if (a.dx) {
-    const int rc = launch(long_dx_kernel<X, D>, uint32_t(a.M), 512, a, s);
-    if (rc != SWZ_OK) return rc;
+  if (a.parts) {  // first: dx may lie over x or dy
+    *P = a.M < 64 ? a.M : 64;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(uint32_t((int64_t(a.N) + 255) / 256), uint32_t(*P));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, long_parts_kernel<X, D>, a));
   }
-  if (!a.parts) return SWZ_OK;
-  *P = a.M < 64 ? a.M : 64;
-  const dim3 grid(uint32_t((int64_t(a.N) + 255) / 256), uint32_t(*P));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  SWZ_CUDA_TRY(cudaLaunchKernelEx(&cfg, long_parts_kernel<X, D>, a));
-  return SWZ_OK;
+  return a.dx ? launch(long_dx_kernel<X, D>, uint32_t(a.M), 512, a, s) : int(SWZ_OK);
 }
 
 template <typename X>
