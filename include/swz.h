@@ -633,7 +633,7 @@ int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void*
 /* Options of swz_gemm_int8; NULL = serpentine order with strips of 8, the rest
  * zero. */
 typedef struct swz_gemm_int8_opts {
-  int order, group;     /* tile order as in swz_gemm                            */
+  int order, group;     /* tile order as in swz_gemm (tiles 128 and 256)        */
   int tile;             /* 0 automatic; 32: up to 32 rows of C, all of them in every
                            CTA; 64: 128 columns of C and up to 256 of its rows, B
                            widened on its way to the tensor core; 128: one CTA, 128 x
