@@ -623,9 +623,9 @@ int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes)
  *   q = x * r, the exact product, rounded to the nearest whole number, ties to
  *   even: -127 .. 127
  * A row of zeros gives zeros; one that holds an infinity or NaN gives zeros with
- * the scale NaN.  The bytes up to the next multiple of 8 of a row of q are written
- * too, with zeros.  M = 0: no-op; K = 0 writes the scales only.  Errors:
- * SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
+ * the scale NaN.  What lies beyond the last column of a row of q is left as it is.
+ * M = 0: no-op; K = 0 writes the scales only.  Errors: SWZ_EINVAL, SWZ_EARCH,
+ * SWZ_ECUDA.
  */
 int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void* q, int64_t ldq,
                       float* scales, void* stream);

@@ -73,6 +73,17 @@ def test_quantize(swz, dtype, m, k):
         assert torch.equal(q, want) and bits(s, ws)
 
 
+@pytest.mark.parametrize("k", [1, 7, 8, 13, 250, 1029, 4099, 16390])
+def test_quantize_leaves_what_is_beside(swz, k):
+    m, ld = 3, (k + 15) // 16 * 16 + 16
+    x = torch.randn((m, k), generator=gen(k), device="cuda")
+    q = torch.full((m, ld), 99, dtype=torch.int8, device="cuda")
+    s = torch.empty(m, device="cuda")
+    assert swz.swz_quantize_int8(x.data_ptr(), swz.SWZ_F32, k, m, k, q.data_ptr(), ld, s.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream) == swz.SWZ_OK
+    assert torch.equal(q[:, :k], exact_q(x)[0]) and (q[:, k:] == 99).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_quantize_values(swz, dtype):
     """Ties, the largest and smallest magnitudes, zeros, infinities and NaN."""

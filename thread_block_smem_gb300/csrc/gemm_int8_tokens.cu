@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
         uint32_t w[X::kWords];
         rows::load8<X>(p.x.base + t * p.x.ld + int64_t(c) * 8 * X::kBytes,
                        t < p.M ? p.K - c * 8 : 0, p.x, w);
-        store_q<X, false>(xq + t * pitch + c * 8, w, r, bad);
+        store_q<X, false>(xq + t * pitch + c * 8, 8, w, r, bad);
       }
     }
   }

@@ -76,9 +76,10 @@ __device__ __forceinline__ uint32_t chunk_max(const uint32_t* w) {
   return m;
 }
 
-// eight values to q at p: bytes, or fp16 numbers of the same values
+// eight values to q at p: the first n as bytes, or all as fp16 numbers of the same values
 template <typename T, bool HALF>
-__device__ __forceinline__ void store_q(uint8_t* p, const uint32_t* w, float r, bool bad) {
+__device__ __forceinline__ void store_q(uint8_t* p, int64_t n, const uint32_t* w, float r,
+                                        bool bad) {
   constexpr float kMagic = 12582912.0f;  // 1.5 2^23
   uint32_t b[8];
 #pragma unroll
@@ -99,7 +100,13 @@ __device__ __forceinline__ void store_q(uint8_t* p, const uint32_t* w, float r, 
     for (int i = 0; i < 2; ++i)
       o[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
                          __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
-    *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+    if (n >= 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+    } else {
+      uint64_t v = (uint64_t(o[1]) << 32) | o[0];
+#pragma unroll 1
+      for (int i = 0; i < int(n); ++i, v >>= 8) p[i] = uint8_t(v);
+    }
   }
 }
 

@@ -75,12 +75,12 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) quantize_int8_kernel(co
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int64_t k = (int64_t(c) * TPR + t) * 8;
-      if (k < p.K) store_q<T, HALF>(q + k * QB, w[c], r, bad);
+      if (k < p.K) store_q<T, HALF>(q + k * QB, p.K - k, w[c], r, bad);
     }
   } else {
     for (int64_t c = t; c < chunks; c += TPR) {
       rows::load8<T>(x + c * 8 * T::kBytes, p.K - c * 8, p.x, w[0]);
-      store_q<T, HALF>(q + c * 8 * QB, w[0], r, bad);
+      store_q<T, HALF>(q + c * 8 * QB, p.K - c * 8, w[0], r, bad);
     }
   }
 }
