@@ -82,38 +82,50 @@ struct WidenArgs {
   int64_t ldo;  // bytes
   int rows[2];
   int K;
-  uint32_t pieces;  // of 16 values, a row
 };
 
-// Two matrices (either may be empty) of bytes to fp16, 16 values a thread and turn.
+// Two matrices (either may be empty) of bytes to fp16: a warp takes a row at a time, four
+// pieces of 16 values a lane under way together.
 __global__ void __launch_bounds__(256) widen_kernel(const WidenArgs p) {
+  constexpr int kAhead = 4;
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
-  const uint64_t first = uint64_t(p.rows[0]) * p.pieces;
-  const uint64_t total = first + uint64_t(p.rows[1]) * p.pieces;
-  for (uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += uint64_t(gridDim.x) * 256) {
-    const int which = i >= first;
-    const uint64_t j = which ? i - first : i;
-    const uint64_t row = j / p.pieces;
-    const int k = int(j - row * p.pieces) * 16;
-    const uint8_t* src = p.in[which] + int64_t(row) * p.ld[which] + k;
-    uint32_t b[4];
-    if (k + 16 <= p.K) {
-      rows::ld16(src, b);
-    } else {
+  const int lane = int(threadIdx.x % 32);
+  const int64_t last = int64_t(p.rows[0]) + p.rows[1];
+  for (int64_t r = int64_t(blockIdx.x) * 8 + threadIdx.x / 32; r < last;
+       r += int64_t(gridDim.x) * 8) {
+    const int which = r >= p.rows[0];
+    const int64_t row = which ? r - p.rows[0] : r;
+    const uint8_t* src = p.in[which] + row * p.ld[which];
+    uint8_t* dst = p.out[which] + row * p.ldo;
+    for (int k0 = lane * 16; k0 - lane * 16 < p.K; k0 += kAhead * 512) {
+      uint32_t b[kAhead][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = 0u;
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j * 512;
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (k + e < p.K) b[e / 4] |= uint32_t(src[e]) << (8 * (e & 3));
+        for (int e = 0; e < 4; ++e) b[j][e] = 0u;
+        if (k + 16 <= p.K) rows::ld16_once(src + k, b[j]);
+        else if (k < p.K) {
+          const uint4 v = load_bytes(src + k, 0, p.K - k, true);
+          b[j][0] = v.x;
+          b[j][1] = v.y;
+          b[j][2] = v.z;
+          b[j][3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int k = k0 + j * 512;
+        if (k >= p.K) continue;
+        uint32_t o[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) widen4(b[j][e], o[2 * e], o[2 * e + 1]);
+        uint4* to = reinterpret_cast<uint4*>(dst + int64_t(k) * 2);
+        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
-    uint32_t o[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) widen4(b[e], o[2 * e], o[2 * e + 1]);
-    uint4* dst = reinterpret_cast<uint4*>(p.out[which] + int64_t(row) * p.ldo + int64_t(k) * 2);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -512,8 +524,8 @@ static int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& pr
 }
 
 static int launch_widen(const WidenArgs& a, int num_sms, cudaStream_t stream) {
-  const uint64_t total = (uint64_t(a.rows[0]) + uint64_t(a.rows[1])) * a.pieces;
-  const uint64_t blocks = (total + 255) / 256, cap = uint64_t(num_sms) * 8;
+  const uint64_t blocks = (uint64_t(a.rows[0]) + uint64_t(a.rows[1]) + 7) / 8;
+  const uint64_t cap = uint64_t(num_sms) * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(blocks < cap ? blocks : cap));
   cfg.blockDim = dim3(256);
@@ -680,7 +692,6 @@ static int widen(const void* A, int64_t lda, int M, const void* B, int64_t ldb, 
   w.rows[0] = A ? M : 0;
   w.rows[1] = B ? N : 0;
   w.K = K;
-  w.pieces = uint32_t(ceil_div(uint64_t(K), 16));
   return launch_widen(w, num_sms, s);
 }
 
