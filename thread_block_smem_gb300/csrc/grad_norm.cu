@@ -9,14 +9,19 @@
 //
 // Sums: a piece's squares are added in fp32 by each thread (64 of them, two sums of
 // 32), a thread's pieces in two fp32 numbers, everything above in 64 bits, in an order
-// that depends on the sizes alone.  Squares leave
-// fp32's range long before the gradients do, so eight values at a time whose largest
-// magnitude is not within 2^-40 .. 2^50 are squared after a multiplication by 2^80
-// or 2^-80 and kept apart.
+// that depends on the sizes alone.  Squares leave fp32's range long before the
+// gradients do, so eight values at a time whose largest magnitude is not within
+// 2^-40 .. 2^50 are squared after a multiplication by 2^80 or 2^-80 and kept apart.
 //
 // Bound: memory: every gradient is read for the norm, read again and written.  The
 // second pass takes the pieces in the opposite order, so that what the first one read
 // last is still in L2.
+//
+// Measured: 671 M bf16 into fp32 837 us (792 at the copy bandwidth, 594 with one read),
+// the norm alone 207 (198); 33.6 M 65 (40); 1.2 M fp32 8.3 (1.5: two launches).  With a
+// thread's pieces added in 64 bits, of which the SM does a few a clock, the norm took
+// 284 us; pieces of two chunks a thread instead of eight 498; the second pass with eight
+// instead of four 894.
 #include <algorithm>
 #include <vector>
 

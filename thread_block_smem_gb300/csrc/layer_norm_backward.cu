@@ -9,10 +9,17 @@
 // thread the same columns of each of them, so that its parts of dw and db stay in
 // registers; the P partial rows go to the workspace and a second kernel adds them in
 // order (deterministic, no atomics).  The next row's loads are under way while this
-// one's two sums cross the CTA; w comes from L1, where x and dy leave it alone.  As many threads as the row asks for, each with NC
-// chunks of eight columns.  P is a quarter of the rows at most, or one a SM, since each
-// partial row costs as much as two thirds of a row of bf16 inputs.  Rows longer than
-// 16384 take dx and the partial sums in two kernels that read both inputs again.
+// one's two sums cross the CTA; w comes from L1, where x and dy leave it alone.  As many
+// threads as the row asks for, each with NC chunks of eight columns.  P is a quarter of
+// the rows at most, or one an SM, since a partial row is 16 bytes a column, written and
+// read, and a row of bf16 inputs and result 6.  Rows longer than 16384 take the partial
+// sums and dx in two kernels that both read the inputs.
+//
+// Measured: 8192 x 4096 bf16 41.3 us (29.7 at the copy bandwidth; 35 without dw and db),
+// fp32 68.5 (59.4), 16384 x 1000 bf16 26.9 (14.5), 4096 x 10240 92 (37, four chunks a
+// thread), 1001 x 600 fp32 7.8 (1.1), 1001 x 1999 fp16 22 (1.8).  With three CTAs an SM
+// instead of two and a row's values worked out twice for it 52 us; an element an
+// instruction 45.
 #include <algorithm>
 #include <type_traits>
 
