@@ -288,3 +288,24 @@ def test_timeout_is_reported(swz):
             swz.check_status()
         assert bits(swz.gemm_int8(a, sa, b, sb, **kw), exact_c(a, sa, b, sb, torch.bfloat16))
         swz.check_status()
+
+
+def test_two_streams_at_once(swz):
+    """Calls of every form under way on two streams together, each with its own workspace."""
+    n, k = 1000, 1500
+    qw, sw = swz.quantize_int8(torch.randn((n, k), generator=gen(1), device="cuda"))
+    xs = [torch.randn((m, k), generator=gen(m), device="cuda").bfloat16() for m in (1, 2, 20, 60, 200, 700)]
+    want = [exact_c(*exact_q(x), qw, sw, torch.bfloat16) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i in range(len(xs)):
+            for j, s in enumerate(streams):
+                at = (i + 3 * j) % len(xs)  # different forms on the two
+                with torch.cuda.stream(s):
+                    got[j].append((at, swz.linear_int8(xs[at], qw, sw)))
+    torch.cuda.synchronize()
+    swz.check_status()
+    for results in got:
+        assert all(bits(y, want[at]) for at, y in results)
