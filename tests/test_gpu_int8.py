@@ -309,3 +309,13 @@ def test_two_streams_at_once(swz):
     swz.check_status()
     for results in got:
         assert all(bits(y, want[at]) for at, y in results)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 5000), (1300, 9, 2048), (7, 5, 131071), (2000, 3000, 4100)])
+def test_wide_form(swz, m, n, k):
+    """Rows of several parts, of one value more than whole ones, and more rows than warps."""
+    a, sa = int8_rows(swz, m, k, 11)
+    b, sb = int8_rows(swz, n, k, 12)
+    want = exact_c(a, sa, b, sb, torch.float32)
+    for tile in (128, 256):
+        assert bits(swz.gemm_int8(a, sa, b, sb, tile=tile, out_dtype=torch.float32), want)

@@ -22,9 +22,10 @@
 //     tile's K and adds the partial tiles through distributed shared memory.
 //   * Tiles are dealt out by the framework's tile orders, w = cluster + i P.
 //
-// Measured, both passes: 8192^3, bf16 result, 593 us (1.85 PFLOP/s), of which the pass
-// that widens (134 MB read, 268 MB written) about 45; 8192 x 4096 x 4096 175 us; 1000
-// rows of 4096 x 4096 45.  Bound: the tensor cores (pipe 85 % busy at 8192 x 4096 x
+// Measured, both passes: 8192^3, bf16 result, 593 to 618 us over boxes (1.8 PFLOP/s), of
+// which the pass that widens (134 MB read, 268 MB written) about 50; 8192 x 4096 x 4096
+// 175 us; 1000 rows of 4096 x 4096 41.  Widening whole rows a warp took 610 us where
+// parts of 2048 took 618, but 183 and 45 of the other two.  Bound: the tensor cores (pipe 85 % busy at 8192 x 4096 x
 // 4096).
 #include <cuda.h>
 
@@ -80,6 +81,7 @@ struct Params {
 };
 
 // ---- widening -------------------------------------------------------------------
+constexpr int kPart = 2048;  // values of a row that a warp widens at a time
 struct WidenArgs {
   const uint8_t* in[2];
   int64_t ld[2];  // bytes
@@ -89,47 +91,56 @@ struct WidenArgs {
   int K;
 };
 
-// Two matrices (either may be empty) of bytes to fp16: a warp takes a row at a time, four
-// pieces of 16 values a lane under way together.
+// Two matrices (either may be empty) of bytes to fp16: a warp takes 2048 values of a row at
+// a time, four pieces of 16 a lane under way together.
 __global__ void __launch_bounds__(256) widen_kernel(const WidenArgs p) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = kPart / 512;
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
   const int lane = int(threadIdx.x % 32);
   const int64_t last = int64_t(p.rows[0]) + p.rows[1];
-  for (int64_t r = int64_t(blockIdx.x) * 8 + threadIdx.x / 32; r < last;
-       r += int64_t(gridDim.x) * 8) {
+  // the warp's row and part of it, and how far the next ones are
+  const int parts = (p.K + kPart - 1) / kPart;
+  const int64_t at = int64_t(blockIdx.x) * 8 + threadIdx.x / 32, far = int64_t(gridDim.x) * 8;
+  const int64_t far_rows = far / parts;
+  const int far_parts = int(far % parts);
+  int64_t r = at / parts;
+  int part = int(at % parts);
+  for (; r < last; r += far_rows, part += far_parts) {
+    if (part >= parts) {
+      part -= parts;
+      if (++r >= last) break;
+    }
     const int which = r >= p.rows[0];
     const int64_t row = which ? r - p.rows[0] : r;
     const uint8_t* src = p.in[which] + row * p.ld[which];
     uint8_t* dst = p.out[which] + row * p.ldo;
-    for (int k0 = lane * 16; k0 - lane * 16 < p.K; k0 += kAhead * 512) {
-      uint32_t b[kAhead][4];
+    const int k0 = part * kPart + lane * 16;
+    uint32_t b[kAhead][4];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int k = k0 + j * 512;
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j * 512;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b[j][e] = 0u;
-        if (k + 16 <= p.K) rows::ld16_once(src + k, b[j]);
-        else if (k < p.K) {
-          const uint4 v = load_bytes(src + k, 0, p.K - k, true);
-          b[j][0] = v.x;
-          b[j][1] = v.y;
-          b[j][2] = v.z;
-          b[j][3] = v.w;
-        }
+      for (int e = 0; e < 4; ++e) b[j][e] = 0u;
+      if (k + 16 <= p.K) rows::ld16_once(src + k, b[j]);
+      else if (k < p.K) {
+        const uint4 v = load_bytes(src + k, 0, p.K - k, true);
+        b[j][0] = v.x;
+        b[j][1] = v.y;
+        b[j][2] = v.z;
+        b[j][3] = v.w;
       }
+    }
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int k = k0 + j * 512;
-        if (k >= p.K) continue;
-        uint32_t o[8];
+    for (int j = 0; j < kAhead; ++j) {
+      const int k = k0 + j * 512;
+      if (k >= p.K) continue;
+      uint32_t o[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) widen4(b[j][e], o[2 * e], o[2 * e + 1]);
-        uint4* to = reinterpret_cast<uint4*>(dst + int64_t(k) * 2);
-        to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        to[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      }
+      for (int e = 0; e < 4; ++e) widen4(b[j][e], o[2 * e], o[2 * e + 1]);
+      uint4* to = reinterpret_cast<uint4*>(dst + int64_t(k) * 2);
+      to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      to[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
   }
 }
@@ -529,7 +540,8 @@ static int launch(const CUtensorMap& ta, const CUtensorMap& tb, const Params& pr
 }
 
 static int launch_widen(const WidenArgs& a, int num_sms, cudaStream_t stream) {
-  const uint64_t blocks = (uint64_t(a.rows[0]) + uint64_t(a.rows[1]) + 7) / 8;
+  const uint64_t parts = (uint64_t(a.K) + kPart - 1) / kPart;
+  const uint64_t blocks = ((uint64_t(a.rows[0]) + uint64_t(a.rows[1])) * parts + 7) / 8;
   const uint64_t cap = uint64_t(num_sms) * 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(blocks < cap ? blocks : cap));

@@ -25,7 +25,8 @@
 // Measured, in a stream of them, with the pass that widens A, B from memory: 64 rows
 // of 4096 x 4096 14.0 us, 128 rows 14.8, 256 rows 18.6 (24 to 34 where all of B is
 // widened to memory first), of 10240 x 4096 25, 32 and 49 (49 to 56), of 8192 x 8192
-// 26, 33 and 49 (77 to 92).  A block of 128 of K takes a CTA 0.65 us, several times its
+// 26, 33 and 49 (77 to 92).  The layer with 512 rows of 4096 x 4096 27 us (37), of 2048 x
+// 2048 15 (18), of 10240 x 4096 73 (83), of 8192 x 8192 97 (96): 512 rows are the most.  A block of 128 of K takes a CTA 0.65 us, several times its
 // MMAs: the way through widening, fence, MMA and release of a stage, of which two or
 // three are in turn.
 #include <mutex>
@@ -381,9 +382,12 @@ BatchPlan batch_plan(int M, int N, int K, int split, int num_sms) {
   auto columns = [&](uint32_t s) { return div_up(2 * div_up(kb, s), kHalvesOfSum) * b.nb; };
   uint32_t s = split ? uint32_t(split) : 1;
   if (!split)
-    // as many CTAs as stay resident, each with a block of K at least
+    // As many CTAs as stay resident, each with a block of K at least.  Clusters of 4 and 8
+    // leave some SMs of a group over: 16 clusters of 8 do not fit one CTA an SM (400 rows of
+    // 1024 x 8192, 16 tiles: 31.5 us by eight, 24.3 by four).
     while (s < 8 && (columns(s) > most ||
-                     (tiles * s * 2 <= uint64_t(num_sms) * b.ctas_per_sm && kb >= 2 * s)))
+                     (tiles * s * 2 <= uint64_t(num_sms) * b.ctas_per_sm * (s == 4 ? 6 : s == 2 ? 7 : 8) / 8 &&
+                      kb >= 2 * s)))
       s *= 2;
   if (s > kb || columns(s) > most) return b;
   b.split = s;

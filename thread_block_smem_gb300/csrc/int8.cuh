@@ -40,7 +40,7 @@ int gemm_int8_rows(const void* A, int64_t lda, const float* sa, const void* B, i
 // The product of a few to some hundred rows of A, given as fp16 numbers (rows of `ld`
 // elements, written by the kernel that the same call launched before), with B as
 // bytes; arguments checked by the caller.
-constexpr int kBatchRows = 256;
+constexpr int kBatchRows = 512;
 struct BatchPlan {
   uint32_t tiles_m, nb, ctas_per_sm, stages, slots, split, tmem_cols;  // split 0: not for it
   uint64_t tiles;
