@@ -64,8 +64,10 @@ def test_gemm_checks(swz):
     for bad in ((-1, 5, 64), (5, -1, 64), (5, 5, -1), (5, 5, 131072), (2 ** 32 + 5, 5, 64)):
         assert swz.swz_gemm_int8_workspace_size(*bad)[0] == E
         assert swz.swz_linear_int8_workspace_size(*bad)[0] == E
-    # fp16 copies of both operands at most, in rows of whole lines
-    assert swz.swz_gemm_int8_workspace_size(500, 300, 70) == (0, 800 * 128 * 2)
+    # by rows of A: nothing, A as fp16 in rows of whole lines, both operands
+    for m, need in ((1, 0), (2, 0), (3, 0), (32, 0), (33, 33), (512, 512), (513, 513 + 300)):
+        assert swz.swz_gemm_int8_workspace_size(m, 300, 70) == (0, need * 128 * 2), m
+    assert swz.swz_gemm_int8_workspace_size(500, 300, 70, 128) == (0, 800 * 128 * 2)
 
 
 def test_linear_checks(swz):
