@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) quantize_int8_kernel(co
   const uint8_t* x = p.x.base + row * p.x.ld;
   uint32_t w[NC ? NC : 1][T::kWords];
   uint32_t m = 0;
-  const int chunks = (p.K + 7) / 8;
+  const int64_t chunks = (int64_t(p.K) + 7) / 8;
   if constexpr (NC > 0) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
