@@ -652,9 +652,11 @@ typedef struct swz_gemm_int8_opts {
  * exact; it is rounded to fp32 and multiplied by sa * sb, which is rounded to
  * fp32, and the product is rounded to fp32 and to C's type.  K up to 131071, so
  * that the sum fits 32 bits; any M, N >= 0 (K = 0 writes zeros).
+ * C must not lie over A, B or their scales (SWZ_EINVAL).
  * d_workspace: 16-byte aligned device scratch of at least
- * swz_gemm_int8_workspace_size bytes (of the same sizes and tile), contents free before and after; calls that
- * share it must not overlap; NULL when the size is 0.  Errors: SWZ_EINVAL,
+ * swz_gemm_int8_workspace_size bytes (of the same sizes and tile), contents free
+ * before and after; calls that share it must not overlap; NULL when the size is
+ * 0.  Errors: SWZ_EINVAL,
  * SWZ_ENOTBIJECTIVE, SWZ_EUNSUPPORTED (unknown tile or split, a split of more
  * parts than blocks of K or of one or two rows, tile 32 with more rows, tile 64
  * where K is longer than its accumulators have room for), SWZ_EARCH, SWZ_ECUDA.
@@ -668,8 +670,11 @@ int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_byte
 /*
  * swz_linear_int8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is
  * quantised by rows as in swz_quantize_int8 and multiplied by W (N x K; 8-bit
- * integers with the scales sw) as in swz_gemm_int8.  d_workspace: as there, of
- * swz_linear_int8_workspace_size bytes.  Errors: as swz_gemm_int8.
+ * integers with the scales sw) as in swz_gemm_int8.  y may lie over x in any way,
+ * not over W or sw (SWZ_EINVAL).  d_workspace: as there, of
+ * swz_linear_int8_workspace_size bytes; with one or two rows of x and y over it, of
+ * at least 256 + M * (K rounded up to a multiple of 16) bytes.  Errors: as
+ * swz_gemm_int8.
  */
 int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void* W, int64_t ldw,
                     const float* sw, void* y, int64_t ldy, int y_dtype, int M, int N, int K,

@@ -60,6 +60,35 @@ int die_of_sms(int num_sms, std::vector<uint8_t>* die_of_sm);
 // `cluster` with `threads` threads and `smem` bytes of dynamic shared memory.
 int placement(int cluster, int threads, int smem, int grid, std::vector<uint32_t>* sm_of_cta);
 
+// `rows` rows of `width` bytes, `ld` bytes apart (at least `width` where there are
+// several).
+struct RowsInMemory {
+  const void* p;
+  int64_t rows, ld, width;
+};
+
+// Whether two of them have a byte in common.  Rows that lie between the other's rows (the
+// halves of one buffer's columns) have none.
+inline bool rows_meet(const RowsInMemory& x, const RowsInMemory& y) {
+  if (x.rows <= 0 || y.rows <= 0 || x.width <= 0 || y.width <= 0) return false;
+  const RowsInMemory &a = x.rows <= y.rows ? x : y, &b = x.rows <= y.rows ? y : x;
+  const int64_t a0 = int64_t(reinterpret_cast<uintptr_t>(a.p));
+  const int64_t b0 = int64_t(reinterpret_cast<uintptr_t>(b.p));
+  if (a0 >= b0 + (b.rows - 1) * b.ld + b.width || b0 >= a0 + (a.rows - 1) * a.ld + a.width)
+    return false;
+  // where both have their rows equally far apart, a's first and last row meet what any does
+  const int64_t step = a.rows > 1 && a.ld == b.ld ? a.rows - 1 : 1;
+  for (int64_t i = 0; i < a.rows; i += step) {
+    const int64_t from = a0 + i * a.ld, to = from + a.width;
+    if (to <= b0) continue;
+    // the last row of b that starts before this one ends
+    int64_t j = b.rows > 1 ? (to - 1 - b0) / b.ld : 0;
+    if (j > b.rows - 1) j = b.rows - 1;
+    if (b0 + j * b.ld + b.width > from) return true;
+  }
+  return false;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 

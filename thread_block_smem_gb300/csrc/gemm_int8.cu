@@ -687,6 +687,21 @@ static bool result_ok(const void* C, int64_t ldc, int c_dtype, int M, int N) {
   return C && reinterpret_cast<uintptr_t>(C) % es == 0 && (M <= 1 || ldc >= N);
 }
 
+static RowsInMemory matrix_at(const void* p, int64_t rows, int64_t ld, int64_t width) {
+  return RowsInMemory{p, rows, rows > 1 ? ld : width, width};
+}
+static RowsInMemory result_at(const void* C, int64_t ldc, int c_dtype, int M, int N) {
+  const int64_t es = c_dtype == SWZ_F32 ? 4 : 2;
+  return matrix_at(C, M, ldc * es, int64_t(N) * es);
+}
+
+// Whether a result lies over 8-bit rows or their scales, which are read while it is written.
+static bool over_int8_rows(const RowsInMemory& C, const void* data, int64_t ld, const float* scales,
+                           int rows, int K) {
+  return rows_meet(C, matrix_at(data, rows, ld, K)) ||
+         rows_meet(C, matrix_at(scales, 1, 0, int64_t(rows) * 4));
+}
+
 static bool float_type(int d) { return d == SWZ_F16 || d == SWZ_BF16 || d == SWZ_F32; }
 
 }  // namespace i8
@@ -734,6 +749,9 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   if (M == 0 || N == 0) return SWZ_OK;
   if (!result_ok(C, ldc, c_dtype, M, N)) return SWZ_EINVAL;
   if (K > 0 && (!int8_rows_ok(A, lda, sa, K) || !int8_rows_ok(B, ldb, sb, K))) return SWZ_EINVAL;
+  const RowsInMemory result = result_at(C, ldc, c_dtype, M, N);
+  if (K > 0 && (over_int8_rows(result, A, lda, sa, M, K) || over_int8_rows(result, B, ldb, sb, N, K)))
+    return SWZ_EINVAL;
   const Form f = form_of(M, N, K, o.tile);
   if ((f == kTokenForm && o.split_k > 1) || (f == kRingForm && M > kRingRows))
     return SWZ_EUNSUPPORTED;
@@ -766,13 +784,14 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
                  s);
 }
 
-// workspace of the layer: the scales of x, then x as bytes (few tokens too long to be
-// quantised by every CTA) or what the product has
+// workspace of the layer: the scales of x, then x as bytes (few tokens that not every CTA
+// quantises itself) or what the product has
 static uint64_t linear_scales_bytes(int M) { return (uint64_t(M) * 4 + 255) & ~uint64_t(255); }
 static int64_t bytes_ld(int K) { return (int64_t(K) + 15) / 16 * 16; }
-static uint64_t linear_bytes(Form f, int M, int N, int K) {
+static uint64_t linear_bytes(Form f, bool fused, int M, int N, int K) {
+  if (fused) return 0;
   if (f == kTokenForm || f == kRingForm)
-    return f == kTokenForm && tokens_fused(M, K) ? 0 : linear_scales_bytes(M) + uint64_t(M) * uint64_t(bytes_ld(K));
+    return linear_scales_bytes(M) + uint64_t(M) * uint64_t(bytes_ld(K));
   return linear_scales_bytes(M) + gemm_bytes(f, M, N, K);
 }
 
@@ -780,7 +799,8 @@ extern "C" int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_b
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
   if (M == 0 || N == 0 || K == 0) return SWZ_OK;
-  *h_bytes = linear_bytes(form_of(M, N, K, 0), M, N, K);
+  const Form f = form_of(M, N, K, 0);
+  *h_bytes = linear_bytes(f, f == kTokenForm && tokens_fused(M, K), M, N, K);
   return SWZ_OK;
 }
 
@@ -795,8 +815,13 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   if (K > 0 && (!x || reinterpret_cast<uintptr_t>(x) % es != 0 || (M > 1 && ldx < K) ||
                 !int8_rows_ok(W, ldw, sw, K)))
     return SWZ_EINVAL;
+  const RowsInMemory result = result_at(y, ldy, y_dtype, M, N);
+  if (K > 0 && over_int8_rows(result, W, ldw, sw, N, K)) return SWZ_EINVAL;
   const Form f = form_of(M, N, K, 0);
-  const uint64_t need = K > 0 ? linear_bytes(f, M, N, K) : 0;
+  // where every CTA quantises x itself, y must not be written over it
+  const bool fused = f == kTokenForm && tokens_fused(M, K) &&
+                     !rows_meet(result, matrix_at(x, M, ldx * int64_t(es), int64_t(K) * int64_t(es)));
+  const uint64_t need = K > 0 ? linear_bytes(f, fused, M, N, K) : 0;
   uint8_t* ws = static_cast<uint8_t*>(d_workspace);
   if (need && (!ws || !aligned16(ws) || workspace_bytes < need)) return SWZ_EINVAL;
   DeviceInfo dev{};
@@ -805,7 +830,7 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ldy = M > 1 ? ldy : N;
   if (K == 0) return zero_result(y, ldy, y_dtype, M, N, s);
-  if (f == kTokenForm && tokens_fused(M, K))
+  if (fused)
     return gemm_int8_tokens(nullptr, 0, nullptr, x, dtype, ldx, W, ldw, sw, y, ldy, y_dtype, M, N,
                             K, dev.num_sms, s);
   float* sx = reinterpret_cast<float*>(ws);

@@ -107,6 +107,13 @@ def _matrix(q, scales, what):
     return at, ld, scales.data_ptr(), m, k
 
 
+def _ranges_meet(a, rows_a, ld_a, cols_a, b, rows_b, ld_b, cols_b):
+    """Whether the memory from a's first value to its last and b's have a byte in common."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return (a0 < b0 + ((rows_b - 1) * ld_b + cols_b) * b.element_size() and
+            b0 < a0 + ((rows_a - 1) * ld_a + cols_a) * a.element_size())
+
+
 def quantize_int8(x, *, stream=None):
     """(q, scales) of x (M x K; fp16, bf16 or fp32, contiguous rows), a scale for
     each row.  For a row with largest magnitude amax: ac = max(amax, 2^-96),
@@ -167,8 +174,9 @@ def gemm_int8(a, sa, b, sb, *, out=None, out_dtype=None, order="serpentine", gro
 
 def linear_int8(x, qw, sw, *, out=None, out_dtype=None, stream=None):
     """y = x W^T (M x N): x (M x K; fp16, bf16 or fp32) is quantised by rows as in
-    ``quantize_int8`` and multiplied by W (N x K) kept as (qw, sw).  ``out`` or
-    ``out_dtype`` (default: x's type)."""
+    ``quantize_int8`` and multiplied by W (N x K) kept as (qw, sw).  ``out`` (may lie
+    over x in any way; over qw or sw it is refused) or ``out_dtype`` (default: x's
+    type)."""
     if _lin.torch is None:
         _lin._init()
     _lin._here(x, qw, sw, out)
@@ -184,6 +192,8 @@ def linear_int8(x, qw, sw, *, out=None, out_dtype=None, stream=None):
     rc = _lin._L.swz_linear_int8_workspace_size(M, N, K, need)
     if rc == 0:
         need = need.value
+        if need == 0 and out is not None and M and _ranges_meet(x, M, ldx, K, out, M, ldy, N):
+            need = 256 + M * ((K + 15) // 16 * 16)  # x is quantised before out is written
         ws = _lin._empty(need, _lin.torch.uint8, x, stream) if need else None
         rc = _lin._L.swz_linear_int8(x.data_ptr(), code, ldx, pw, ldw, psw, y.data_ptr(), ldy, ycode,
                                      M, N, K, ws.data_ptr() if need else None, need,
