@@ -654,9 +654,9 @@ typedef struct swz_gemm_int8_opts {
  * that the sum fits 32 bits; any M, N >= 0 (K = 0 writes zeros).
  * C must not lie over A, B or their scales (SWZ_EINVAL).
  * d_workspace: 16-byte aligned device scratch of at least
- * swz_gemm_int8_workspace_size bytes (of the same sizes and tile), contents free
- * before and after; calls that share it must not overlap; NULL when the size is
- * 0.  Errors: SWZ_EINVAL,
+ * swz_gemm_int8_workspace_size_ex bytes (of the same sizes and options; without _ex:
+ * of a tile and no split of its own), contents free before and after; calls that
+ * share it must not overlap; NULL when the size is 0.  Errors: SWZ_EINVAL,
  * SWZ_ENOTBIJECTIVE, SWZ_EUNSUPPORTED (unknown tile or split, a split of more
  * parts than blocks of K or of one or two rows, tile 32 with more rows, tile 64
  * where K is longer than its accumulators have room for), SWZ_EARCH, SWZ_ECUDA.
@@ -666,6 +666,8 @@ int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const void* B, in
                   const swz_gemm_int8_opts* opts, void* d_workspace, uint64_t workspace_bytes,
                   void* stream);
 int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes);
+int swz_gemm_int8_workspace_size_ex(int M, int N, int K, const swz_gemm_int8_opts* opts,
+                                    uint64_t* h_bytes);
 
 /*
  * swz_linear_int8 -- y = x * W^T: x (M x K; SWZ_F16, SWZ_BF16 or SWZ_F32) is

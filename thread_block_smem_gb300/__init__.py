@@ -45,8 +45,8 @@ EXPORTS = ["swz_tile_map", "swz_is_bijective", "swz_gemm", "swz_gemm_ex", "swz_g
            "swz_l2_model_bytes", "swz_calibrate", "swz_gemm_die_plan", "swz_quantize_fp8",
            "swz_gemm_fp8", "swz_linear_fp8", "swz_linear_fp8_workspace_size",
            "swz_newton_schulz", "swz_newton_schulz_workspace_size", "swz_quantize_int8",
-           "swz_gemm_int8", "swz_gemm_int8_workspace_size", "swz_linear_int8",
-           "swz_linear_int8_workspace_size", "swz_layer_norm", "swz_layer_norm_backward",
+           "swz_gemm_int8", "swz_gemm_int8_workspace_size", "swz_gemm_int8_workspace_size_ex",
+           "swz_linear_int8", "swz_linear_int8_workspace_size", "swz_layer_norm", "swz_layer_norm_backward",
            "swz_layer_norm_backward_workspace_size", "swz_grad_norm", "swz_clip_grad_norm",
            "swz_grad_norm_workspace_size"]
 
@@ -498,7 +498,8 @@ from .linear import (SWZ_BLOCK_ROW, SWZ_BLOCK_SQUARE, SWZ_E4M3, SWZ_E5M2, SWZ_F3
 from . import int8  # noqa: E402
 from .int8 import (gemm_int8, int8_empty, linear_int8, quantize_int8,  # noqa: E402,F401
                    swz_gemm_int8, swz_gemm_int8_opts, swz_gemm_int8_workspace_size,
-                   swz_linear_int8, swz_linear_int8_workspace_size, swz_quantize_int8)
+                   swz_gemm_int8_workspace_size_ex, swz_linear_int8,
+                   swz_linear_int8_workspace_size, swz_quantize_int8)
 
 # around a linear layer in training (training.py)
 from . import training  # noqa: E402

@@ -650,12 +650,13 @@ static int product(const void* a16, const void* b16, int64_t ld, const float* sa
 // How a product is made: by dp4a (few tokens), with B widened on its way to the tensor
 // core (batches), or with both operands widened first.
 enum Form { kTokenForm, kRingForm, kBatchForm, kWideForm };
-static Form form_of(int M, int N, int K, int tile) {
+static Form form_of(int M, int N, int K, int tile, int split) {
   if (tile == 128 || tile == 256) return kWideForm;
   // (the tokens' form reads whole pieces of 16 bytes of a row of B)
   if (tile == 0 && M <= kTokens && K >= 16) return kTokenForm;
   if (tile == 32 || (tile == 0 && M <= kRingRows)) return kRingForm;
-  if (tile == 64 || (M <= kBatchRows && batch_plan(M, N, K, 0, 1).split)) return kBatchForm;
+  // (where it has the split that was asked for: how many SMs there are does not matter to that)
+  if (tile == 64 || (M <= kBatchRows && batch_plan(M, N, K, split, 1).split)) return kBatchForm;
   return kWideForm;
 }
 
@@ -727,12 +728,19 @@ static int widen(const void* A, int64_t lda, int M, const void* B, int64_t ldb, 
   return launch_widen(w, num_sms, s);
 }
 
-extern "C" int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes) {
+extern "C" int swz_gemm_int8_workspace_size_ex(int M, int N, int K, const swz_gemm_int8_opts* opts,
+                                               uint64_t* h_bytes) {
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
   if (M == 0 || N == 0 || K == 0) return SWZ_OK;
-  *h_bytes = gemm_bytes(form_of(M, N, K, tile), M, N, K);
+  *h_bytes = gemm_bytes(form_of(M, N, K, opts ? opts->tile : 0, opts ? opts->split_k : 0), M, N, K);
   return SWZ_OK;
+}
+
+extern "C" int swz_gemm_int8_workspace_size(int M, int N, int K, int tile, uint64_t* h_bytes) {
+  swz_gemm_int8_opts o = {};
+  o.tile = tile;
+  return swz_gemm_int8_workspace_size_ex(M, N, K, &o, h_bytes);
 }
 
 extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const void* B,
@@ -752,7 +760,7 @@ extern "C" int swz_gemm_int8(const void* A, int64_t lda, const float* sa, const 
   const RowsInMemory result = result_at(C, ldc, c_dtype, M, N);
   if (K > 0 && (over_int8_rows(result, A, lda, sa, M, K) || over_int8_rows(result, B, ldb, sb, N, K)))
     return SWZ_EINVAL;
-  const Form f = form_of(M, N, K, o.tile);
+  const Form f = form_of(M, N, K, o.tile, o.split_k);
   if ((f == kTokenForm && o.split_k > 1) || (f == kRingForm && M > kRingRows))
     return SWZ_EUNSUPPORTED;
   const uint64_t need = K > 0 ? gemm_bytes(f, M, N, K) : 0;
@@ -799,7 +807,7 @@ extern "C" int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_b
   if (!h_bytes || M < 0 || N < 0 || K < 0 || K > kMaxK) return SWZ_EINVAL;
   *h_bytes = 0;
   if (M == 0 || N == 0 || K == 0) return SWZ_OK;
-  const Form f = form_of(M, N, K, 0);
+  const Form f = form_of(M, N, K, 0, 0);
   *h_bytes = linear_bytes(f, f == kTokenForm && tokens_fused(M, K), M, N, K);
   return SWZ_OK;
 }
@@ -817,7 +825,7 @@ extern "C" int swz_linear_int8(const void* x, int dtype, int64_t ldx, const void
     return SWZ_EINVAL;
   const RowsInMemory result = result_at(y, ldy, y_dtype, M, N);
   if (K > 0 && over_int8_rows(result, W, ldw, sw, N, K)) return SWZ_EINVAL;
-  const Form f = form_of(M, N, K, 0);
+  const Form f = form_of(M, N, K, 0, 0);
   // where every CTA quantises x itself, y must not be written over it
   const bool fused = f == kTokenForm && tokens_fused(M, K) &&
                      !rows_meet(result, matrix_at(x, M, ldx * int64_t(es), int64_t(K) * int64_t(es)));

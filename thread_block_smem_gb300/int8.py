@@ -33,6 +33,8 @@ def declare(L):
     L.swz_gemm_int8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i, i, i, i,
                                 ctypes.POINTER(swz_gemm_int8_opts), vp, u64, vp]
     L.swz_gemm_int8_workspace_size.argtypes = [i, i, i, i, ctypes.POINTER(u64)]
+    L.swz_gemm_int8_workspace_size_ex.argtypes = [i, i, i, ctypes.POINTER(swz_gemm_int8_opts),
+                                                  ctypes.POINTER(u64)]
     L.swz_linear_int8.argtypes = [vp, i, i64, vp, i64, vp, vp, i64, i, i, i, i, vp, u64, vp]
     L.swz_linear_int8_workspace_size.argtypes = [i, i, i, ctypes.POINTER(u64)]
 
@@ -71,6 +73,15 @@ def _size(fn, *sizes):
 
 def swz_gemm_int8_workspace_size(M, N, K, tile=0):
     return _size(_swz.lib().swz_gemm_int8_workspace_size, M, N, K, tile)
+
+
+def swz_gemm_int8_workspace_size_ex(M, N, K, opts=None):
+    if not _lin._ints(M, N, K):
+        return _swz.SWZ_EINVAL, 0
+    b = ctypes.c_uint64(0)
+    rc = _swz.lib().swz_gemm_int8_workspace_size_ex(
+        M, N, K, ctypes.byref(opts) if opts is not None else None, ctypes.byref(b))
+    return rc, b.value
 
 
 def swz_linear_int8_workspace_size(M, N, K):
@@ -161,7 +172,7 @@ def gemm_int8(a, sa, b, sb, *, out=None, out_dtype=None, order="serpentine", gro
         _lin._keep(stream, a, sa, b, sb, out)
     opts = swz_gemm_int8_opts(order, group, tile, split_k, debug_flags, timeout_ms)
     need = _lin._u64()
-    rc = _lin._L.swz_gemm_int8_workspace_size(M, N, K, tile, need)
+    rc = _lin._L.swz_gemm_int8_workspace_size_ex(M, N, K, opts, need)
     if rc == 0:
         need = need.value
         ws = _lin._empty(need, torch.uint8, a, stream) if need else None
