@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kBatchThreads, CTAS)
   const uint32_t rank = p.split > 1 ? ptx::cluster_ctarank() : 0u;
   const uint32_t tile = blockIdx.x / p.split;
   const int m0 = int(tile % p.tiles_m) * int(p.nb);
-  const int n0 = int(tile / p.tiles_m) * 128;
+  const int n0 = int(tile / p.tiles_m) * 128;  // (n0 + 127 may not fit 32 bits)
   const uint32_t kb0 = uint32_t(uint64_t(p.num_kb) * rank / p.split);
   const uint32_t kb1 = uint32_t(uint64_t(p.num_kb) * (rank + 1) / p.split);
 
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kBatchThreads, CTAS)
   int32_t* const part = reinterpret_cast<int32_t*>(smem);  // nb rows of 128, over the stages and
   // slots (every MMA has completed, and so every load that it waited for)
   if (warp < kBatchWarps && !aborted) {
-    const int n = n0 + int(q * 32 + lane);
+    const int64_t n = n0 + int64_t(q * 32 + lane);
     const float sb = n < p.N ? p.sb[n] : 0.0f;
     for (uint32_t m = warp / 4 * 16; m < p.nb; m += 32) {
       if (m0 + int(m) >= p.M) break;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kBatchThreads, CTAS)
     ptx::cluster_sync();
     if (warp < kBatchWarps && !aborted) {
       // rank r takes every split-th row of A, a warp a row, a lane four columns
-      const int n = n0 + int(lane) * 4;
+      const int64_t n = n0 + int64_t(lane) * 4;
       float sb[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) sb[e] = n + e < p.N ? p.sb[n + e] : 0.0f;

@@ -71,8 +71,11 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t slot = warp % p.slots, group = warp / p.slots;
   const int pitch = (p.K + 15) / 16 * 16;
-  const int n0 = int(int64_t(p.N) * blockIdx.x / gridDim.x);
-  const int n1 = int(int64_t(p.N) * (blockIdx.x + 1) / gridDim.x);
+  // rows are counted from this CTA's first: with N just below 2^31 what the loops add to
+  // a row's own number would not fit 32 bits
+  const int64_t n0 = int64_t(p.N) * blockIdx.x / gridDim.x;
+  const int count = int(int64_t(p.N) * (blockIdx.x + 1) / gridDim.x - n0);
+  const uint8_t* const B = p.B + n0 * p.ldb;
   const int k0 = int(slot) * 512 + int(lane) * 16, k_step = int(p.slots) * 512;
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
@@ -86,10 +89,10 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int row = n + i * int(p.groups);
-      b[i] = *reinterpret_cast<const uint4*>(p.B + int64_t(row < n1 ? row : n1 - 1) * p.ldb + k);
+      b[i] = *reinterpret_cast<const uint4*>(B + int64_t(row < count ? row : count - 1) * p.ldb + k);
     }
   };
-  fetch(n0 + int(group), k0);
+  fetch(int(group), k0);
   for (uint32_t i = threadIdx.x; i < MT * kTokRows; i += kTokThreads) (&part[0][0])[i] = 0;
 
   if constexpr (FUSED) {
@@ -128,8 +131,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   __syncthreads();
 
   // whole turns of kTokRows rows: the partial sums of a turn fit shared memory
-  for (int turn = n0; turn < n1; turn += kTokRows) {
-    const int end = n1 - turn < kTokRows ? n1 : turn + kTokRows;
+  for (int turn = 0; turn < count; turn += kTokRows) {
+    const int end = count - turn < kTokRows ? count : turn + kTokRows;
     for (int k = k0; k - int(lane) * 16 < p.K; k += k_step) {
       uint4 a[MT];
 #pragma unroll
@@ -141,13 +144,13 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
         }
       }
       for (int n = turn + int(group); n < end; n += kAhead * int(p.groups)) {
-        if (!(turn == n0 && k == k0 && n == n0 + int(group))) fetch(n, k);
+        if (!(turn == 0 && k == k0 && n == int(group))) fetch(n, k);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const int row = n + i * int(p.groups);
           if (row >= end) break;
           if (k == cut)
-            b[i] = load_bytes(p.B + int64_t(row) * p.ldb, k, p.K, row + 1 == p.N);
+            b[i] = load_bytes(B + int64_t(row) * p.ldb, k, p.K, n0 + row + 1 == p.N);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             int32_t s = __dp4a(int(b[i].x), int(a[t].x), 0);
@@ -165,8 +168,9 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
     for (int i = int(threadIdx.x); i < p.M * (end - turn); i += kTokThreads) {
       const int t = i / (end - turn), n = i % (end - turn);
       const float sa = FUSED ? scale[t] : p.sa[t];
-      rows::store1(p.C + (int64_t(t) * p.ldc + turn + n) * es,
-                   float(part[t][n]) * (sa * p.sb[turn + n]), p.c_dtype);
+      const int64_t col = n0 + turn + n;
+      rows::store1(p.C + (int64_t(t) * p.ldc + col) * es, float(part[t][n]) * (sa * p.sb[col]),
+                   p.c_dtype);
       part[t][n] = 0;
     }
     __syncthreads();
