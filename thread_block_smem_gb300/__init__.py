@@ -216,6 +216,8 @@ def gemm_mma_sync(A, B, layout="swizzle128", order="panel", group=8, out=None, s
     _check(swz_gemm_mma_sync(A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K,
                              SWZ_BF16 if A.dtype == torch.bfloat16 else SWZ_F16, *lay,
                              _order(order), group, _stream(stream)), "swz_gemm_mma_sync")
+    if out is not None:
+        _written(out)
     return C
 
 
@@ -329,6 +331,20 @@ def _check(rc, what):
 
 
 # ---- tensor-level calls -----------------------------------------------------
+_increment_version = _Tensor = None
+
+
+def _written(*tensors):
+    """Moves autograd's version counter of tensors that a call has written where they were:
+    an operation that saved their old values then raises in its backward.  (What only
+    looks like a tensor has no counter.)"""
+    global _increment_version, _Tensor
+    if _increment_version is None:
+        from torch import Tensor as _Tensor
+        from torch.autograd.graph import increment_version as _increment_version
+    _increment_version([t for t in tensors if isinstance(t, _Tensor)])
+
+
 def _stream(stream):
     import torch
     if stream is None:
@@ -440,6 +456,8 @@ def gemm(A, B, order="panel", group=8, persistent=False, *, out=None, tile_n=0,
                      smem_swizzle, dynamic, die_split)
     _check(swz_gemm_ex(A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K, _order(order),
                        group, int(bool(persistent)), opts, _stream(stream)), "swz_gemm_ex")
+    if out is not None:
+        _written(out)
     return C
 
 
@@ -465,6 +483,7 @@ def gemm_host(hA, hB, hC, dA, dB, dC, order="panel", group=8, *, tile_n=0, cta_p
     _check(swz_gemm_host(hA.data_ptr(), hB.data_ptr(), hC.data_ptr(), M, N, K, _order(order),
                          group, opts, dA.data_ptr(), dB.data_ptr(), dC.data_ptr(), slabs,
                          _stream(stream)), "swz_gemm_host")
+    _written(hC, dA, dB, dC)
     return hC
 
 
@@ -478,6 +497,8 @@ def transpose(x, layout="xor", out=None, stream=None):
     lay = LAYOUTS[layout] if isinstance(layout, str) else int(layout)
     _check(swz_transpose(x.data_ptr(), y.data_ptr(), M, N, lay, _stream(stream)),
            "swz_transpose")
+    if out is not None:
+        _written(out)
     return y
 
 

@@ -180,7 +180,7 @@ def gemm_int8(a, sa, b, sb, *, out=None, out_dtype=None, order="serpentine", gro
                                    ws.data_ptr() if need else None, need, _lin._handle(stream, a))
     if rc:
         raise _swz.SwzError(rc, "swz_gemm_int8")
-    return C if out is not None else _lin._no_gradient("gemm_int8", C, a, sa, b, sb)
+    return _lin._result("gemm_int8", C, out, a, sa, b, sb)
 
 
 def linear_int8(x, qw, sw, *, out=None, out_dtype=None, stream=None):
@@ -211,4 +211,4 @@ def linear_int8(x, qw, sw, *, out=None, out_dtype=None, stream=None):
                                      _lin._handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_linear_int8")
-    return y if out is not None else _lin._no_gradient("linear_int8", y, x, qw, sw)
+    return _lin._result("linear_int8", y, out, x, qw, sw)

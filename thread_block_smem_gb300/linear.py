@@ -296,6 +296,14 @@ def _no_gradient(what, y, *inputs):
     return y
 
 
+def _result(what, y, out, *inputs):
+    """What a call returns that has written y, which is ``out`` where that was given."""
+    if out is None:
+        return _no_gradient(what, y, *inputs)
+    _swz._written(out)
+    return out
+
+
 # ---- operators --------------------------------------------------------------------
 def quantize_fp8(x, block="row", fmt="e4m3", transposed=False, *, stream=None):
     """(q, scales) of x (M x K; fp16, bf16 or fp32, contiguous rows), with
@@ -381,7 +389,7 @@ def gemm_fp8(a, sa, b, sb, *, b_block="square", out=None, out_dtype=None, order=
                              timeout_ms)
     _swz._check(_L.swz_gemm_fp8(A, B, C.data_ptr(), ldc, code, M, N, K, opts, _handle(stream, a)),
                 "swz_gemm_fp8")
-    return C if out is not None else _no_gradient("gemm_fp8", C, a, sa, b, sb)
+    return _result("gemm_fp8", C, out, a, sa, b, sb)
 
 
 def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=None):
@@ -408,7 +416,7 @@ def linear_fp8(x, qw, sw, *, w_block="square", out=None, out_dtype=None, stream=
                                ws.data_ptr() if need else None, need, _handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_linear_fp8")
-    return y if out is not None else _no_gradient("linear_fp8", y, x, qw, sw)
+    return _result("linear_fp8", y, out, x, qw, sw)
 
 
 def linear_fp8_forward(x, w, *, out_dtype=None, stream=None):
@@ -540,4 +548,4 @@ def newton_schulz(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     _swz._check(_L.swz_newton_schulz(g.data_ptr(), code, *ld[0], y.data_ptr(), ycode, *ld[1], batch, m,
                                      n, steps, a, b, c, eps, opts, ws.data_ptr(), need,
                                      _handle(stream, G)), "swz_newton_schulz")
-    return _no_gradient("newton_schulz", out, G) if fresh else out
+    return _result("newton_schulz", out, None if fresh else out, G)

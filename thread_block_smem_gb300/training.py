@@ -130,6 +130,8 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out=None, out_dty
                                 _lin._handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_layer_norm")
+    if out is not None:
+        _swz._written(out)
     return y, mean, rstd
 
 
@@ -299,4 +301,6 @@ def clip_grad_norm(grads, max_norm, eps=1e-6, *, out=None, stream=None):
     max_norm, eps = float(max_norm), float(eps)
     if not max_norm >= 0 or not eps >= 0:
         raise ValueError("max_norm and eps must be at least 0")
-    return _norm_call("swz_clip_grad_norm", grads, out, stream, max_norm, eps)
+    norm = _norm_call("swz_clip_grad_norm", grads, out, stream, max_norm, eps)
+    _swz._written(*(grads if out is None else out))
+    return norm
