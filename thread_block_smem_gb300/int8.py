@@ -7,7 +7,9 @@ Matrices are ``torch.int8`` tensors of shape (rows, K) whose rows start on
 multiples of 16 bytes (``quantize_int8`` makes them so; ``int8_empty`` allocates
 one), their scales fp32 tensors of shape (rows,).  All operands of a call are on
 the current device; ``stream`` is as in ``linear``.  The operators have no
-gradient: a backward through what they return raises (``out`` takes values only).
+gradient: a backward through what they return raises (``out`` takes values only),
+through the product of rows that were quantised from x as well; weights that are kept
+for serving are quantised from a detached tensor or under ``torch.no_grad``.
 """
 from __future__ import annotations
 
@@ -147,7 +149,7 @@ def quantize_int8(x, *, stream=None):
                                    _lin._handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_quantize_int8")
-    return q, s
+    return q, _lin._no_gradient("quantize_int8", s, x)
 
 
 def gemm_int8(a, sa, b, sb, *, out=None, out_dtype=None, order="serpentine", group=8, tile=0,
