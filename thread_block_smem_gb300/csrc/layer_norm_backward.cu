@@ -44,6 +44,14 @@ struct BwdArgs {
   int64_t pitch;
 };
 
+// Whether mean rstd leaves fp32's range.  Beyond a row's end x reads as zero, and its xhat
+// there, -mean rstd, times the zero of dy makes the sum of g xhat NaN.  That sum is zero in
+// truth: a row with a value other than its mean has rstd <= sqrt(N) / |x - mean| <= 2^40 /
+// |mean|, so every value of such a row is its mean (1e33 throughout, with an eps of 1e-12).
+__device__ __forceinline__ bool far_constant(float mean, float rstd) {
+  return isinf(mean * rstd) && isfinite(mean) && isfinite(rstd);
+}
+
 // NC chunks a thread; WARP: a row a warp, eight a CTA, otherwise a row the CTA; G: the
 // common case (layer_norm.cuh) or 0.
 template <typename X, typename D, int NC, bool WARP, int G>
@@ -91,6 +99,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) layer_norm_backward_kernel(c
     if (!AHEAD) fetch(row);
     uint64_t xhat[AHEAD ? NC : 1][4], d[AHEAD ? NC : 1][4], s0 = 0ull, s1 = 0ull;
     const uint64_t m2 = both(-mean), r2 = both(rstd);
+    const bool far = far_constant(mean, rstd);
     auto values = [&](int c, uint64_t (&h)[4], uint64_t (&g)[4], uint64_t (&v)[4]) {
       uint64_t x[4], w[4];
       pairs_of<X>(xw[c], x);
@@ -132,7 +141,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512) layer_norm_backward_kernel(c
           b += u.y;
         }
       }
-      const uint64_t a2 = both(-a * inv), b2 = both(-b * inv);
+      const uint64_t a2 = both(-a * inv), b2 = both(far ? 0.0f : -b * inv);
       uint8_t* dx = p.dx + row * p.lddx;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(512) long_dx_kernel(const BwdArgs p) {
     s[1] += u[1];
   }
   rows::row_sums<TPR, 2>(s, part);
-  const float a = s[0] * inv, b = s[1] * inv;
+  const float a = s[0] * inv, b = far_constant(mean, rstd) ? 0.0f : s[1] * inv;
   for (int64_t c = 0; c < turns; ++c) {
     const int64_t k = (c * TPR + threadIdx.x) * 8;
     fetch(k);
