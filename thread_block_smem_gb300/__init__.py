@@ -331,18 +331,16 @@ def _check(rc, what):
 
 
 # ---- tensor-level calls -----------------------------------------------------
-_increment_version = _Tensor = None
+_increment_version = None
 
 
 def _written(*tensors):
     """Moves autograd's version counter of tensors that a call has written where they were:
-    an operation that saved their old values then raises in its backward.  (What only
-    looks like a tensor has no counter.)"""
-    global _increment_version, _Tensor
+    an operation that saved their old values then raises in its backward."""
+    global _increment_version
     if _increment_version is None:
-        from torch import Tensor as _Tensor
-        from torch.autograd.graph import increment_version as _increment_version
-    _increment_version([t for t in tensors if isinstance(t, _Tensor)])
+        from torch._C import _increment_version  # the public wrapper costs as much again
+    _increment_version(tensors)
 
 
 def _stream(stream):

@@ -300,7 +300,8 @@ def _result(what, y, out, *inputs):
     """What a call returns that has written y, which is ``out`` where that was given."""
     if out is None:
         return _no_gradient(what, y, *inputs)
-    _swz._written(out)
+    if isinstance(out, torch.Tensor):  # (what only looks like one has no version)
+        _swz._written(out)
     return out
 
 
