@@ -695,7 +695,8 @@ int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
  *   y = (x - mean) * rstd * weight + bias      (rows ldy apart)
  * weight and bias: N values each, NULL for 1 and 0 (their types are then not
  * used).  mean and rstd (M values each) are written for the gradient.  y may be x
- * itself where types and rows are the same; otherwise they must not overlap.
+ * itself where types and rows are the same; otherwise it must not lie over x, weight
+ * or bias (SWZ_EINVAL).
  * M = 0 or N = 0: no-op.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
  */
 int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void* weight, int w_dtype,
@@ -708,9 +709,10 @@ int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void* weight, in
  *   dw = sum of dy * xhat, db = sum of dy                       over the rows
  * from the operands and results of swz_layer_norm.  dx, dw (N values) and db (N
  * values; of dw_dtype too) may each be NULL where it is not wanted, not all of
- * them; dx may be dy or x itself where types and rows are the same.  The sums over
- * rows are taken in an order that depends on the sizes and the device only (no
- * atomics).  M = 0 writes zeros to dw and db.  d_workspace (for dw and db):
+ * them; dx may be dy or x itself where types and rows are the same, and otherwise
+ * must not lie over an operand (SWZ_EINVAL).  The sums over rows are taken in an
+ * order that depends on the sizes and the device only (no atomics).  M = 0 writes
+ * zeros to dw and db.  d_workspace (for dw and db):
  * 16-byte aligned device scratch of at least
  * swz_layer_norm_backward_workspace_size bytes, contents free before and after;
  * calls that share it must not overlap.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.

@@ -1,4 +1,4 @@
-"""What the 8-bit integer products refuse of results that lie over their operands (CPU
+"""What the 8-bit integer products and the layer norm refuse of results over operands (CPU
 only: every call here is refused before any CUDA call), and the test of two sets of rows
 in memory behind it against all of their bytes."""
 import os
@@ -105,3 +105,29 @@ def test_linear_over_its_operands(swz, m):
             for ws, size in ((6 * MB, 256 + m * k - 1), (0, 0)):
                 a[12:] = [ws, size]
                 assert swz.swz_linear_int8(*a) == swz.SWZ_EINVAL, to
+
+
+def test_layer_norm_over_its_operands(swz):
+    m, n, bf16 = 8, 64, swz.SWZ_BF16
+    size = m * n * 2
+    # x, dtype, ldx, w, w_dtype, b, b_dtype, eps, y, y_dtype, ldy, mean, rstd, M, N
+    good = [MB, bf16, n, 2 * MB, bf16, 3 * MB, 3, 1e-5, 4 * MB, bf16, n, 5 * MB, 6 * MB, m, n]
+    changes = [{8: MB + 2}, {8: MB + size - 2}, {8: MB - size + 2}, {8: MB, 9: swz.SWZ_F16}, {8: MB, 9: 3},
+               {8: MB, 10: n + 8}, {8: MB, 2: n + 8}, {8: 2 * MB}, {8: 2 * MB + 2 * n - 2}, {8: 3 * MB},
+               {8: 3 * MB + 4 * n - 2}, {8: 3 * MB - size + 2}]
+    for at in changes:
+        a = list(good)
+        for k, v in at.items():
+            a[k] = v
+        assert swz.swz_layer_norm(*a) == swz.SWZ_EINVAL, at
+    # dy, dtype, ld, x, dtype, ld, w, dtype, mean, rstd, dx, dtype, ld, dw, db, dtype, M, N, ws, bytes
+    good = [MB, bf16, n, 2 * MB, bf16, n, 3 * MB, bf16, 4 * MB, 5 * MB, 6 * MB, bf16, n, 7 * MB, 8 * MB, 3, m, n,
+            9 * MB, 1 << 30]
+    changes = [{10: MB + 2}, {10: MB - size + 2}, {10: MB, 11: 3}, {10: MB, 12: n + 8}, {10: 2 * MB + size - 2},
+               {10: 2 * MB, 11: swz.SWZ_F16}, {10: 2 * MB, 5: n + 2}, {10: 3 * MB}, {10: 3 * MB + 2 * n - 2},
+               {10: 4 * MB}, {10: 4 * MB + 4 * m - 2}, {10: 5 * MB}, {10: 5 * MB - size + 2}]
+    for at in changes:
+        a = list(good)
+        for k, v in at.items():
+            a[k] = v
+        assert swz.swz_layer_norm_backward(*a) == swz.SWZ_EINVAL, at

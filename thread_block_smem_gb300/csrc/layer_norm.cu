@@ -275,6 +275,10 @@ extern "C" int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void*
   if (!matrix_ok(x, dtype, ldx, M, N) || !matrix_ok(y, y_dtype, ldy, M, N)) return SWZ_EINVAL;
   if (!vector_ok(weight, w_dtype) || !vector_ok(bias, b_dtype)) return SWZ_EINVAL;
   if (!mean || !aligned4(mean) || !rstd || !aligned4(rstd)) return SWZ_EINVAL;
+  const RowsInMemory result = rows_at(y, y_dtype, ldy, M, N);
+  if (!may_lie(result, y_dtype, rows_at(x, dtype, ldx, M, N), dtype) ||
+      !apart(result, weight, N * size_of(w_dtype)) || !apart(result, bias, N * size_of(b_dtype)))
+    return SWZ_EINVAL;
   DeviceInfo dev{};
   const int rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;

@@ -179,6 +179,21 @@ inline bool vector_ok(const void* p, int dtype) {
   return reinterpret_cast<uintptr_t>(p) % uintptr_t(size_of(dtype)) == 0;
 }
 
+// Whether a result may be written while an input is read: nothing in common, or the same
+// rows of the same type, which are read before they are written.
+inline RowsInMemory rows_at(const void* p, int dtype, int64_t ld, int M, int N) {
+  const int64_t es = size_of(dtype);
+  return RowsInMemory{p, M, (M > 1 ? ld : int64_t(N)) * es, int64_t(N) * es};
+}
+inline bool may_lie(const RowsInMemory& result, int result_dtype, const RowsInMemory& input,
+                    int input_dtype) {
+  return (result.p == input.p && result_dtype == input_dtype && result.ld == input.ld) ||
+         !rows_meet(result, input);
+}
+inline bool apart(const RowsInMemory& result, const void* values, int64_t bytes) {
+  return !values || !rows_meet(result, RowsInMemory{values, 1, bytes, bytes});
+}
+
 // Threads of a CTA whose threads hold nc chunks of a row of N values each.
 inline int threads_of(int N, int nc) {
   return int((int64_t(N) + int64_t(nc) * 256 - 1) / (int64_t(nc) * 256)) * 32;

@@ -384,6 +384,14 @@ extern "C" int swz_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
         (dx && !matrix_ok(dx, dx_dtype, lddx, M, N)))
       return SWZ_EINVAL;
     if (!mean || !aligned4(mean) || !rstd || !aligned4(rstd)) return SWZ_EINVAL;
+    if (dx) {
+      const RowsInMemory result = rows_at(dx, dx_dtype, lddx, M, N);
+      if (!may_lie(result, dx_dtype, rows_at(x, dtype, ldx, M, N), dtype) ||
+          !may_lie(result, dx_dtype, rows_at(dy, dy_dtype, lddy, M, N), dy_dtype) ||
+          !apart(result, weight, N * size_of(w_dtype)) || !apart(result, mean, int64_t(M) * 4) ||
+          !apart(result, rstd, int64_t(M) * 4))
+        return SWZ_EINVAL;
+    }
     uint64_t need = 0;
     swz_layer_norm_backward_workspace_size(M, N, &need);
     if (sums && (!d_workspace || !aligned16(d_workspace) || workspace_bytes < need))

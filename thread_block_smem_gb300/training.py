@@ -110,8 +110,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out=None, out_dty
     """(y, mean, rstd) of the rows of x (M x N; fp16, bf16 or fp32, contiguous rows):
     y = (x - mean) rstd weight + bias, rstd = 1 / sqrt(var + eps) with the mean square
     of x - mean as var.  ``weight`` and ``bias`` (N values, of any of the types) may be
-    None.  ``out`` (M x N; may be x) or ``out_dtype`` (default: x's type).  mean and
-    rstd (fp32) are for layer_norm_backward."""
+    None.  ``out`` (M x N; may be x itself, refused where it lies across an operand) or
+    ``out_dtype`` (default: x's type).  mean and rstd (fp32) are for
+    layer_norm_backward."""
     if _lin.torch is None:
         _lin._init()
     torch = _lin.torch
