@@ -624,8 +624,8 @@ int swz_newton_schulz_workspace_size(int batch, int m, int n, uint64_t* h_bytes)
  *   even: -127 .. 127
  * A row of zeros gives zeros; one that holds an infinity or NaN gives zeros with
  * the scale NaN.  What lies beyond the last column of a row of q is left as it is.
- * M = 0: no-op; K = 0 writes the scales only.  Errors: SWZ_EINVAL, SWZ_EARCH,
- * SWZ_ECUDA.
+ * q and scales must not lie over x (SWZ_EINVAL).  M = 0: no-op; K = 0 writes the
+ * scales only.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
  */
 int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, int K, void* q, int64_t ldq,
                       float* scales, void* stream);

@@ -131,3 +131,15 @@ def test_layer_norm_over_its_operands(swz):
         for k, v in at.items():
             a[k] = v
         assert swz.swz_layer_norm_backward(*a) == swz.SWZ_EINVAL, at
+
+
+def test_quantize_over_its_input(swz):
+    m, k = 8, 64
+    # x, dtype, ldx, M, K, q, ldq, scales
+    good = [MB, swz.SWZ_BF16, k, m, k, 2 * MB, k, 3 * MB]
+    for at in ({5: MB}, {5: MB + 2 * m * k - 16}, {5: MB - m * k + 16}, {7: MB}, {7: MB + 2 * m * k - 4},
+               {7: MB - 4 * m + 4}, {5: MB + k, 6: 2 * k, 2: k + 8}):
+        a = list(good)
+        for i, v in at.items():
+            a[i] = v
+        assert swz.swz_quantize_int8(*a) == swz.SWZ_EINVAL, at

@@ -142,6 +142,11 @@ extern "C" int swz_quantize_int8(const void* x, int dtype, int64_t ldx, int M, i
   if (K > 0 && (!x || reinterpret_cast<uintptr_t>(x) % es != 0 || (M > 1 && ldx < K) || !q ||
                 !aligned16(q) || ldq < K || ldq % 16 != 0))
     return SWZ_EINVAL;
+  const int64_t width = int64_t(K) * int64_t(es);
+  const RowsInMemory input{x, M, M > 1 ? ldx * int64_t(es) : width, width};
+  if (rows_meet(input, RowsInMemory{q, M, M > 1 ? ldq : K, K}) ||
+      rows_meet(input, RowsInMemory{scales, 1, 0, int64_t(M) * 4}))
+    return SWZ_EINVAL;
   DeviceInfo dev{};
   const int rc = current_device(&dev);
   if (rc != SWZ_OK) return rc;
