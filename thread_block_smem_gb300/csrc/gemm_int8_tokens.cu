@@ -10,7 +10,8 @@
 // numbers, in any order.
 //   * The layer quantises x here where it is short: every CTA needs all of it, and a
 //     few thousand values are read and rounded while its first loads of B are under
-//     way; a kernel of its own takes 1.8 us.
+//     way; a kernel of its own takes 1.8 us (and is what a result over x takes: other
+//     CTAs store theirs while one still reads x).
 //   * Rates on this GPU, multiply-adds a clock and SM: dp4a 255, mma.sync on 8-bit
 //     integers 252, on fp16 1020.  B at the memory's rate asks for 24 a row of A.
 //
@@ -31,7 +32,7 @@ namespace i8 {
 
 constexpr int kTokWarps = 16, kTokThreads = kTokWarps * 32;
 constexpr int kTokBytes = 32 * 1024;  // of x in shared memory, at most
-constexpr int kTokRows = 1024;        // rows of B a CTA and turn
+constexpr uint32_t kTokRows = 1024;        // rows of B a CTA and turn
 
 struct TokParams {
   const uint8_t* A;  // bytes; NULL: x is quantised here
@@ -71,11 +72,9 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t slot = warp % p.slots, group = warp / p.slots;
   const int pitch = (p.K + 15) / 16 * 16;
-  // rows are counted from this CTA's first: with N just below 2^31 what the loops add to
-  // a row's own number would not fit 32 bits
-  const int64_t n0 = int64_t(p.N) * blockIdx.x / gridDim.x;
-  const int count = int(int64_t(p.N) * (blockIdx.x + 1) / gridDim.x - n0);
-  const uint8_t* const B = p.B + n0 * p.ldb;
+  // (rows are unsigned: with N just below 2^31 the loops go to numbers beyond it)
+  const uint32_t n0 = uint32_t(int64_t(p.N) * blockIdx.x / gridDim.x);
+  const uint32_t n1 = uint32_t(int64_t(p.N) * (blockIdx.x + 1) / gridDim.x);
   const int k0 = int(slot) * 512 + int(lane) * 16, k_step = int(p.slots) * 512;
   ptx::grid_dep_wait();
   if (threadIdx.x == 0) ptx::grid_dep_launch_dependents();
@@ -84,15 +83,15 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   // summed, and what is beyond K meets zeros.
   uint4 b[kAhead];
   const int cut = p.K % 16 ? p.K - p.K % 16 : -1;  // the piece that K cuts
-  auto fetch = [&](int n, int k) {
+  auto fetch = [&](uint32_t n, int k) {
     if (k >= p.K || k == cut) k = 0;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int row = n + i * int(p.groups);
-      b[i] = *reinterpret_cast<const uint4*>(B + int64_t(row < count ? row : count - 1) * p.ldb + k);
+      const uint32_t row = n + i * p.groups;
+      b[i] = *reinterpret_cast<const uint4*>(p.B + int64_t(row < n1 ? row : n1 - 1) * p.ldb + k);
     }
   };
-  fetch(int(group), k0);
+  fetch(n0 + group, k0);
   for (uint32_t i = threadIdx.x; i < MT * kTokRows; i += kTokThreads) (&part[0][0])[i] = 0;
 
   if constexpr (FUSED) {
@@ -131,8 +130,8 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
   __syncthreads();
 
   // whole turns of kTokRows rows: the partial sums of a turn fit shared memory
-  for (int turn = 0; turn < count; turn += kTokRows) {
-    const int end = count - turn < kTokRows ? count : turn + kTokRows;
+  for (uint32_t turn = n0; turn < n1; turn += kTokRows) {
+    const uint32_t end = n1 - turn < kTokRows ? n1 : turn + kTokRows;
     for (int k = k0; k - int(lane) * 16 < p.K; k += k_step) {
       uint4 a[MT];
 #pragma unroll
@@ -143,14 +142,14 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
           else a[t] = keep_below(load_bytes(p.A + int64_t(t) * p.lda, k, p.K, t + 1 == p.M), k, p.K);
         }
       }
-      for (int n = turn + int(group); n < end; n += kAhead * int(p.groups)) {
-        if (!(turn == 0 && k == k0 && n == int(group))) fetch(n, k);
+      for (uint32_t n = turn + group; n < end; n += kAhead * p.groups) {
+        if (!(turn == n0 && k == k0 && n == n0 + group)) fetch(n, k);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          const int row = n + i * int(p.groups);
+          const uint32_t row = n + i * p.groups;
           if (row >= end) break;
           if (k == cut)
-            b[i] = load_bytes(B + int64_t(row) * p.ldb, k, p.K, n0 + row + 1 == p.N);
+            b[i] = load_bytes(p.B + int64_t(row) * p.ldb, k, p.K, row + 1 == uint32_t(p.N));
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             int32_t s = __dp4a(int(b[i].x), int(a[t].x), 0);
@@ -165,10 +164,11 @@ __global__ void __launch_bounds__(kTokThreads, 2) gemm_int8_tokens_kernel(const 
     }
     __syncthreads();
     const int es = p.c_dtype == SWZ_F32 ? 4 : 2;
-    for (int i = int(threadIdx.x); i < p.M * (end - turn); i += kTokThreads) {
-      const int t = i / (end - turn), n = i % (end - turn);
+    const int cols = int(end - turn);
+    for (int i = int(threadIdx.x); i < p.M * cols; i += kTokThreads) {
+      const int t = i / cols, n = i % cols;
       const float sa = FUSED ? scale[t] : p.sa[t];
-      const int64_t col = n0 + turn + n;
+      const int64_t col = int64_t(turn) + n;
       rows::store1(p.C + (int64_t(t) * p.ldc + col) * es, float(part[t][n]) * (sa * p.sb[col]),
                    p.c_dtype);
       part[t][n] = 0;
