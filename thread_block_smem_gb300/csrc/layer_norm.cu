@@ -2,10 +2,14 @@
 //     mean = sum x / N,  var = sum (x - mean)^2 / N,  rstd = 1 / sqrt(var + eps)
 //     y = (x - mean) rstd w + b
 // All in fp32, y rounded once.  The variance is taken of differences from a mean, not
-// as a difference of sums, so a row far from zero loses nothing: each warp takes the
-// mean of its part of the row and the squares around that, and the parts are joined by
+// as a difference of sums, so that of a row far from zero loses nothing: each warp takes
+// the mean of its part of the row and the squares around that, and the parts are joined by
 //     sum (x - mean)^2 = sum over the warps of  M2_w + n_w (mean_w - mean)^2
-// which needs one exchange between the warps instead of two.
+// which needs one exchange between the warps instead of two.  The mean itself is a sum of
+// fp32 additions, up to 4 units in its last place off (rows of up to 20000 values, measured),
+// and y as much times rstd w: up to 0.27 for constant rows of 500 to 2000 with an eps of
+// 1e-5, of which the rounding of a mean to fp32 alone may cost 0.04.  A mean corrected by
+// the sum of x - mean was exact there, and took 29.2 us instead of 25.9 for 8192 x 4096 bf16.
 //
 // Bound: memory, x read and y written once.  A row stays in registers: the threads of a
 // CTA (a warp where rows have 512 values or less) hold NC chunks of eight values each,

@@ -288,7 +288,8 @@ def grad_norm(grads, *, stream=None):
 
 def clip_grad_norm(grads, max_norm, eps=1e-6, *, out=None, stream=None):
     """Multiplies all gradients by min(1, max_norm / (norm + eps)) in place, or writes
-    the products to the tensors of ``out`` (the same shapes; fp16, bf16 or fp32 each),
+    the products to the tensors of ``out`` (the same shapes, and the same strides where
+    the gradients' own are not contiguous; fp16, bf16 or fp32 each),
     and returns the norm they had, a scalar fp32 tensor on the device, without waiting
     for it.  ``grads`` as in ``grad_norm``; no result may lie over another tensor.  A NaN
     among the gradients makes all of them NaN; an infinity makes the finite ones zero."""
