@@ -120,13 +120,6 @@ def _matrix(q, scales, what):
     return at, ld, scales.data_ptr(), m, k
 
 
-def _ranges_meet(a, rows_a, ld_a, cols_a, b, rows_b, ld_b, cols_b):
-    """Whether the memory from a's first value to its last and b's have a byte in common."""
-    a0, b0 = a.data_ptr(), b.data_ptr()
-    return (a0 < b0 + ((rows_b - 1) * ld_b + cols_b) * b.element_size() and
-            b0 < a0 + ((rows_a - 1) * ld_a + cols_a) * a.element_size())
-
-
 def quantize_int8(x, *, stream=None):
     """(q, scales) of x (M x K; fp16, bf16 or fp32, contiguous rows), a scale for
     each row.  For a row with largest magnitude amax: ac = max(amax, 2^-96),
@@ -205,12 +198,15 @@ def linear_int8(x, qw, sw, *, out=None, out_dtype=None, stream=None):
     rc = _lin._L.swz_linear_int8_workspace_size(M, N, K, need)
     if rc == 0:
         need = need.value
-        if need == 0 and out is not None and M and _ranges_meet(x, M, ldx, K, out, M, ldy, N):
-            need = 256 + M * ((K + 15) // 16 * 16)  # x is quantised before out is written
         ws = _lin._empty(need, _lin.torch.uint8, x, stream) if need else None
-        rc = _lin._L.swz_linear_int8(x.data_ptr(), code, ldx, pw, ldw, psw, y.data_ptr(), ldy, ycode,
-                                     M, N, K, ws.data_ptr() if need else None, need,
+        call = (x.data_ptr(), code, ldx, pw, ldw, psw, y.data_ptr(), ldy, ycode, M, N, K)
+        rc = _lin._L.swz_linear_int8(*call, ws.data_ptr() if need else None, need,
                                      _lin._handle(stream, x))
+        if rc == _swz.SWZ_EINVAL and need == 0 and out is not None:
+            # out lies over x, which is then quantised before out is written
+            need = 256 + M * ((K + 15) // 16 * 16)
+            ws = _lin._empty(need, _lin.torch.uint8, x, stream)
+            rc = _lin._L.swz_linear_int8(*call, ws.data_ptr(), need, _lin._handle(stream, x))
     if rc:
         raise _swz.SwzError(rc, "swz_linear_int8")
     return _lin._result("linear_int8", y, out, x, qw, sw)
