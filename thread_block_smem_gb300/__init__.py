@@ -346,6 +346,8 @@ def _written(*tensors):
 def _stream(stream):
     import torch
     if stream is None:
+        if torch.cuda.is_initialized():  # (a stream object costs as much as the launch)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
