@@ -696,7 +696,8 @@ int swz_linear_int8_workspace_size(int M, int N, int K, uint64_t* h_bytes);
  * weight and bias: N values each, NULL for 1 and 0 (their types are then not
  * used).  mean and rstd (M values each) are written for the gradient.  y may be x
  * itself where types and rows are the same; otherwise it must not lie over x, weight
- * or bias (SWZ_EINVAL).
+ * or bias (SWZ_EINVAL).  Squares of x - mean are fp32: rows that spread over 1e19 or
+ * more have the rstd 0.
  * M = 0 or N = 0: no-op.  Errors: SWZ_EINVAL, SWZ_EARCH, SWZ_ECUDA.
  */
 int swz_layer_norm(const void* x, int dtype, int64_t ldx, const void* weight, int w_dtype,
